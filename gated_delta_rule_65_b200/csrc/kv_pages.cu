@@ -1,0 +1,424 @@
+// kv_pages.cu -- bookkeeping of the paged key-value cache on the device (sm_100a): reserving pages for new tokens,
+// forking (and reordering and releasing) sequences, compacting the pool, and the page copies these need.
+//
+// A cache: pools k_pages, v_pages [num_pages, Hk, page_size, d]; table [R, P], entry (r, j) the page of tokens
+// j page_size ... of sequence r (anything outside [0, num_pages) means none); lens [R]; ref [num_pages], how many
+// entries name a page (plus what the caller adds to pin one); a page with ref <= 0 is free. Pages are handed out
+// lowest number first, to the entries in (r, j) order, so every call has one possible result.
+//
+// The bookkeeping moves 8 (R P + num_pages) bytes or so, a microsecond of HBM time at most; its cost is the few
+// dependent passes (count, rank, assign). It runs as one kernel on one cluster of up to 8 CTAs whose barriers separate
+// the passes: a kernel for each pass would pay a launch for each, a single CTA the loads of one SM. Every warp owns a
+// contiguous strip of the items (pages, entries or sequences) and counts by ballots, so a rank is the sum of the
+// strips before (a scan over at most 256 numbers) plus a population count. Integer atomics only, whose order does
+// not show. The copies follow in a kernel over the whole GPU, one warp for each 4 KB of a page's rows of one head.
+#include <cooperative_groups.h>
+
+#include "attn.h"
+#include "common.cuh"
+#include "kernels.h"
+
+namespace gdr2 {
+namespace {
+
+namespace cg = cooperative_groups;
+
+constexpr int kThreads = 1024;
+constexpr int kMaxCluster = 8;
+constexpr int kMaxWarps = kMaxCluster * kThreads / 32;
+
+// Workspace, ints: strip totals of two counts, the copies' count, then lists.
+struct Lists {
+    int *ta, *tb;    // [kMaxWarps] strip totals
+    int *ncopy;      // [4]
+    int *pages;      // [num_pages] free pages by rank (compact: the free ones below the live count)
+    int *high;       // [num_pages] compact: live pages at or above the live count, by rank
+    int *rank;       // [num_pages] compact: rank of such a page
+    int *owner;      // [R] fork: who keeps a sequence's partly filled page
+    int *src, *dst, *rows;  // [R] fork: copies
+};
+
+Lists lists(void *ws, int R, int num_pages) {
+    Lists w;
+    int *p = static_cast<int *>(ws);
+    auto take = [&](size_t n) {
+        int *x = p;
+        p += (n + 3) / 4 * 4;
+        return x;
+    };
+    w.ta = take(kMaxWarps), w.tb = take(kMaxWarps), w.ncopy = take(4);
+    w.pages = take(num_pages), w.high = take(num_pages), w.rank = take(num_pages);
+    w.owner = take(R), w.src = take(R), w.dst = take(R), w.rows = take(R);
+    return w;
+}
+
+// A warp's strip of n items: [first, last), whole multiples of 32 long.
+struct Strip {
+    long long first, last;
+};
+__device__ __forceinline__ Strip strip(long long n, int warp, int warps) {
+    const long long len = ((n + warps - 1) / warps + 31) / 32 * 32;
+    Strip s;
+    s.first = min(n, len * warp);
+    s.last = min(n, s.first + len);
+    return s;
+}
+
+// Sum of t[0 .. warp) and of all t; every warp on its own. t was written before the cluster's last barrier.
+__device__ __forceinline__ void before(const int *t, int warp, int warps, int lane, int &pre, int &total) {
+    int a = 0, b = 0;
+    for (int i = lane; i < warps; i += 32) {
+        const int v = __ldcg(t + i);
+        b += v;
+        if (i < warp) a += v;
+    }
+    pre = __reduce_add_sync(0xffffffffu, a);
+    total = __reduce_add_sync(0xffffffffu, b);
+}
+
+__device__ __forceinline__ int entry(const int *table, long long at, int num_pages) {
+    const int e = __ldcg(table + at);
+    return e >= 0 && e < num_pages ? e : -1;
+}
+
+// The number of free pages in a strip, and the free pages of rank < most listed by rank.
+__device__ __forceinline__ int count_free(const int *ref, Strip s, int lane) {
+    int c = 0;
+    for (long long b = s.first; b < s.last; b += 32) {
+        const long long i = b + lane;
+        c += __popc(__ballot_sync(0xffffffffu, i < s.last && __ldcg(ref + i) <= 0));
+    }
+    return c;
+}
+__device__ __forceinline__ void list_free(const int *ref, Strip s, int rank, int most, int *out, int lane) {
+    for (long long b = s.first; b < s.last && rank < most; b += 32) {
+        const long long i = b + lane;
+        const bool is = i < s.last && __ldcg(ref + i) <= 0;
+        const unsigned m = __ballot_sync(0xffffffffu, is);
+        const int at = rank + __popc(m & ((1u << lane) - 1));
+        if (is && at < most) out[at] = (int)i;
+        rank += __popc(m);
+    }
+}
+
+struct Place {
+    int gid, threads, warp, warps, lane;
+};
+__device__ __forceinline__ Place place() {
+    Place t;
+    t.gid = blockIdx.x * kThreads + threadIdx.x;
+    t.threads = gridDim.x * kThreads;
+    t.warp = t.gid >> 5, t.warps = t.threads >> 5, t.lane = threadIdx.x & 31;
+    return t;
+}
+
+// Pages for want[r] tokens of every sequence that holds lens[r]: entries from the one of token lens[r] to the one of
+// token want[r] - 1 that are empty get a page. Before that, pages wholly behind the window of the token at lens[r]
+// are released. The grid is one cluster.
+__global__ void __launch_bounds__(kThreads) kv_reserve_kernel(KvPagesArgs a, Lists w) {
+    cg::cluster_group cl = cg::this_cluster();
+    const Place t = place();
+    const long long E = (long long)a.R * a.P;
+    const int ps = a.page_size;
+    for (int i = t.gid; i < a.num_pages; i += t.threads) a.ref_out[i] = __ldcg(a.ref + i);
+    if (t.gid == 0) *a.count_out = 0;
+    cl.sync();
+    // entries: released, and counted where a page is needed
+    const Strip es = strip(E, t.warp, t.warps), pg = strip(a.num_pages, t.warp, t.warps);
+    auto needs = [&](int r, int j, int e) {
+        if (e >= 0) return false;
+        const int len = max(a.lens[r], 0), want = a.want[r];
+        return j >= len / ps && want > 0 && j < (want - 1) / ps + 1;
+    };
+    int c = 0;
+    for (long long b = es.first; b < es.last; b += 32) {
+        const long long i = b + t.lane;
+        bool need = false;
+        if (i < es.last) {
+            const int r = (int)(i / a.P), j = (int)(i - (long long)r * a.P);
+            int e = entry(a.table, i, a.num_pages);
+            if (e >= 0 && a.window > 0 && (long long)(j + 1) * ps + a.window <= (long long)max(a.lens[r], 0) + 1) {
+                atomicSub(a.ref_out + e, 1);
+                e = -1;
+            }
+            a.table_out[i] = e;
+            need = needs(r, j, e);
+        }
+        c += __popc(__ballot_sync(0xffffffffu, need));
+    }
+    if (t.lane == 0) w.ta[t.warp] = c;
+    int over = 0;  // pages past the table's end
+    for (int r = t.gid; r < a.R; r += t.threads) {
+        const int want = a.want[r];
+        if (want > 0) over += max(0, (want - 1) / ps + 1 - a.P);
+    }
+    over = __reduce_add_sync(0xffffffffu, over);
+    if (t.lane == 0 && over) atomicAdd(a.count_out, over);
+    cl.sync();
+    c = count_free(a.ref_out, pg, t.lane);
+    if (t.lane == 0) w.tb[t.warp] = c;
+    cl.sync();
+    int need0, needed, free0, nfree;
+    before(w.ta, t.warp, t.warps, t.lane, need0, needed);
+    before(w.tb, t.warp, t.warps, t.lane, free0, nfree);
+    list_free(a.ref_out, pg, free0, needed, w.pages, t.lane);
+    cl.sync();
+    if (w.ta[t.warp] > 0) {
+        for (long long b = es.first; b < es.last; b += 32) {
+            const long long i = b + t.lane;
+            bool need = false;
+            if (i < es.last) {
+                const int r = (int)(i / a.P);
+                need = needs(r, (int)(i - (long long)r * a.P), __ldcg(a.table_out + i));
+            }
+            const unsigned m = __ballot_sync(0xffffffffu, need);
+            const int rank = need0 + __popc(m & ((1u << t.lane) - 1));
+            if (need && rank < nfree) {
+                const int page = __ldcg(w.pages + rank);
+                a.table_out[i] = page;
+                a.ref_out[page] = 1;
+            }
+            need0 += __popc(m);
+        }
+    }
+    if (t.gid == 0 && needed > nfree) atomicAdd(a.count_out, needed - nfree);
+}
+
+// Every sequence r takes over the content of sequence parent[r] as it was before the call (r itself: stays; outside
+// [0, R): released). Full pages are shared. The partly filled last page stays with one taker, the parent itself if it
+// is one, else the first; every other taker gets a copy of its tokens on a fresh page. The grid is one cluster.
+__global__ void __launch_bounds__(kThreads) kv_fork_kernel(KvPagesArgs a, Lists w) {
+    cg::cluster_group cl = cg::this_cluster();
+    const Place t = place();
+    const long long E = (long long)a.R * a.P;
+    const int ps = a.page_size;
+    cudaTriggerProgrammaticLaunchCompletion();
+    for (int i = t.gid; i < a.num_pages; i += t.threads) a.ref_out[i] = __ldcg(a.ref + i);
+    for (int r = t.gid; r < a.R; r += t.threads) w.owner[r] = a.R;
+    if (t.gid == 0) *a.count_out = 0;
+    cl.sync();
+    for (int r = t.gid; r < a.R; r += t.threads) {
+        const int p = a.parent[r];
+        if (p >= 0 && p < a.R) atomicMin(w.owner + p, r == p ? -1 : r);
+    }
+    cl.sync();
+    auto length = [&](int p) { return (int)min((long long)max(a.lens[p], 0), (long long)a.P * ps); };
+    auto owns = [&](int r, int p) { return __ldcg(w.owner + p) == (r == p ? -1 : r); };
+    const Strip es = strip(E, t.warp, t.warps), pg = strip(a.num_pages, t.warp, t.warps), rs = strip(a.R, t.warp, t.warps);
+    for (long long i = es.first + t.lane; i < es.last; i += 32) {
+        const int r = (int)(i / a.P), j = (int)(i - (long long)r * a.P), p = a.parent[r];
+        const int was = entry(a.table, i, a.num_pages);
+        int e = -1;
+        if (p == r) {
+            e = was;
+        } else {
+            if (p >= 0 && p < a.R && (owns(r, p) || j < length(p) / ps)) e = entry(a.table, (long long)p * a.P + j, a.num_pages);
+            if (was >= 0) atomicSub(a.ref_out + was, 1);
+            if (e >= 0) atomicAdd(a.ref_out + e, 1);
+        }
+        a.table_out[i] = e;
+        if (j == 0) a.lens_out[r] = p >= 0 && p < a.R ? length(p) : 0;
+    }
+    // sequences that need a copy; source of the copy, or -1
+    auto source = [&](long long r) {
+        if (r >= rs.last) return -1;
+        const int p = a.parent[r];
+        if (p < 0 || p >= a.R || owns((int)r, p)) return -1;
+        const int len = length(p);
+        return len % ps ? entry(a.table, (long long)p * a.P + len / ps, a.num_pages) : -1;
+    };
+    int c = 0;
+    for (long long b = rs.first; b < rs.last; b += 32) c += __popc(__ballot_sync(0xffffffffu, source(b + t.lane) >= 0));
+    if (t.lane == 0) w.ta[t.warp] = c;
+    cl.sync();
+    c = count_free(a.ref_out, pg, t.lane);
+    if (t.lane == 0) w.tb[t.warp] = c;
+    cl.sync();
+    int need0, needed, free0, nfree;
+    before(w.ta, t.warp, t.warps, t.lane, need0, needed);
+    before(w.tb, t.warp, t.warps, t.lane, free0, nfree);
+    list_free(a.ref_out, pg, free0, needed, w.pages, t.lane);
+    cl.sync();
+    for (long long b = rs.first; b < rs.last; b += 32) {
+        const int r = (int)b + t.lane, src = source(r);
+        const unsigned m = __ballot_sync(0xffffffffu, src >= 0);
+        const int rank = need0 + __popc(m & ((1u << t.lane) - 1));
+        if (src >= 0) {
+            const int len = length(a.parent[r]), j = len / ps;
+            if (rank < nfree) {
+                const int page = __ldcg(w.pages + rank);
+                a.table_out[(long long)r * a.P + j] = page;
+                a.ref_out[page] = 1;
+                w.src[rank] = src, w.dst[rank] = page, w.rows[rank] = len - j * ps;
+            } else {
+                a.lens_out[r] = j * ps;
+            }
+        }
+        need0 += __popc(m);
+    }
+    if (t.gid == 0) {
+        w.ncopy[0] = min(needed, nfree);
+        if (needed > nfree) *a.count_out = needed - nfree;
+    }
+}
+
+// Live pages numbered live or above move to the free numbers below, in order; table and counts follow.
+__global__ void __launch_bounds__(kThreads) kv_compact_kernel(KvPagesArgs a, Lists w) {
+    cg::cluster_group cl = cg::this_cluster();
+    const Place t = place();
+    const long long E = (long long)a.R * a.P;
+    cudaTriggerProgrammaticLaunchCompletion();
+    const Strip pg = strip(a.num_pages, t.warp, t.warps);
+    const int nf = count_free(a.ref, pg, t.lane);
+    if (t.lane == 0) w.ta[t.warp] = (int)(pg.last - pg.first) - nf;
+    cl.sync();
+    int live0, live;  // live pages before this strip, and in all
+    before(w.ta, t.warp, t.warps, t.lane, live0, live);
+    // live pages below number `live`: those of the strips before the one that holds it, and of its first part
+    const long long len = ((a.num_pages + t.warps - 1) / t.warps + 31) / 32 * 32;
+    const int mid = (int)(live / len);
+    int below, all;
+    before(w.ta, mid, t.warps, t.lane, below, all);
+    for (long long b = mid * len; b < live; b += 32) {
+        const long long i = b + t.lane;
+        below += __popc(__ballot_sync(0xffffffffu, i < live && __ldcg(a.ref + i) > 0));
+    }
+    const int moves = live - below;  // as many live above as free below
+    for (long long b = pg.first; b < pg.last; b += 32) {
+        const long long i = b + t.lane;
+        const int n = i < pg.last ? __ldcg(a.ref + i) : 0;
+        const bool is = n > 0;
+        const unsigned m = __ballot_sync(0xffffffffu, is);
+        const int lb = live0 + __popc(m & ((1u << t.lane) - 1));  // live pages before i
+        if (i < pg.last) {
+            if (i < live) {
+                if (is)
+                    a.ref_out[i] = n;
+                else
+                    w.pages[i - lb] = (int)i;
+            } else {
+                w.rank[i] = is ? lb - below : -1;
+                if (is)
+                    w.high[lb - below] = (int)i;
+                else
+                    a.ref_out[i] = 0;
+            }
+        }
+        live0 += __popc(m);
+    }
+    cl.sync();
+    for (int k = t.gid; k < moves; k += t.threads) {
+        const int src = __ldcg(w.high + k), dst = __ldcg(w.pages + k);
+        const int n = __ldcg(a.ref + src);
+        a.ref_out[dst] = n;
+        a.ref_out[src] = 0;
+    }
+    for (long long i = t.gid; i < E; i += t.threads) {
+        int e = entry(a.table, i, a.num_pages);
+        if (e >= live) {
+            const int k = __ldcg(w.rank + e);
+            if (k >= 0) e = __ldcg(w.pages + k);
+        }
+        a.table_out[i] = e;
+    }
+    if (t.gid == 0) {
+        w.ncopy[0] = moves;
+        *a.count_out = live;
+    }
+}
+
+// Copies the first rows[i] (null: all) token rows of every head of page src[i] to page dst[i], in both pools. A warp
+// moves up to 4 KB of one head's rows, eight 16-byte loads a lane in flight.
+__global__ void __launch_bounds__(256) kv_copy_kernel(const int *ncopy, const int *src, const int *dst, const int *rows,
+                                                      uint8_t *k, uint8_t *v, int Hk, int page_size, int row_bytes) {
+    cudaGridDependencySynchronize();
+    constexpr int kPiece = 4096;
+    const int lane = threadIdx.x & 31;
+    const long long block = (long long)page_size * row_bytes;
+    const int pieces = (int)((block + kPiece - 1) / kPiece);
+    const long long items = (long long)__ldcg(ncopy) * Hk * 2 * pieces;
+    for (long long x = (long long)blockIdx.x * 8 + (threadIdx.x >> 5); x < items; x += (long long)gridDim.x * 8) {
+        const int piece = (int)(x % pieces);
+        const long long y = x / pieces;
+        const int hh = (int)(y % (2 * Hk)), i = (int)(y / (2 * Hk)), h = hh >> 1;
+        const long long bytes = rows ? (long long)__ldcg(rows + i) * row_bytes : block;
+        uint8_t *pool = hh & 1 ? v : k;
+        const uint8_t *s = pool + ((long long)__ldcg(src + i) * Hk + h) * block;
+        uint8_t *d = pool + ((long long)__ldcg(dst + i) * Hk + h) * block;
+        const long long base = (long long)piece * kPiece + lane * 16;
+        uint4 r[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+            if (base + u * 512 < bytes) r[u] = __ldcs(reinterpret_cast<const uint4 *>(s + base + u * 512));
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+            if (base + u * 512 < bytes) *reinterpret_cast<uint4 *>(d + base + u * 512) = r[u];
+    }
+}
+
+// CTAs of the cluster: one while each of its threads has a few items, the largest portable cluster above that.
+int cluster_size(const KvPagesArgs &a) {
+    const long long items = (long long)a.R * a.P + a.num_pages;
+    int c = 1;
+    while (c < kMaxCluster && items > 4LL * c * kThreads) c *= 2;
+    return c;
+}
+
+cudaError_t launch_cluster(void (*kernel)(KvPagesArgs, Lists), const KvPagesArgs &a, const Lists &w, cudaStream_t st) {
+    cudaLaunchConfig_t cfg{};
+    const int c = cluster_size(a);
+    cfg.gridDim = dim3(c);
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = st;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = c;
+    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, a, w);
+}
+
+cudaError_t launch_copy(const KvPagesArgs &a, const Lists &w, const int *src, const int *dst, const int *rows, long long most,
+                        cudaStream_t st) {
+    const int row_bytes = a.d * (a.dtype == 1 ? 2 : 4);
+    const long long pieces = ((long long)a.page_size * row_bytes + 4095) / 4096;
+    const long long want = (most * a.Hk * 2 * pieces + 7) / 8, full = 8LL * kAttnSms;
+    const int grid = (int)(want < full ? want : full);
+    cudaError_t e;
+    GDR2_LAUNCH("kv_copy", st,
+                e = launch_dependent(kv_copy_kernel, dim3(grid), dim3(256), 0, st, (const int *)w.ncopy, src, dst, rows,
+                                     (uint8_t *)a.k_pages, (uint8_t *)a.v_pages, a.Hk, a.page_size, row_bytes));
+    return e;
+}
+
+}  // namespace
+
+size_t kv_workspace_bytes(int R, int num_pages) {
+    const size_t n = ((size_t)num_pages + 3) / 4 * 4, r = ((size_t)R + 3) / 4 * 4;
+    return (2 * (size_t)kMaxWarps + 4 + 3 * n + 4 * r) * sizeof(int);
+}
+
+cudaError_t launch_kv_reserve(const KvPagesArgs &a, cudaStream_t st) {
+    cudaError_t e;
+    GDR2_LAUNCH("kv_reserve", st, e = launch_cluster(kv_reserve_kernel, a, lists(a.workspace, a.R, a.num_pages), st));
+    return e;
+}
+
+cudaError_t launch_kv_fork(const KvPagesArgs &a, cudaStream_t st) {
+    const Lists w = lists(a.workspace, a.R, a.num_pages);
+    cudaError_t e;
+    GDR2_LAUNCH("kv_fork", st, e = launch_cluster(kv_fork_kernel, a, w, st));
+    if (e != cudaSuccess) return e;
+    return launch_copy(a, w, w.src, w.dst, w.rows, a.R, st);
+}
+
+cudaError_t launch_kv_compact(const KvPagesArgs &a, cudaStream_t st) {
+    const Lists w = lists(a.workspace, a.R, a.num_pages);
+    cudaError_t e;
+    GDR2_LAUNCH("kv_compact", st, e = launch_cluster(kv_compact_kernel, a, w, st));
+    if (e != cudaSuccess) return e;
+    return launch_copy(a, w, w.high, w.pages, nullptr, (a.num_pages + 1) / 2, st);
+}
+
+}  // namespace gdr2

@@ -25,12 +25,18 @@ EXPORTED = ("gdr2_version", "gdr2_status_string", "gdr2_check", "gdr2_workspace_
             "gdr2_gate_prologue_bwd", "gdr2_workspace_bytes_gva", "gdr2_chunk_fwd_gva", "gdr2_chunk_fwd_train_gva",
             "gdr2_chunk_bwd_gva", "gdr2_chunk_bwd_saved_gva", "gdr2_workspace_bytes_varlen_gva",
             "gdr2_chunk_fwd_varlen_gva", "gdr2_chunk_fwd_train_varlen_gva", "gdr2_chunk_bwd_varlen_gva",
-            "gdr2_chunk_bwd_saved_varlen_gva", "gdr2_set_chunk_path", "gdr2_get_chunk_path")
+            "gdr2_chunk_bwd_saved_varlen_gva", "gdr2_set_chunk_path", "gdr2_get_chunk_path", "gdr2_rope_freqs",
+            "gdr2_attn_prologue_fwd", "gdr2_attn_prologue_workspace_bytes", "gdr2_attn_prologue_bwd",
+            "gdr2_attn_prologue_cache", "gdr2_attn_decode_workspace_bytes", "gdr2_attn_decode",
+            "gdr2_kv_workspace_bytes", "gdr2_kv_reserve", "gdr2_kv_fork", "gdr2_kv_compact")
 
 _lib = None
 _lock = threading.Lock()
 _VP = ctypes.c_void_p
 _I = ctypes.c_int
+_LL = ctypes.c_longlong
+_F = ctypes.c_float
+_D = ctypes.c_double
 
 
 class GDR2Error(RuntimeError):
@@ -108,6 +114,31 @@ def lib(build_if_missing: bool = True) -> ctypes.CDLL:
             L.gdr2_decode_step.argtypes = [_VP] * 8 + [_I] * 5 + [_VP]
             L.gdr2_chunk_fwd_noalloc.restype = _I
             L.gdr2_chunk_fwd_noalloc.argtypes = [_VP] * 9 + [_I] * 6 + [_VP]
+            L.gdr2_rope_freqs.restype = _I
+            L.gdr2_rope_freqs.argtypes = [_VP, _VP, _I, _D, _I, _D, _D, _D, _D]
+            L.gdr2_attn_prologue_fwd.restype = _I
+            L.gdr2_attn_prologue_fwd.argtypes = ([_VP] * 4 + [_I, _F, _VP, _VP, _F, _I, _I, _VP, _VP] + [_I] * 5 +
+                                                 [_LL] * 2 + [_VP])
+            L.gdr2_attn_prologue_workspace_bytes.restype = ctypes.c_size_t
+            L.gdr2_attn_prologue_workspace_bytes.argtypes = [_I]
+            L.gdr2_attn_prologue_bwd.restype = _I
+            L.gdr2_attn_prologue_bwd.argtypes = ([_VP] * 4 + [_I, _F, _VP, _VP, _F, _I, _I] + [_VP] * 6 + [_I] * 5 +
+                                                 [_LL] * 4 + [_VP, ctypes.c_size_t, _VP])
+            L.gdr2_attn_prologue_cache.restype = _I
+            L.gdr2_attn_prologue_cache.argtypes = ([_VP] * 5 + [_I, _F, _VP, _VP, _VP, _F, _I, _I] + [_VP] * 4 +
+                                                   [_I] * 9 + [_LL] * 3 + [_VP])
+            L.gdr2_attn_decode_workspace_bytes.restype = ctypes.c_size_t
+            L.gdr2_attn_decode_workspace_bytes.argtypes = [_I]
+            L.gdr2_attn_decode.restype = _I
+            L.gdr2_attn_decode.argtypes = ([_VP] * 6 + [_F, _I, _VP, _VP] + [_I] * 9 + [_VP, ctypes.c_size_t, _VP])
+            L.gdr2_kv_workspace_bytes.restype = ctypes.c_size_t
+            L.gdr2_kv_workspace_bytes.argtypes = [_I] * 2
+            L.gdr2_kv_reserve.restype = _I
+            L.gdr2_kv_reserve.argtypes = [_VP] * 7 + [_I] * 5 + [_VP, ctypes.c_size_t, _VP]
+            L.gdr2_kv_fork.restype = _I
+            L.gdr2_kv_fork.argtypes = [_VP] * 10 + [_I] * 7 + [_VP, ctypes.c_size_t, _VP]
+            L.gdr2_kv_compact.restype = _I
+            L.gdr2_kv_compact.argtypes = [_VP] * 7 + [_I] * 7 + [_VP, ctypes.c_size_t, _VP]
             L.gdr2_profile_enable.restype = _I
             L.gdr2_profile_enable.argtypes = [_I]
             L.gdr2_profile_collect.restype = _I
@@ -450,6 +481,330 @@ def decode_step(q, k, v, log_alpha, b, w, state, o=None, *, stream=None):
                                 B, H, dk, dv, _dtype_code(q), _stream(stream))
     _check("gdr2_decode_step", st)
     return o
+
+
+# ---- the attention half of the hybrid cell: query / key prologue, paged cache, attention of one new token ----
+
+ROPE_PLAIN, ROPE_LINEAR, ROPE_BASE, ROPE_PARTS = range(4)
+_ROPE = {"none": ROPE_PLAIN, "linear": ROPE_LINEAR, "base": ROPE_BASE, "parts": ROPE_PARTS}
+
+
+def _shaped(name, t, shape, dtype):
+    """`t` contiguous, of this shape and dtype (its device is looked at where its pointer is taken)."""
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"gdr2: {name} has shape {tuple(t.shape)}, not {tuple(shape)}")
+    if t.dtype != dtype:
+        raise TypeError(f"gdr2: {name} is {t.dtype}, not {dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"gdr2: {name} must be contiguous")
+    return t
+
+
+def _token_rows(name, x, dtype=None):
+    """Token rows [T, H, d] or [B, T, H, d] with contiguous heads and channels and one stride from token to token
+    (a view of a fused projection may have a larger one): (tokens, heads, channels, stride in elements)."""
+    if x.dim() not in (3, 4):
+        raise ValueError(f"gdr2: {name} must be [T, H, d] or [B, T, H, d]")
+    if dtype is not None and x.dtype != dtype:
+        raise TypeError(f"gdr2: {name} is {x.dtype}, not {dtype}")
+    H, d = x.shape[-2], x.shape[-1]
+    T = x.numel() // (H * d) if H * d else 0
+    if T == 0:
+        raise ValueError(f"gdr2: {name} is empty")
+    if (d > 1 and x.stride(-1) != 1) or (H > 1 and x.stride(-2) != d):
+        raise ValueError(f"gdr2: heads and channels of {name} must be contiguous")
+    n = x.shape[-3]
+    if n > 1:
+        stride = x.stride(-3)
+        if x.dim() == 4 and x.shape[0] > 1 and x.stride(0) != n * stride:
+            raise ValueError(f"gdr2: the tokens of {name} must have one stride across the batch")
+    elif T > 1:
+        stride = x.stride(0)
+    else:
+        stride = H * d
+    return T, H, d, stride
+
+
+def _device(*tensors):
+    """Every tensor on the current CUDA device, which is where the library launches."""
+    dev = tensors[0].device
+    if dev.type != "cuda":
+        raise ValueError("gdr2: tensors must live on a CUDA device")
+    for t in tensors:
+        if t is not None and t.device != dev:
+            raise ValueError(f"gdr2: tensors on different devices ({dev} and {t.device})")
+    if dev.index != torch.cuda.current_device():
+        raise ValueError(f"gdr2: tensors on {dev}, which is not the current CUDA device")
+    return dev
+
+
+def _p(t):
+    return None if t is None else t.data_ptr()
+
+
+def _scratch(n, dev, stream):
+    """Workspace of one call; with an explicit stream it is kept until that stream has passed the call."""
+    return _kept(torch.empty(n, dtype=torch.uint8, device=dev), stream)
+
+
+def _kept(t, stream):
+    if stream is not None:
+        t.record_stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream)))
+    return t
+
+
+def _raw_stream(stream):
+    if stream is None:
+        return torch.cuda.current_stream().cuda_stream
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _workspace(workspace, need, dev, stream):
+    if workspace is None:
+        workspace = _scratch(need, dev, stream)
+    elif workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError("gdr2: the workspace must be contiguous and on the tensors' device")
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def rope_freqs(rot, base=10000.0, *, scaling="none", factor=1.0, orig_len=0, turns_low=1.0, turns_high=32.0,
+               device="cuda"):
+    """gdr2_rope_freqs: (freqs, mag), the radians per position of the rot / 2 rotated pairs (float64 tensor on
+    `device`) and the magnitude for the prologue's `mag`. scaling: "none", "linear", "base" or "parts"."""
+    if scaling not in _ROPE:
+        raise ValueError(f"gdr2: unknown scaling {scaling!r}; use one of {sorted(_ROPE)}")
+    buf = (_D * max(1, int(rot) // 2))()
+    mag = _D(1.0)
+    _check("gdr2_rope_freqs", lib().gdr2_rope_freqs(buf, ctypes.byref(mag), int(rot), float(base), _ROPE[scaling],
+                                                    float(factor), float(orig_len), float(turns_low),
+                                                    float(turns_high)))
+    return torch.tensor(list(buf), dtype=torch.float64, device=device), float(mag.value)
+
+
+def _gains(gq, gk, norm, d):
+    if not norm and (gq is not None or gk is not None):
+        raise ValueError("gdr2: gq and gk are gains of the norm; pass None without it")
+    for name, g in (("gq", gq), ("gk", gk)):
+        if g is not None:
+            _shaped(name, g, (d,), torch.float32)
+
+
+def _rope_args(pos, freqs, T, d):
+    """(tokens' positions, frequencies, rot)"""
+    if freqs is None:
+        return 0
+    if freqs.dtype != torch.float64 or freqs.dim() != 1 or not freqs.is_contiguous():
+        raise TypeError("gdr2: freqs must be a contiguous 1-D float64 tensor")
+    if pos is None or pos.dtype != torch.int32 or pos.numel() != T or not pos.is_contiguous():
+        raise ValueError("gdr2: pos must hold one int32 position for each token")
+    return 2 * freqs.numel()
+
+
+def _prologue_checks(xq, xk, gq, gk, pos, freqs, norm):
+    T, Hq, d, sq = _token_rows("xq", xq)
+    Tk, Hk, dk, sk = _token_rows("xk", xk, xq.dtype)
+    if Tk != T or dk != d:
+        raise ValueError("gdr2: xq and xk must have the same tokens and channels")
+    dt = _dtype_code(xq)
+    _gains(gq, gk, norm, d)
+    return T, Hq, Hk, d, sq, sk, dt, _rope_args(pos, freqs, T, d)
+
+
+def attn_prologue_fwd(xq, xk, gq=None, gk=None, pos=None, freqs=None, *, norm=True, eps=1e-6, mag=1.0,
+                      interleaved=False, out=None, stream=None):
+    """gdr2_attn_prologue_fwd: per-head RMS norm (unless norm=False) with gains gq, gk [d] fp32 (None: ones) and
+    rotary positions of xq [.., T, Hq, d] and xk [.., T, Hk, d] (views of a fused projection allowed), pos int32 for
+    each token and freqs float64 (rope_freqs; None: no rotation). Returns a dict q, k (contiguous)."""
+    T, Hq, Hk, d, sq, sk, dt, rot = _prologue_checks(xq, xk, gq, gk, pos, freqs, norm)
+    dev = _device(xq, xk, gq, gk, pos, freqs)
+    if out is None:
+        out = {"q": torch.empty(xq.shape, dtype=xq.dtype, device=dev),
+               "k": torch.empty(xk.shape, dtype=xq.dtype, device=dev)}
+        _kept(out["q"], stream), _kept(out["k"], stream)
+    else:
+        _shaped("q", out["q"], xq.shape, xq.dtype), _shaped("k", out["k"], xk.shape, xq.dtype)
+        _device(xq, out["q"], out["k"])
+    st = lib().gdr2_attn_prologue_fwd(_p(xq), _p(xk), _p(gq), _p(gk), int(norm), eps, _p(pos), _p(freqs), mag, rot,
+                                      int(interleaved), _p(out["q"]), _p(out["k"]), T, Hq, Hk, d, dt, sq, sk,
+                                      _raw_stream(stream))
+    _check("gdr2_attn_prologue_fwd", st)
+    return out
+
+
+def attn_prologue_bwd(xq, xk, gq, gk, pos, freqs, dq, dk, *, norm=True, eps=1e-6, mag=1.0, interleaved=False,
+                      out=None, workspace=None, stream=None):
+    """gdr2_attn_prologue_bwd: returns a dict dxq, dxk and, with the norm, dgq, dgk [d] fp32 (written for gains of
+    None too, as the gradient of a gain of ones). `out` may hold dxq, dxk as views of one fused gradient, and may
+    leave dgq, dgk out or None when they are not wanted."""
+    T, Hq, Hk, d, sq, sk, dt, rot = _prologue_checks(xq, xk, gq, gk, pos, freqs, norm)
+    _shaped("dq", dq, xq.shape, xq.dtype), _shaped("dk", dk, xk.shape, xq.dtype)
+    dev = _device(xq, xk, gq, gk, pos, freqs, dq, dk)
+    if out is None:
+        out = {"dxq": torch.empty(xq.shape, dtype=xq.dtype, device=dev),
+               "dxk": torch.empty(xk.shape, dtype=xq.dtype, device=dev)}
+        if norm:
+            out["dgq"] = torch.empty(d, dtype=torch.float32, device=dev)
+            out["dgk"] = torch.empty(d, dtype=torch.float32, device=dev)
+        for t in out.values():
+            _kept(t, stream)
+    dgq, dgk = out.get("dgq"), out.get("dgk")
+    Tq, hq, eq, sdq = _token_rows("dxq", out["dxq"], xq.dtype)
+    Tk, hk, ek, sdk = _token_rows("dxk", out["dxk"], xq.dtype)
+    if (Tq, hq, eq) != (T, Hq, d) or (Tk, hk, ek) != (T, Hk, d):
+        raise ValueError("gdr2: dxq and dxk must have the shapes of xq and xk")
+    for name, g in (("dgq", dgq), ("dgk", dgk)):
+        if g is not None:
+            _shaped(name, g, (d,), torch.float32)
+    _device(xq, out["dxq"], out["dxk"], dgq, dgk)
+    nbytes = 0
+    if dgq is not None or dgk is not None:
+        workspace, nbytes = _workspace(workspace, max(16, int(lib().gdr2_attn_prologue_workspace_bytes(d))), dev, stream)
+    st = lib().gdr2_attn_prologue_bwd(_p(xq), _p(xk), _p(gq), _p(gk), int(norm), eps, _p(pos), _p(freqs), mag, rot,
+                                      int(interleaved), _p(dq), _p(dk), _p(out["dxq"]), _p(out["dxk"]), _p(dgq),
+                                      _p(dgk), T, Hq, Hk, d, dt, sq, sk, sdq, sdk, _p(workspace), nbytes,
+                                      _raw_stream(stream))
+    _check("gdr2_attn_prologue_bwd", st)
+    return out
+
+
+def _pools(k_pages, v_pages):
+    if k_pages.dim() != 4:
+        raise ValueError("gdr2: k_pages must be [num_pages, Hk, page_size, d]")
+    _shaped("k_pages", k_pages, k_pages.shape, k_pages.dtype)
+    _shaped("v_pages", v_pages, k_pages.shape, k_pages.dtype)
+    return k_pages.shape
+
+
+def _table(table):
+    if table.dim() != 2:
+        raise ValueError("gdr2: table must be [R, P]")
+    _shaped("table", table, table.shape, torch.int32)
+    return table.shape
+
+
+def attn_prologue_cache(xq, xk, xv, gq, gk, seq, pos, freqs, k_pages, v_pages, table, *, norm=True, eps=1e-6,
+                        mag=1.0, interleaved=False, q=None, stream=None):
+    """gdr2_attn_prologue_cache: the prologue for new tokens xq [T, Hq, d], xk, xv [T, Hk, d]; token t is token
+    pos[t] of sequence seq[t] (int32; outside [0, R): padding). Keys and values go to the pools k_pages, v_pages
+    [num_pages, Hk, page_size, d] by table int32 [R, P]; q is returned (padding rows as they were)."""
+    T, Hq, Hk, d, sq, sk, dt, rot = _prologue_checks(xq, xk, gq, gk, pos, freqs, norm)
+    Tv, Hv, dv, sv = _token_rows("xv", xv, xq.dtype)
+    num, Hp, ps, dp = _pools(k_pages, v_pages)
+    R, P = _table(table)
+    if (Tv, Hv, dv) != (T, Hk, d) or (Hp, dp) != (Hk, d) or k_pages.dtype != xq.dtype:
+        raise ValueError("gdr2: xk, xv and the pools must agree in heads, channels and dtype")
+    if pos is None:
+        raise ValueError("gdr2: pos is needed to find a token's page")
+    _shaped("seq", seq, (T,), torch.int32), _shaped("pos", pos.view(-1), (T,), torch.int32)
+    dev = _device(xq, xk, xv, gq, gk, seq, pos, freqs, k_pages, v_pages, table, q)
+    if q is None:
+        q = _kept(torch.empty(xq.shape, dtype=xq.dtype, device=dev), stream)
+    else:
+        _shaped("q", q, xq.shape, xq.dtype)
+    st = lib().gdr2_attn_prologue_cache(_p(xq), _p(xk), _p(xv), _p(gq), _p(gk), int(norm), eps, _p(seq), _p(pos),
+                                        _p(freqs), mag, rot, int(interleaved), _p(q), _p(k_pages), _p(v_pages),
+                                        _p(table), T, Hq, Hk, d, R, P, ps, num, dt, sq, sk, sv, _raw_stream(stream))
+    _check("gdr2_attn_prologue_cache", st)
+    return q
+
+
+def attn_decode(q, k_pages, v_pages, table, lens, seq=None, *, scale=None, window=0, want_lse=False, o=None,
+                lse=None, workspace=None, stream=None):
+    """gdr2_attn_decode: attention of one new token for each row of q [N, Hq, d] over sequence seq[n] (int32 [N];
+    None: n) of the cache, its last `window` tokens (0: all), lens int32 [R] with the new token counted. scale: by
+    default d^-1/2. Returns o [N, Hq, d], or (o, lse fp32 [N, Hq]) with want_lse or a given lse."""
+    if q.dim() != 3:
+        raise ValueError("gdr2: q must be [N, Hq, d]")
+    N, Hq, d = _shaped("q", q, q.shape, q.dtype).shape
+    num, Hk, ps, dp = _pools(k_pages, v_pages)
+    R, P = _table(table)
+    if dp != d or k_pages.dtype != q.dtype:
+        raise ValueError("gdr2: q and the pools must agree in channels and dtype")
+    _shaped("lens", lens, (R,), torch.int32)
+    if seq is not None:
+        _shaped("seq", seq, (N,), torch.int32)
+    dt = _dtype_code(q)
+    dev = _device(q, k_pages, v_pages, table, lens, seq, o, lse)
+    if o is None:
+        o = _kept(torch.empty_like(q), stream)
+    else:
+        _shaped("o", o, q.shape, q.dtype)
+    if lse is not None:
+        _shaped("lse", lse, (N, Hq), torch.float32)
+    elif want_lse:
+        lse = _kept(torch.empty((N, Hq), dtype=torch.float32, device=dev), stream)
+    L = lib()
+    workspace, nbytes = _workspace(workspace, max(16, int(L.gdr2_attn_decode_workspace_bytes(d))), dev, stream)
+    st = L.gdr2_attn_decode(_p(q), _p(k_pages), _p(v_pages), _p(table), _p(lens), _p(seq),
+                            d ** -0.5 if scale is None else scale, window, _p(o), _p(lse), N, Hq, Hk, d, R, P, ps,
+                            num, dt, _p(workspace), nbytes, _raw_stream(stream))
+    _check("gdr2_attn_decode", st)
+    return o if lse is None else (o, lse)
+
+
+def _kv_outs(names, given, likes, dev, stream):
+    """The bookkeeping outputs, given in `out` or fresh."""
+    got = []
+    for name, (shape, like) in zip(names, likes):
+        t = None if given is None else given.get(name)
+        if t is None:
+            t = _kept(torch.empty(shape, dtype=torch.int32, device=dev), stream)
+        else:
+            _shaped(name, t, shape, torch.int32)
+            _device(like, t)
+        got.append(t)
+    return got
+
+
+def kv_reserve(table, lens, want, ref, *, page_size, window=0, out=None, workspace=None, stream=None):
+    """gdr2_kv_reserve: pages for tokens [lens[r], want[r]) of every sequence (pages behind the window released
+    first). Returns (table, ref, missing int32 [1]) after the call; `out` may name them (also the inputs)."""
+    R, P = _table(table)
+    _shaped("lens", lens, (R,), torch.int32), _shaped("want", want, (R,), torch.int32)
+    num = _shaped("ref", ref, (ref.numel(),), torch.int32).numel()
+    dev = _device(table, lens, want, ref)
+    t, r, m = _kv_outs(("table", "ref", "missing"), out, (((R, P), table), ((num,), ref), ((1,), ref)), dev, stream)
+    L = lib()
+    workspace, nbytes = _workspace(workspace, max(16, int(L.gdr2_kv_workspace_bytes(R, num))), dev, stream)
+    st = L.gdr2_kv_reserve(_p(table), _p(lens), _p(want), _p(ref), _p(t), _p(r), _p(m), R, P, page_size, num, window,
+                           _p(workspace), nbytes, _raw_stream(stream))
+    _check("gdr2_kv_reserve", st)
+    return t, r, m
+
+
+def kv_fork(table, lens, ref, parent, k_pages, v_pages, *, out=None, workspace=None, stream=None):
+    """gdr2_kv_fork: sequence r takes over the content of sequence parent[r] (int32 [R]; r: stays, outside [0, R):
+    released). Partly filled last pages are copied in the pools. Returns (table, lens, ref, missing int32 [1])."""
+    R, P = _table(table)
+    num, Hk, ps, d = _pools(k_pages, v_pages)
+    _shaped("lens", lens, (R,), torch.int32), _shaped("parent", parent, (R,), torch.int32)
+    _shaped("ref", ref, (num,), torch.int32)
+    dt = _dtype_code(k_pages)
+    dev = _device(table, lens, ref, parent, k_pages, v_pages)
+    t, n, r, m = _kv_outs(("table", "lens", "ref", "missing"), out,
+                          (((R, P), table), ((R,), lens), ((num,), ref), ((1,), ref)), dev, stream)
+    L = lib()
+    workspace, nbytes = _workspace(workspace, max(16, int(L.gdr2_kv_workspace_bytes(R, num))), dev, stream)
+    st = L.gdr2_kv_fork(_p(table), _p(lens), _p(ref), _p(parent), _p(t), _p(n), _p(r), _p(m), _p(k_pages),
+                        _p(v_pages), R, P, Hk, ps, d, num, dt, _p(workspace), nbytes, _raw_stream(stream))
+    _check("gdr2_kv_fork", st)
+    return t, n, r, m
+
+
+def kv_compact(table, ref, k_pages, v_pages, *, out=None, workspace=None, stream=None):
+    """gdr2_kv_compact: the live pages moved to [0, live). Returns (table, ref, live int32 [1])."""
+    R, P = _table(table)
+    num, Hk, ps, d = _pools(k_pages, v_pages)
+    _shaped("ref", ref, (num,), torch.int32)
+    dt = _dtype_code(k_pages)
+    dev = _device(table, ref, k_pages, v_pages)
+    t, r, m = _kv_outs(("table", "ref", "live"), out, (((R, P), table), ((num,), ref), ((1,), ref)), dev, stream)
+    L = lib()
+    workspace, nbytes = _workspace(workspace, max(16, int(L.gdr2_kv_workspace_bytes(R, num))), dev, stream)
+    st = L.gdr2_kv_compact(_p(table), _p(ref), _p(t), _p(r), _p(m), _p(k_pages), _p(v_pages), R, P, Hk, ps, d, num,
+                           dt, _p(workspace), nbytes, _raw_stream(stream))
+    _check("gdr2_kv_compact", st)
+    return t, r, m
 
 
 def profile_enable(on: bool = True) -> None:

@@ -369,6 +369,140 @@ GDR2_API int gdr2_decode_step(const void *q, const void *k, const void *v, const
                      int B, int H, int dk, int dv, int dtype, void *stream);
 
 /*
+ * The attention half of the hybrid cell ("Gated DeltaNet-2", review page, hybrid design: the mixer alternates
+ * with sliding-window softmax attention). Training and prefill take the query / key prologue; serving takes the
+ * prologue that writes into a paged key-value cache, the attention of one new token over that cache, and the
+ * cache's bookkeeping. The conventions at the top of this file hold, except that arrays of ints, the gains gq
+ * and gk, dgq, dgk and lse need the alignment of their own type only.
+ *
+ * Sizes: d in {64, 128}; any Hq, Hk >= 1 (attention: Hq a multiple of Hk, query head j reads KV head
+ * j / (Hq / Hk)); any page_size >= 1 with P * page_size below 2^31 - 65536.
+ */
+
+/*
+ * Frequencies of the rotary positions, in radians per position and 64 bits, written to HOST memory: freqs [rot / 2]
+ * and, unless NULL, the magnitude mag of the rotated channels. Pair i turns by base^(-2 i / rot) a position;
+ *   GDR2_ROPE_PLAIN   as it is;
+ *   GDR2_ROPE_LINEAR  divided by factor (positions interpolated);
+ *   GDR2_ROPE_BASE    with base * factor^(rot / (rot - 2)) for base (the slowest pair slows by factor, the first
+ *                     keeps its pace; rot > 2);
+ *   GDR2_ROPE_PARTS   pairs that make fewer than turns_low turns over the original context of orig_len positions
+ *                     divided by factor, those with more than turns_high kept, a linear ramp in the number of
+ *                     turns between; mag = 0.1 ln(factor) + 1.
+ * rot even, base > 0, factor >= 1, 0 <= turns_low < turns_high; arguments a scaling does not use are ignored.
+ */
+enum { GDR2_ROPE_PLAIN = 0, GDR2_ROPE_LINEAR = 1, GDR2_ROPE_BASE = 2, GDR2_ROPE_PARTS = 3 };
+GDR2_API int gdr2_rope_freqs(double *freqs, double *mag, int rot, double base, int scaling, double factor,
+                             double orig_len, double turns_low, double turns_high);
+
+/*
+ * Query / key prologue of the attention layer. Per (token t, head), x the d channels of the projection:
+ *     u = x / sqrt(mean(x^2) + eps) (.) g          (norm = 1; g = gq for queries, gk for keys, NULL = ones)
+ *     u = x                                         (norm = 0; gq and gk have to be NULL)
+ *     the first rot channels of u turned pairwise by pos[t] * freqs[i], i < rot / 2, and multiplied by mag; pair i
+ *     is (i, i + rot / 2), or (2 i, 2 i + 1) when interleaved != 0; the other channels pass unchanged.
+ *   xq [T, Hq, d], xk [T, Hk, d] dtype   heads and channels contiguous, xq_stride / xk_stride elements from token to
+ *                  token (multiples of 16 bytes; larger than H d for views of a fused projection). Batches are
+ *                  flattened: T = B * sequence length.
+ *   gq, gk [d] fp32   pos int32 [T] (any sign)   freqs fp64 [rot / 2], DEVICE memory; both may be NULL when rot = 0
+ *   q [T, Hq, d], k [T, Hk, d] dtype (written, contiguous)
+ * rot is a multiple of 16 of at most d. Angles are formed in 64 bits, norms and sums in fp32.
+ * gdr2_attn_prologue_bwd takes the same inputs and dq, dk (contiguous, dtype) and writes dxq, dxk (with their own
+ * token strides, so that they can be views of one gradient of a fused projection) and, unless NULL, dgq, dgk [d]
+ * fp32: sums over every token and head, in a fixed order. Its workspace of
+ * gdr2_attn_prologue_workspace_bytes(d) bytes is needed with dgq or dgk only.
+ */
+GDR2_API int gdr2_attn_prologue_fwd(const void *xq, const void *xk, const float *gq, const float *gk, int norm,
+                                    float eps, const int *pos, const double *freqs, float mag, int rot,
+                                    int interleaved, void *q, void *k, int T, int Hq, int Hk, int d, int dtype,
+                                    long long xq_stride, long long xk_stride, void *stream);
+
+GDR2_API size_t gdr2_attn_prologue_workspace_bytes(int d);
+
+GDR2_API int gdr2_attn_prologue_bwd(const void *xq, const void *xk, const float *gq, const float *gk, int norm,
+                                    float eps, const int *pos, const double *freqs, float mag, int rot,
+                                    int interleaved, const void *dq, const void *dk, void *dxq, void *dxk, float *dgq,
+                                    float *dgk, int T, int Hq, int Hk, int d, int dtype, long long xq_stride,
+                                    long long xk_stride, long long dxq_stride, long long dxk_stride, void *workspace,
+                                    size_t workspace_bytes, void *stream);
+
+/*
+ * The paged key-value cache: pools k_pages, v_pages [num_pages, Hk, page_size, d] dtype and a page table
+ * int32 [R, P] in device memory. Entry (r, j) is the page that holds tokens [j page_size, (j + 1) page_size) of
+ * sequence r; any value outside [0, num_pages) means that there is none.
+ *
+ * gdr2_attn_prologue_cache is the prologue for T new tokens of any of the cache's sequences (one each for a decode
+ * step, whole prompts packed for a prefill): q is written as by gdr2_attn_prologue_fwd, the finished key and the value
+ * row xv[t] go to the cache. Token t is token pos[t] of sequence seq[t].
+ *   seq, pos int32 [T]     xv [T, Hk, d] dtype, xv_stride elements from token to token
+ * A token whose seq is outside [0, R) is padding: nothing of it is written, its q row included. A token whose page is
+ * not there (or whose pos is outside the table) gets its q row only. Two tokens for one place leave either's row.
+ */
+GDR2_API int gdr2_attn_prologue_cache(const void *xq, const void *xk, const void *xv, const float *gq, const float *gk,
+                                      int norm, float eps, const int *seq, const int *pos, const double *freqs,
+                                      float mag, int rot, int interleaved, void *q, void *k_pages, void *v_pages,
+                                      const int *table, int T, int Hq, int Hk, int d, int R, int P, int page_size,
+                                      int num_pages, int dtype, long long xq_stride, long long xk_stride,
+                                      long long xv_stride, void *stream);
+
+/*
+ * Attention of one new token for each of N slots over the cache. Slot n reads sequence seq[n] (seq NULL: n, with
+ * N <= R), tokens [max(0, len - window), len) with len = lens[seq[n]] (the new token included; held to
+ * [0, P page_size]) and window = 0 for all of them; tokens whose page is not there are left out:
+ *     s_i = scale q_j . k_i,   o_j = sum_i exp(s_i) v_i / sum_i exp(s_i),   lse_j = ln sum_i exp(s_i)
+ *   q, o [N, Hq, d] dtype     lens int32 [R]     lse fp32 [N, Hq], or NULL when not wanted
+ * With no token left o = 0 and lse = -inf. A slot whose seq is outside [0, R) is padding: its rows of o and lse are
+ * left as they were. What lies in the pools outside the tokens read (NaN included) has no effect. Statistics and sums
+ * are fp32; a finite v is assumed. Repeated calls give identical bits. The lengths are read on the stream, so a
+ * captured call stays valid as sequences grow.
+ */
+GDR2_API size_t gdr2_attn_decode_workspace_bytes(int d);
+
+GDR2_API int gdr2_attn_decode(const void *q, const void *k_pages, const void *v_pages, const int *table,
+                              const int *lens, const int *seq, float scale, int window, void *o, float *lse, int N,
+                              int Hq, int Hk, int d, int R, int P, int page_size, int num_pages, int dtype,
+                              void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Page bookkeeping, on the device and without the host's knowledge of any length. ref int32 [num_pages] counts the
+ * table entries that name a page (a caller may add to it to pin one); a page with ref <= 0 is free. Free pages are
+ * handed out lowest number first to entries in (r, j) order, so each call has exactly one result. Each call reads
+ * table, lens and ref and writes the state after it to table_out, lens_out, ref_out; the workspace is
+ * gdr2_kv_workspace_bytes(R, num_pages) bytes.
+ *
+ * gdr2_kv_reserve: pages for tokens [lens[r], want[r]) of every sequence: the entries from the one of token lens[r]
+ * to the one of token want[r] - 1 that have no page get one (want[r] <= lens[r] asks for none). With window > 0 the
+ * pages that lie wholly behind the window of the token at lens[r] are released first. missing (int32 [1]): how many
+ * pages were asked for and not found, past the table's end included; their entries stay empty. table_out may be
+ * table and ref_out may be ref.
+ *
+ * gdr2_kv_fork: every sequence r takes over the content that sequence parent[r] had before the call: r itself (it
+ * stays as it is), another one (a fork or a reordering), or, outside [0, R), none (its pages are released, its length
+ * is 0). Full pages are shared. The last, partly filled page of a parent stays with one taker, together with pages
+ * reserved beyond it: with the parent if it stays, else with the lowest r; every other taker gets the tokens of that
+ * page copied to a fresh one (the rest of the fresh page is left as it was). missing: how many copies found no page;
+ * those sequences end at their last full page. table_out and lens_out must not be table and lens; ref_out may be ref.
+ *
+ * gdr2_kv_compact: the live pages end up in [0, live): those numbered live or above move, in order, to the free numbers
+ * below. table_out and ref_out follow, live (int32 [1]) is written. table_out may be table and ref_out may be ref.
+ * An entry that names a free page keeps its number.
+ */
+GDR2_API size_t gdr2_kv_workspace_bytes(int R, int num_pages);
+
+GDR2_API int gdr2_kv_reserve(const int *table, const int *lens, const int *want, const int *ref, int *table_out,
+                             int *ref_out, int *missing, int R, int P, int page_size, int num_pages, int window,
+                             void *workspace, size_t workspace_bytes, void *stream);
+
+GDR2_API int gdr2_kv_fork(const int *table, const int *lens, const int *ref, const int *parent, int *table_out,
+                          int *lens_out, int *ref_out, int *missing, void *k_pages, void *v_pages, int R, int P,
+                          int Hk, int page_size, int d, int num_pages, int dtype, void *workspace,
+                          size_t workspace_bytes, void *stream);
+
+GDR2_API int gdr2_kv_compact(const int *table, const int *ref, int *table_out, int *ref_out, int *live, void *k_pages,
+                             void *v_pages, int R, int P, int Hk, int page_size, int d, int num_pages, int dtype,
+                             void *workspace, size_t workspace_bytes, void *stream);
+
+/*
  * gdr2_chunk_fwd for callers that cannot allocate device memory. The paper has no counterpart to
  * this entry point: it exists for callers that only receive input and output buffers -- plugins in a
  * host framework that owns all device memory through its own pool, or latency-critical loops where a
