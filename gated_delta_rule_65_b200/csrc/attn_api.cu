@@ -42,8 +42,16 @@ int check_prologue(int T, int Hq, int Hk, int d, int dtype, int norm, const floa
 
 int check_pages(int R, int P, int page_size, int num_pages) {
     if (R <= 0 || P <= 0 || page_size <= 0 || num_pages <= 0) return GDR2_ERR_INVALID_ARG;
-    if ((long long)P * page_size > 0x7fff0000LL) return GDR2_ERR_UNSUPPORTED;  // token numbers are 32-bit
+    // token numbers and places in the table are 32-bit
+    if ((long long)P * page_size > 0x7fff0000LL || (long long)R * P > 0x7fff0000LL || num_pages > 0x7fff0000)
+        return GDR2_ERR_UNSUPPORTED;
     return GDR2_OK;
+}
+
+// The copies of kv_fork and kv_compact count 4 KB pieces of a page's heads in 32 bits.
+bool copies_fit(int Hk, int page_size, int d, int num_pages, int dtype) {
+    const long long pieces = ((long long)page_size * d * (dtype == GDR2_BF16 ? 2 : 4) + 4095) / 4096;
+    return pieces < (1LL << 31) && pieces * 2 * Hk < (1LL << 31) && pieces * 2 * Hk * num_pages < 0xffff0000LL;
 }
 
 int done(cudaError_t e) { return e == cudaSuccess ? GDR2_OK : GDR2_ERR_CUDA; }
@@ -190,6 +198,7 @@ int gdr2_kv_fork(const int *table, const int *lens, const int *ref, const int *p
                  int num_pages, int dtype, void *workspace, size_t workspace_bytes, void *stream) {
     int st = check_heads(Hk, Hk, d, dtype);
     if (st == GDR2_OK) st = check_pages(R, P, page_size, num_pages);
+    if (st == GDR2_OK && !copies_fit(Hk, page_size, d, num_pages, dtype)) st = GDR2_ERR_UNSUPPORTED;
     if (st != GDR2_OK) return st;
     if (!ok_num(table) || !ok_num(lens) || !ok_num(ref) || !ok_num(parent) || !ok_num(table_out) || !ok_num(lens_out) ||
         !ok_num(ref_out) || !ok_num(missing) || !ok_ptr(k_pages) || !ok_ptr(v_pages) || table_out == table ||
@@ -210,6 +219,7 @@ int gdr2_kv_compact(const int *table, const int *ref, int *table_out, int *ref_o
                     void *workspace, size_t workspace_bytes, void *stream) {
     int st = check_heads(Hk, Hk, d, dtype);
     if (st == GDR2_OK) st = check_pages(R, P, page_size, num_pages);
+    if (st == GDR2_OK && !copies_fit(Hk, page_size, d, num_pages, dtype)) st = GDR2_ERR_UNSUPPORTED;
     if (st != GDR2_OK) return st;
     if (!ok_num(table) || !ok_num(ref) || !ok_num(table_out) || !ok_num(ref_out) || !ok_num(live) || !ok_ptr(k_pages) ||
         !ok_ptr(v_pages))

@@ -13,11 +13,13 @@
 // formed in fp64 in units of turns, its whole turns are dropped there, and the rest (exact to 2^-24 of a turn) goes
 // to sincospif.
 //
-// Both directions are bound by HBM: 2 (forward) or 3 (backward) rows of d elements moved per (token, head), about 50
-// fp32 operations per lane and row. A lane holds 8 consecutive channels of a row (16 bytes of bf16), d / 8 lanes make
-// a row, and a group of d / 8 lanes keeps ONE token and walks its heads: cos and sin stay in registers for all of
-// them (read per row from shared memory they cost 16 wavefronts per two rows, more than a third of the time that the
-// rows' bytes take). The angles of a CTA's tokens are formed once by all its threads.
+// Bound: HBM moves 2 (forward) or 3 (backward) rows of d elements per (token, head); next to it stands the issue of
+// instructions. So a lane holds two 16-byte chunks of a row, in the half layout the two that are rotated into one
+// another: the rotation needs no exchange between lanes, a warp takes four bf16 rows of 128 channels at once, and all
+// arithmetic runs on pairs of floats. A warp keeps ONE token and walks its heads, so the coefficients (gain, cosine and
+// sine folded together) stay in registers for all of them and the token's angles are formed once, two a lane. Every
+// lane feeds itself: cp.async into shared memory that only it reads, several rows deep and running on into the next
+// token, so that nothing but a warp's own exchange of angles ever waits.
 #include "attn.h"
 #include "attn_vec.cuh"
 #include "common.cuh"
@@ -26,65 +28,125 @@
 namespace gdr2 {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kMaxTok = 16;                  // tokens of a CTA at a time
-constexpr int kBwdCtas = 2 * kAttnSms;       // CTAs of the backward (a partial sum of dg each)
+constexpr int kThreads = 256, kWarps = kThreads / 32;
+// CTAs on an SM and rows of a lane in flight, measured on the training batch (B = 8, T = 4096, 16 + 16 heads of 128
+// channels, bf16). Forward, 2 CTAs: 90 us with 8 rows, 91 with 5; 3 CTAs: 118 to 130 us with 4 to 8 rows (spills, and
+// more warps on more tokens scatter the requests). Backward, 2 CTAs: 173 us fetching row by row (4 rows ahead), 140 in
+// bursts of 2 and 145 of 3; 1 CTA: 149 row by row, 151 to 160 in bursts of 2 to 6.
+constexpr int kFwdCtas = 2, kFwdDepth = 8;
+constexpr int kBwdCtas = 2, kBwdBurst = 2, kBwdDepth = 2 * kBwdBurst;
+constexpr int kBwdGrid = kBwdCtas * kAttnSms;  // CTAs of the backward (a partial sum of dgq or dgk each)
 
-// cos and sin of the CTA's tokens t0 .. t0 + tb - 1, scaled by mag.
-template <int D>
-__device__ __forceinline__ void make_angles(const AttnPrologueArgs &p, int t0, int tb, float (*sc)[D / 2],
-                                            float (*ss)[D / 2]) {
-    const int half = p.rot / 2;
-    for (int x = threadIdx.x; x < tb * half; x += kThreads) {
-        const int tok = x / half, i = x - tok * half;
-        if (t0 + tok >= p.T) break;
-        const double turns = (double)p.pos[t0 + tok] * (p.freqs[i] * 0.15915494309189533577);
-        float s, c;
-        sincospif(2.f * (float)(turns - rint(turns)), &s, &c);
-        sc[tok][i] = p.mag * c;
-        ss[tok][i] = p.mag * s;
-    }
-}
-
-// What a lane multiplies its 8 channels and their partners with: y = c x + s partner(x).
-struct Turn {
-    float c[8], s[8];
-    int partner;  // lane of the row (half layout)
-    bool on;      // the lane's channels are rotated
+// How lanes hold a row: kLanes lanes of two chunks each, kRows rows in a warp.
+template <int D, typename T> struct Layout {
+    static constexpr int kElems = Chunk<T>::kElems, kPairs = Chunk<T>::kPairs;
+    static constexpr int kLanes = D / (2 * kElems), kRows = 32 / kLanes;
 };
 
-template <int D, bool kInter>
-__device__ __forceinline__ void load_turn(const AttnPrologueArgs &p, int l, const float *sc, const float *ss, Turn &t) {
-    t.on = 8 * l < p.rot;
-    t.partner = l;
-    if (!t.on) return;
-    if constexpr (kInter) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            t.c[e] = sc[4 * l + e / 2];
-            t.s[e] = (e & 1) ? ss[4 * l + e / 2] : -ss[4 * l + e / 2];
+// The two channels at which lane l's chunks start, and which of them are rotated. Half layout: lanes below
+// rot / (2 kElems) hold chunk l and the one rotated with it; the rest of the row is split in two runs, so that each
+// access of the lanes is contiguous.
+template <int D, typename T, bool kInter> struct Slot {
+    using Y = Layout<D, T>;
+    int at0, at1;
+    bool on0, on1;
+    __device__ __forceinline__ Slot(int l, int rot) {
+        if constexpr (kInter) {
+            at0 = l * Y::kElems, at1 = (l + Y::kLanes) * Y::kElems;
+            on0 = at0 < rot, on1 = at1 < rot;
+        } else {
+            const int hp = rot / (2 * Y::kElems);
+            on0 = on1 = l < hp;
+            at0 = (on0 ? l : l + hp) * Y::kElems;
+            at1 = (on0 ? l + hp : l + Y::kLanes) * Y::kElems;
         }
-    } else {
-        const int hl = p.rot / 16;  // lanes of a half
-        const bool low = l < hl;
-        const int i0 = 8 * (low ? l : l - hl);
-        t.partner = low ? l + hl : l - hl;
+    }
+};
+
+// Radians per position of the two pairs whose angles a lane forms, in turns.
+struct Freqs {
+    double f[2];
+    __device__ __forceinline__ void load(const AttnPrologueArgs &p, int lane) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            t.c[e] = sc[i0 + e];
-            t.s[e] = low ? -ss[i0 + e] : ss[i0 + e];
+        for (int i = 0; i < 2; ++i)
+            f[i] = lane + 32 * i < p.rot / 2 ? p.freqs[lane + 32 * i] * 0.15915494309189533577 : 0.0;
+    }
+    // cos and sin of the warp's token, scaled by mag: cs[0 .. D / 2) and cs[D / 2 .. D)
+    template <int D> __device__ __forceinline__ void angles(const AttnPrologueArgs &p, int pos, float *cs, int lane) const {
+        __syncwarp();  // the token before has been read
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int x = lane + 32 * i;
+            if (x < p.rot / 2) {
+                const double turns = (double)pos * f[i];
+                float s, c;
+                sincospif(2.f * (float)(turns - rint(turns)), &s, &c);
+                cs[x] = p.mag * c;
+                cs[D / 2 + x] = p.mag * s;
+            }
+        }
+        __syncwarp();
+    }
+};
+
+// 2 N consecutive floats of shared memory, 16-byte aligned.
+template <int N> __device__ __forceinline__ void load_pairs(const float *p, F2 (&w)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+        const float4 v = *reinterpret_cast<const float4 *>(p + 2 * i);
+        w[i] = f2(v.x, v.y), w[i + 1] = f2(v.z, v.w);
+    }
+}
+
+// A token's rotation as lane l applies it, y = c0 (.) x0 + s0 (.) partner(x0), likewise for chunk 1: the partner of
+// chunk 0 is chunk 1 (half layout) or chunk 0 with its pairs swapped (interleaved). Unrotated chunks have c = 1, s = 0.
+template <typename T> struct Turn {
+    F2 c0[Chunk<T>::kPairs], s0[Chunk<T>::kPairs], c1[Chunk<T>::kPairs], s1[Chunk<T>::kPairs];
+};
+
+template <int D, typename T, bool kInter>
+__device__ __forceinline__ void load_turn(const Slot<D, T, kInter> &w, const float *sc, const float *ss, Turn<T> &t) {
+    constexpr int N = Chunk<T>::kPairs;
+    const F2 one = f2(1.f, 1.f), zero = f2(0.f, 0.f);
+    if constexpr (kInter) {
+        auto both = [&](int at, bool on, F2(&c)[N], F2(&s)[N]) {
+#pragma unroll
+            for (int i = 0; i < N; i += 2) {
+                const float2 cc = *reinterpret_cast<const float2 *>(sc + at / 2 + i);
+                const float2 si = *reinterpret_cast<const float2 *>(ss + at / 2 + i);
+                c[i] = on ? f2(cc.x, cc.x) : one, c[i + 1] = on ? f2(cc.y, cc.y) : one;
+                s[i] = on ? f2(-si.x, si.x) : zero, s[i + 1] = on ? f2(-si.y, si.y) : zero;
+            }
+        };
+        both(w.at0, w.on0, t.c0, t.s0);
+        both(w.at1, w.on1, t.c1, t.s1);
+    } else {
+        const int a = w.on0 ? w.at0 : 0;
+        load_pairs(sc + a, t.c0);
+        load_pairs(ss + a, t.s1);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            if (!w.on0) t.c0[i] = one, t.s1[i] = zero;
+            t.c1[i] = t.c0[i];
+            t.s0[i] = neg(t.s1[i]);
         }
     }
 }
 
-// y = the rotation (kBack: its transpose) of x. Every lane of the warp takes part.
-template <int L, bool kInter, bool kBack>
-__device__ __forceinline__ void turn(const Turn &t, const float (&x)[8], float (&y)[8]) {
+// y = c (.) x + s (.) partner(x) for both chunks. An infinity in an unrotated channel must not reach another one as
+// 0 * inf: without a rotation the partner's place is taken by a zero (`all`: the whole row is rotated).
+template <typename T, bool kInter, int N>
+__device__ __forceinline__ void turn(const Turn<T> &t, bool on0, bool on1, bool all, const F2 (&x0)[N], const F2 (&x1)[N],
+                                     F2 (&y0)[N], F2 (&y1)[N]) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        const float o = kInter ? x[e ^ 1] : __shfl_sync(0xffffffffu, x[e], t.partner, L);
-        const float s = kBack ? -t.s[e] : t.s[e];
-        y[e] = t.on ? fmaf(x[e], t.c[e], o * s) : x[e];
+    for (int i = 0; i < N; ++i) {
+        F2 p0 = kInter ? swap(x0[i]) : x1[i], p1 = kInter ? swap(x1[i]) : x0[i];
+        if (!all) {
+            p0.v = on0 ? p0.v : 0;
+            p1.v = on1 ? p1.v : 0;
+        }
+        y0[i] = fma(t.c0[i], x0[i], mul(t.s0[i], p0));
+        y1[i] = fma(t.c1[i], x1[i], mul(t.s1[i], p1));
     }
 }
 
@@ -94,255 +156,415 @@ template <int L> __device__ __forceinline__ float sum_row(float v) {
     return v;
 }
 
-__device__ __forceinline__ void load_gain(const float *g, int l, float (&w)[8]) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) w[e] = g ? __ldg(g + 8 * l + e) : 1.f;
+// A row's gain in shared memory (ones where there is none).
+template <int D> __device__ __forceinline__ void stage_gain(const float *g, float *sg) {
+    for (int i = threadIdx.x; i < D; i += kThreads) sg[i] = g ? g[i] : 1.f;
 }
 
-// One token's H rows of x, heads h0, h0 + step, ... (this group's share), normed, rotated and stored at out + h hs.
-// Trip counts are the same for every group of the CTA: a group without a row left works on zeros and stores nothing.
-template <int D, typename T, bool kInter>
-__device__ __forceinline__ void fwd_rows(const AttnPrologueArgs &p, const T *x, const float *gain, T *out,
-                                         long long hs, int H, int h0, int step, bool live, int l, const Turn &t) {
-    constexpr int L = D / 8, U = 4;
-    float g[8];
-    load_gain(gain, l, g);
-    const int iters = (H + step - 1) / step;
-    for (int i0 = 0; i0 < iters; i0 += U) {
-        Vec8<T> raw[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int h = h0 + (i0 + u) * step;
-            if (live && h < H)
-                raw[u].load_stream(x + (size_t)h * D + 8 * l);
-            else
-                raw[u].zero();
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (i0 + u < iters) {
-                const int h = h0 + (i0 + u) * step;
-                float v[8], y[8];
-                raw[u].get(v);
-                if (p.norm) {
-                    float q = 0.f;
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) q = fmaf(v[e], v[e], q);
-                    const float n = rsqrtf(sum_row<L>(q) * (1.f / D) + p.eps);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) v[e] *= n * g[e];
-                }
-                turn<L, kInter, false>(t, v, y);
-                if (live && h < H) Vec8<T>::store(out + h * hs + 8 * l, y);
-            }
-        }
-    }
-}
+// The work of a warp: units u = warp, warp + warps, ... of (token, part), token u / parts; part k of a token takes the
+// heads k kRows + (the lane's row), + parts kRows, ... of each tensor.
+struct Units {
+    int parts, count, stride;
+};
 
-// tb: tokens of a CTA, a power of two of at most kMaxTok and at most the CTA's groups.
+__device__ __forceinline__ void cp16(void *dst, const void *src, bool on) {  // off: zeros, nothing is read
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src),
+                 "r"(on ? 16 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// ---- forward and cache form ----------------------------------------------------------------------------------
+
+template <int D> struct FwdShared {
+    uint4 ring[kFwdDepth][2][kThreads];
+    alignas(16) float gain[2][D];
+    alignas(16) float cs[kWarps][D];
+};
+
 template <int D, typename T, bool kInter, bool kCache>
-__global__ void __launch_bounds__(kThreads) attn_prologue_fwd_kernel(AttnPrologueArgs p, int tb) {
-    constexpr int L = D / 8, NG = kThreads / L;
-    __shared__ float sc[kMaxTok][D / 2], ss[kMaxTok][D / 2];
-    const int grp = threadIdx.x / L, l = threadIdx.x % L;
-    const int t0 = blockIdx.x * tb, step = NG / tb, tok = grp / step, h0 = grp % step;
-    make_angles<D>(p, t0, tb, sc, ss);
-    __syncthreads();
-    const int tt = t0 + tok;
-    bool live = tt < p.T;
-    int page = -1, off = 0;
+__global__ void __launch_bounds__(kThreads, kFwdCtas) attn_prologue_fwd_kernel(AttnPrologueArgs p, Units un) {
+    using Y = Layout<D, T>;
+    constexpr int N = Y::kPairs;
+    extern __shared__ __align__(16) uint8_t raw[];
+    FwdShared<D> &sh = *reinterpret_cast<FwdShared<D> *>(raw);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, grp = lane / Y::kLanes, l = lane % Y::kLanes;
+    const Slot<D, T, kInter> w(l, p.rot);
+    const int step = un.parts * Y::kRows;
+    const int tq = (p.Hq + step - 1) / step, tk = (p.Hk + step - 1) / step;
+    int u = blockIdx.x * kWarps + warp;
+
+    // the ring: what this lane fetches next is row `src` (head ha of ea) of tensor seg of unit ua, `left` rows of it
+    // remaining, its own the first of each step
+    int ua = u, seg = -1, left = 0, ha = 0, ea = 0;
+    const T *src = nullptr;
+    auto enter = [&]() {
+        const int tok = ua / un.parts;
+        ha = (ua - tok * un.parts) * Y::kRows + grp;
+        ++seg;
+        const T *x = static_cast<const T *>(seg == 0 ? p.xq : seg == 1 ? p.xk : p.xv);
+        src = x + (size_t)tok * (seg == 0 ? p.sxq : seg == 1 ? p.sxk : p.sxv) + (size_t)ha * D;
+        ea = seg == 0 ? p.Hq : p.Hk;
+        left = seg == 0 ? tq : tk;
+    };
+    if (ua < un.count) enter();
+    auto fetch = [&](int slot) {
+        if (ua < un.count) {
+            const bool on = ha < ea;
+            const T *x = on ? src : static_cast<const T *>(p.xq);
+            cp16(&sh.ring[slot][0][threadIdx.x], x + w.at0, on);
+            cp16(&sh.ring[slot][1][threadIdx.x], x + w.at1, on);
+            src += step * D, ha += step;
+            if (--left == 0) {
+                if (seg == (kCache ? 2 : 1)) seg = -1, ua += un.stride;
+                if (ua < un.count) enter();
+            }
+        }
+        cp_commit();
+    };
+#pragma unroll
+    for (int i = 0; i < kFwdDepth; ++i) fetch(i);
+    // the token of a unit, read one unit ahead (its sequence two)
+    auto token = [&](int v) { return v < un.count ? v / un.parts : 0; };
+    int pos = 0, seq = 0, page = -1, npos = 0, nseq = 0;
+    auto find_page = [&](int q, int s) {
+        if (s < 0 || s >= p.R || q < 0) return -1;
+        const int j = q / p.page_size;
+        return j < p.P ? __ldg(p.table + (size_t)s * p.P + j) : -1;
+    };
+    if (p.rot || kCache) {
+        pos = p.pos[token(u)];
+        npos = p.pos[token(u + un.stride)];
+    }
     if constexpr (kCache) {
-        const int s = live ? p.seq[tt] : -1;
-        live = s >= 0 && s < p.R;
-        if (live) {
-            const int pos = p.pos[tt], j = pos / p.page_size;
-            if (pos >= 0 && j < p.P) {
-                page = p.table[(size_t)s * p.P + j];
-                off = pos - j * p.page_size;
-                if (page >= p.num_pages) page = -1;
+        seq = p.seq[token(u)];
+        nseq = p.seq[token(u + un.stride)];
+        page = find_page(pos, seq);
+    }
+    Freqs fr;
+    fr.load(p, lane);
+    stage_gain<D>(p.gq, sh.gain[0]);
+    stage_gain<D>(p.gk, sh.gain[1]);
+    __syncthreads();
+    const bool all = p.rot == D;
+    int slot = 0;
+    for (; u < un.count; u += un.stride) {
+        const int tok = u / un.parts, h0 = (u - tok * un.parts) * Y::kRows + grp;
+        int fpos = 0, fseq = 0, npage = -1;
+        if (p.rot || kCache) fpos = p.pos[token(u + 2 * un.stride)];
+        if constexpr (kCache) {
+            fseq = p.seq[token(u + 2 * un.stride)];
+            npage = find_page(npos, nseq);
+        }
+        fr.angles<D>(p, pos, sh.cs[warp], lane);
+        const bool live = !kCache || (seq >= 0 && seq < p.R);
+        const bool put = !kCache || (live && page >= 0 && page < p.num_pages);
+        const long long hs = kCache ? (long long)p.page_size * D : D;  // from head to head where keys go
+        const size_t at = kCache ? (put ? ((size_t)page * p.Hk * p.page_size + pos % p.page_size) * D : 0) : (size_t)tok * p.Hk * D;
+#pragma unroll 1
+        for (int which = 0; which < 2; ++which) {
+            // u (.) g folded into the rotation: the partner's gain goes with its sine
+            Turn<T> t;
+            load_turn<D, T, kInter>(w, sh.cs[warp], sh.cs[warp] + D / 2, t);
+            F2 g0[N], g1[N];
+            load_pairs(sh.gain[which] + w.at0, g0);
+            load_pairs(sh.gain[which] + w.at1, g1);
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                t.c0[i] = mul(t.c0[i], g0[i]), t.c1[i] = mul(t.c1[i], g1[i]);
+                t.s0[i] = mul(t.s0[i], kInter ? swap(g0[i]) : g1[i]), t.s1[i] = mul(t.s1[i], kInter ? swap(g1[i]) : g0[i]);
+            }
+            const int H = (which ? put : live) ? (which ? p.Hk : p.Hq) : 0, trips = which ? tk : tq;  // H: heads to store
+            const long long os = which ? hs : D, inc = os * step;
+            T *out = (which == 0 ? static_cast<T *>(p.q) + (size_t)tok * p.Hq * D : static_cast<T *>(kCache ? p.k_pages : p.k) + at) +
+                     h0 * os;
+#pragma unroll 1
+            for (int i = 0, h = h0; i < trips; ++i, h += step, out += inc) {
+                cp_wait<kFwdDepth - 1>();
+                Chunk<T> a, b;
+                a.v = sh.ring[slot][0][threadIdx.x];
+                b.v = sh.ring[slot][1][threadIdx.x];
+                F2 x0[N], x1[N], y0[N], y1[N];
+                a.get(x0);
+                b.get(x1);
+                turn<T, kInter>(t, w.on0, w.on1, all, x0, x1, y0, y1);
+                if (p.norm) {
+                    F2 q = mul(x0[0], x0[0]);
+#pragma unroll
+                    for (int i = 1; i < N; ++i) q = fma(x0[i], x0[i], q);
+#pragma unroll
+                    for (int i = 0; i < N; ++i) q = fma(x1[i], x1[i], q);
+                    const float n = rsqrtf(sum_row<Y::kLanes>(sum2(q)) * (1.f / D) + p.eps);
+                    const F2 nn = f2(n, n);
+#pragma unroll
+                    for (int i = 0; i < N; ++i) y0[i] = mul(y0[i], nn), y1[i] = mul(y1[i], nn);
+                }
+                fetch(slot);
+                if (++slot == kFwdDepth) slot = 0;
+                if (h < H) {
+                    Chunk<T>::store(out + w.at0, y0);
+                    Chunk<T>::store(out + w.at1, y1);
+                }
             }
         }
-    }
-    Turn t;
-    load_turn<D, kInter>(p, l, sc[tok], ss[tok], t);
-    const size_t tr = live ? (size_t)tt : 0;
-    fwd_rows<D, T, kInter>(p, static_cast<const T *>(p.xq) + tr * p.sxq, p.gq,
-                           static_cast<T *>(p.q) + tr * p.Hq * D, D, p.Hq, h0, step, live, l, t);
-    if constexpr (!kCache) {
-        fwd_rows<D, T, kInter>(p, static_cast<const T *>(p.xk) + tr * p.sxk, p.gk,
-                               static_cast<T *>(p.k) + tr * p.Hk * D, D, p.Hk, h0, step, live, l, t);
-    } else {
-        const bool put = live && page >= 0;
-        const long long hs = (long long)p.page_size * D;
-        const size_t slot = put ? (size_t)page * p.Hk * hs + (size_t)off * D : 0;
-        fwd_rows<D, T, kInter>(p, static_cast<const T *>(p.xk) + tr * p.sxk, p.gk,
-                               static_cast<T *>(p.k_pages) + slot, hs, p.Hk, h0, step, put, l, t);
-        if (put) {
-            const T *v = static_cast<const T *>(p.xv) + tr * p.sxv + 8 * l;
-            T *dst = static_cast<T *>(p.v_pages) + slot + 8 * l;
-            for (int h = h0; h < p.Hk; h += step) {
-                Vec8<T> raw;
-                raw.load_stream(v + (size_t)h * D);
-                raw.put(dst + h * hs);
+        if constexpr (kCache) {
+            T *v = static_cast<T *>(p.v_pages) + at;
+#pragma unroll 1
+            for (int i = 0, h = h0; i < tk; ++i, h += step) {
+                cp_wait<kFwdDepth - 1>();
+                Chunk<T> a, b;
+                a.v = sh.ring[slot][0][threadIdx.x];
+                b.v = sh.ring[slot][1][threadIdx.x];
+                if (put && h < p.Hk) {
+                    a.put(v + h * hs + w.at0);
+                    b.put(v + h * hs + w.at1);
+                }
+                fetch(slot);
+                if (++slot == kFwdDepth) slot = 0;
             }
         }
+        pos = npos, npos = fpos;
+        seq = nseq, nseq = fseq;
+        page = npage;
     }
+    cp_wait<0>();
 }
 
+// ---- backward --------------------------------------------------------------------------------------------------
+
+template <int D> struct BwdShared {
+    uint4 ring[kBwdDepth][4][kThreads];
+    alignas(16) float gain[D];
+    alignas(16) float cs[kWarps][D];
+};
+
+// The first `cq` CTAs take the queries, the others the keys (one set of sums in a lane's registers), each warp a fixed
+// set of units: the sums over tokens have a fixed order.
 template <int D, typename T, bool kInter>
-__device__ __forceinline__ void bwd_rows(const AttnPrologueArgs &p, const T *x, const T *dy, const float *gain, T *dx,
-                                         int H, int h0, int step, bool live, int l, const Turn &t, float (&acc)[8]) {
-    constexpr int L = D / 8, U = sizeof(T) == 2 ? 4 : 2;
-    float g[8];
-    load_gain(gain, l, g);
-    const int iters = (H + step - 1) / step;
-    for (int i0 = 0; i0 < iters; i0 += U) {
-        Vec8<T> rx[U], rd[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int h = h0 + (i0 + u) * step;
-            if (live && h < H) {
-                rd[u].load_stream(dy + (size_t)h * D + 8 * l);
-                if (p.norm) rx[u].load_stream(x + (size_t)h * D + 8 * l);
-            } else {
-                rd[u].zero();
-                rx[u].zero();
+__global__ void __launch_bounds__(kThreads, kBwdCtas) attn_prologue_bwd_kernel(AttnPrologueArgs p, Units uq, Units uk, int cq,
+                                                                               float *__restrict__ partial) {
+    using Y = Layout<D, T>;
+    constexpr int N = Y::kPairs;
+    extern __shared__ __align__(16) uint8_t raw[];
+    BwdShared<D> &sh = *reinterpret_cast<BwdShared<D> *>(raw);
+    cudaTriggerProgrammaticLaunchCompletion();
+    const bool keys = blockIdx.x >= cq;
+    const Units un = keys ? uk : uq;
+    const T *x = static_cast<const T *>(keys ? p.xk : p.xq), *dy = static_cast<const T *>(keys ? p.dk : p.dq);
+    T *dx = static_cast<T *>(keys ? p.dxk : p.dxq);
+    const long long sx = keys ? p.sxk : p.sxq, sdx = keys ? p.sdxk : p.sdxq;
+    const int H = keys ? p.Hk : p.Hq;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, grp = lane / Y::kLanes, l = lane % Y::kLanes;
+    const Slot<D, T, kInter> w(l, p.rot);
+    const int step = un.parts * Y::kRows, rows = (H + step - 1) / step;
+    int u = (blockIdx.x - (keys ? cq : 0)) * kWarps + warp;
+    int ua = u, left = 0, ha = 0;  // as in the forward: the row this lane fetches next
+    const T *sd = nullptr, *sr = nullptr;
+    auto enter = [&]() {
+        const int tok = ua / un.parts;
+        ha = (ua - tok * un.parts) * Y::kRows + grp;
+        sd = dy + ((size_t)tok * H + ha) * D;
+        sr = x + (size_t)tok * sx + (size_t)ha * D;
+        left = rows;
+    };
+    if (ua < un.count) enter();
+    auto fetch = [&](int slot) {
+        if (ua < un.count) {
+            const bool on = ha < H, ox = on && p.norm;
+            const T *g = on ? sd : dy, *r = on ? sr : x;
+            cp16(&sh.ring[slot][0][threadIdx.x], g + w.at0, on);
+            cp16(&sh.ring[slot][1][threadIdx.x], g + w.at1, on);
+            cp16(&sh.ring[slot][2][threadIdx.x], r + w.at0, ox);
+            cp16(&sh.ring[slot][3][threadIdx.x], r + w.at1, ox);
+            sd += step * D, sr += step * D, ha += step;
+            if (--left == 0) {
+                ua += un.stride;
+                if (ua < un.count) enter();
             }
         }
+        cp_commit();
+    };
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (i0 + u < iters) {
-                const int h = h0 + (i0 + u) * step;
-                float v[8], dz[8];
-                rd[u].get(v);
-                turn<L, kInter, true>(t, v, dz);
-                if (p.norm) {
-                    rx[u].get(v);
-                    float q = 0.f, m = 0.f;
+    for (int i = 0; i < kBwdDepth; ++i) fetch(i);
+    auto position = [&](int v) { return p.rot ? p.pos[v < un.count ? v / un.parts : 0] : 0; };
+    int pos = position(u);
+    Freqs fr;
+    fr.load(p, lane);
+    stage_gain<D>(keys ? p.gk : p.gq, sh.gain);
+    __syncthreads();
+    F2 g0[N], g1[N], a0[N], a1[N];
+    load_pairs(sh.gain + w.at0, g0);
+    load_pairs(sh.gain + w.at1, g1);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        q = fmaf(v[e], v[e], q);
-                        m = fmaf(v[e] * g[e], dz[e], m);
-                    }
-                    q = sum_row<L>(q);
-                    m = sum_row<L>(m);
-                    const float n = rsqrtf(q * (1.f / D) + p.eps), c = m * (1.f / D) * n * n;
+    for (int i = 0; i < N; ++i) a0[i] = a1[i] = f2(0.f, 0.f);
+    const bool all = p.rot == D;
+    int slot = 0;
+    for (; u < un.count; u += un.stride) {
+        const int tok = u / un.parts, h0 = (u - tok * un.parts) * Y::kRows + grp;
+        const int npos = position(u + un.stride);
+        fr.angles<D>(p, pos, sh.cs[warp], lane);
+        Turn<T> t;
+        load_turn<D, T, kInter>(w, sh.cs[warp], sh.cs[warp] + D / 2, t);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        acc[e] = fmaf(dz[e] * n, v[e], acc[e]);
-                        dz[e] = n * fmaf(-c, v[e], g[e] * dz[e]);
+        for (int i = 0; i < N; ++i) t.s0[i] = neg(t.s0[i]), t.s1[i] = neg(t.s1[i]);  // the transposed rotation
+        T *out = dx + (size_t)tok * sdx + (size_t)h0 * D;
+#pragma unroll 1
+        for (int i = 0, h = h0; i < rows; ++i, h += step, out += step * D) {
+            if (slot % kBwdBurst == 0) cp_wait<kBwdBurst>();
+            Chunk<T> a, b;
+            a.v = sh.ring[slot][0][threadIdx.x];
+            b.v = sh.ring[slot][1][threadIdx.x];
+            F2 d0[N], d1[N], z0[N], z1[N];
+            a.get(d0);
+            b.get(d1);
+            turn<T, kInter>(t, w.on0, w.on1, all, d0, d1, z0, z1);
+            if (p.norm) {
+                F2 x0[N], x1[N];
+                a.v = sh.ring[slot][2][threadIdx.x];
+                b.v = sh.ring[slot][3][threadIdx.x];
+                a.get(x0);
+                b.get(x1);
+                F2 q = f2(0.f, 0.f), m = q;
+#pragma unroll
+                for (int i = 0; i < N; ++i) {
+                    q = fma(x0[i], x0[i], q);
+                    q = fma(x1[i], x1[i], q);
+                    d0[i] = mul(x0[i], z0[i]);
+                    d1[i] = mul(x1[i], z1[i]);
+                    m = fma(g0[i], d0[i], m);
+                    m = fma(g1[i], d1[i], m);
+                }
+                const float qs = sum_row<Y::kLanes>(sum2(q)), ms = sum_row<Y::kLanes>(sum2(m));
+                const float n = rsqrtf(qs * (1.f / D) + p.eps), c = -ms * (1.f / D) * n * n;
+                const F2 nn = f2(n, n), cc = f2(c, c);
+                if (h < H) {  // a lane without a row has n = eps^-1/2, infinite for eps = 0
+#pragma unroll
+                    for (int i = 0; i < N; ++i) {
+                        a0[i] = fma(d0[i], nn, a0[i]);
+                        a1[i] = fma(d1[i], nn, a1[i]);
                     }
                 }
-                if (live && h < H) Vec8<T>::store(dx + (size_t)h * D + 8 * l, dz);
+#pragma unroll
+                for (int i = 0; i < N; ++i) {
+                    z0[i] = mul(fma(cc, x0[i], mul(g0[i], z0[i])), nn);
+                    z1[i] = mul(fma(cc, x1[i], mul(g1[i], z1[i])), nn);
+                }
+            }
+            if (++slot % kBwdBurst == 0) {
+#pragma unroll
+                for (int x = kBwdBurst; x > 0; --x) fetch(slot - x);
+                if (slot == kBwdDepth) slot = 0;
+            }
+            if (h < H) {
+                Chunk<T>::store(out + w.at0, z0);
+                Chunk<T>::store(out + w.at1, z1);
             }
         }
+        pos = npos;
     }
-}
-
-// A CTA takes the token blocks b, b + gridDim, ...: a fixed assignment, so the sums over tokens have a fixed order.
-template <int D, typename T, bool kInter>
-__global__ void __launch_bounds__(kThreads, 2) attn_prologue_bwd_kernel(AttnPrologueArgs p, int tb,
-                                                                        float *__restrict__ partial) {
-    constexpr int L = D / 8, NG = kThreads / L;
-    __shared__ float sc[kMaxTok][D / 2], ss[kMaxTok][D / 2];
-    __shared__ float red[NG][D];
-    cudaTriggerProgrammaticLaunchCompletion();
-    const int grp = threadIdx.x / L, l = threadIdx.x % L;
-    const int step = NG / tb, tok = grp / step, h0 = grp % step;
-    float aq[8], ak[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) aq[e] = ak[e] = 0.f;
-    const int blocks = (p.T + tb - 1) / tb;
-    for (int b = blockIdx.x; b < blocks; b += gridDim.x) {
-        const int t0 = b * tb, tt = t0 + tok;
-        __syncthreads();  // the block before has been read
-        make_angles<D>(p, t0, tb, sc, ss);
-        __syncthreads();
-        const bool live = tt < p.T;
-        const size_t tr = live ? (size_t)tt : 0;
-        Turn t;
-        load_turn<D, kInter>(p, l, sc[tok], ss[tok], t);
-        bwd_rows<D, T, kInter>(p, static_cast<const T *>(p.xq) + tr * p.sxq, static_cast<const T *>(p.dq) + tr * p.Hq * D,
-                               p.gq, static_cast<T *>(p.dxq) + tr * p.sdxq, p.Hq, h0, step, live, l, t, aq);
-        bwd_rows<D, T, kInter>(p, static_cast<const T *>(p.xk) + tr * p.sxk, static_cast<const T *>(p.dk) + tr * p.Hk * D,
-                               p.gk, static_cast<T *>(p.dxk) + tr * p.sdxk, p.Hk, h0, step, live, l, t, ak);
-    }
+    cp_wait<0>();
     if (partial == nullptr) return;
+    __syncthreads();  // the ring becomes the table of the lanes' sums
+    constexpr int kGroups = kWarps * Y::kRows;
+    static_assert(sizeof(sh.ring) >= kGroups * D * sizeof(float), "sums fit the ring");
+    float *red = reinterpret_cast<float *>(&sh.ring[0][0][0]), *mine = red + (warp * Y::kRows + grp) * D;
 #pragma unroll
-    for (int which = 0; which < 2; ++which) {
-        __syncthreads();
+    for (int i = 0; i < N; ++i) {
+        split(a0[i], mine[w.at0 + 2 * i], mine[w.at0 + 2 * i + 1]);
+        split(a1[i], mine[w.at1 + 2 * i], mine[w.at1 + 2 * i + 1]);
+    }
+    __syncthreads();
+    if (threadIdx.x < D) {
+        float v = 0.f;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) red[grp][8 * l + e] = which ? ak[e] : aq[e];
-        __syncthreads();
-        if (threadIdx.x < D) {
-            float v = 0.f;
-#pragma unroll
-            for (int x = 0; x < NG; ++x) v += red[x][threadIdx.x];
-            partial[((size_t)blockIdx.x * 2 + which) * D + threadIdx.x] = v;
-        }
+        for (int i = 0; i < kGroups; ++i) v += red[i * D + threadIdx.x];
+        partial[(size_t)blockIdx.x * D + threadIdx.x] = v;
     }
 }
 
-// dg[c] = the CTAs' partial sums: slice s adds the CTAs s, s + 32, ... in order, then the slices are added in order.
+// dg[c] = the partial sums of its CTAs: slice s adds the CTAs s, s + 32, ... in order, then the slices in order.
 template <int D>
-__global__ void __launch_bounds__(1024) attn_prologue_reduce_kernel(const float *__restrict__ partial, int ctas,
+__global__ void __launch_bounds__(1024) attn_prologue_reduce_kernel(const float *__restrict__ partial, int cq, int ctas,
                                                                     float *dgq, float *dgk) {
     __shared__ float red[32][33];
     const int which = blockIdx.x, c = blockIdx.y * 32 + threadIdx.x % 32, sl = threadIdx.x / 32;
+    float *out = which ? dgk : dgq;
     cudaGridDependencySynchronize();
+    if (out == nullptr) return;
+    const int a = which ? cq : 0, e = which ? ctas : cq;
     float v = 0.f;
 #pragma unroll 4
-    for (int i = sl; i < ctas; i += 32) v += __ldcg(partial + ((size_t)i * 2 + which) * D + c);
+    for (int i = a + sl; i < e; i += 32) v += __ldcg(partial + (size_t)i * D + c);
     red[sl][threadIdx.x % 32] = v;
     __syncthreads();
     if (sl == 0) {
         float s = 0.f;
 #pragma unroll
         for (int x = 0; x < 32; ++x) s += red[x][threadIdx.x];
-        float *out = which ? dgk : dgq;
-        if (out) out[c] = s;
+        out[c] = s;
     }
 }
 
-// Tokens of a CTA: about 8 rows for a group of lanes (fewer leave its loads uncovered, more leave SMs idle at the
-// end), fewer tokens while the grid would not fill the GPU twice.
-int tokens_per_cta(int T, int rows, int groups) {
-    int tb = kMaxTok < groups ? kMaxTok : groups;
-    while (tb > 1 && (tb * rows > 8 * groups || (T + tb - 1) / tb < 8 * kAttnSms)) tb /= 2;
-    return tb;
+// Parts of a token: one warp for all its heads while there are `fill` units for each warp of the grid (a part repeats
+// the token's angles, and with fewer units the last round leaves most warps idle), more below, up to one row a lane.
+Units split_units(int T, int most, int rows, int warps, int fill) {
+    Units un;
+    un.parts = 1;
+    while (un.parts * rows < most && (long long)T * un.parts < (long long)fill * warps) un.parts *= 2;
+    un.count = T * un.parts;
+    un.stride = warps;
+    return un;
 }
 
-template <int D, typename T, bool kInter>
-cudaError_t run_fwd(const AttnPrologueArgs &a, bool cache, cudaStream_t st) {
-    const int tb = tokens_per_cta(a.T, a.Hq + a.Hk, kThreads / (D / 8));
-    const int grid = (a.T + tb - 1) / tb;
-    if (cache)
-        GDR2_LAUNCH("attn_prologue_cache", st,
-                    (attn_prologue_fwd_kernel<D, T, kInter, true><<<grid, kThreads, 0, st>>>(a, tb)));
-    else
-        GDR2_LAUNCH("attn_prologue_fwd", st,
-                    (attn_prologue_fwd_kernel<D, T, kInter, false><<<grid, kThreads, 0, st>>>(a, tb)));
+template <typename K> cudaError_t allow_shared(K *kernel, size_t bytes) {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+}
+
+template <int D, typename T, bool kInter, bool kCache>
+cudaError_t run_fwd(const AttnPrologueArgs &a, cudaStream_t st) {
+    constexpr int smem = sizeof(FwdShared<D>), full = kFwdCtas * kAttnSms;
+    const auto kernel = attn_prologue_fwd_kernel<D, T, kInter, kCache>;
+    cudaError_t e = allow_shared(kernel, smem);
+    if (e != cudaSuccess) return e;
+    Units un = split_units(a.T, a.Hq > a.Hk ? a.Hq : a.Hk, Layout<D, T>::kRows, full * kWarps, 2);
+    const int need = (int)(((long long)un.count + kWarps - 1) / kWarps), grid = need < full ? need : full;
+    un.stride = grid * kWarps;
+    GDR2_LAUNCH(kCache ? "attn_prologue_cache" : "attn_prologue_fwd", st, (kernel<<<grid, kThreads, smem, st>>>(a, un)));
     return cudaGetLastError();
 }
 
 template <int D, typename T, bool kInter>
 cudaError_t run_bwd(const AttnPrologueArgs &a, cudaStream_t st) {
-    const int tb = tokens_per_cta(a.T, a.Hq + a.Hk, kThreads / (D / 8));
-    const int blocks = (a.T + tb - 1) / tb, grid = blocks < kBwdCtas ? blocks : kBwdCtas;
+    constexpr int smem = sizeof(BwdShared<D>);
+    const auto kernel = attn_prologue_bwd_kernel<D, T, kInter>;
+    cudaError_t e = allow_shared(kernel, smem);
+    if (e != cudaSuccess) return e;
+    // CTAs in proportion to the heads, at least one each
+    const long long heads = (long long)a.Hq + a.Hk;
+    int cq = (int)((kBwdGrid * (long long)a.Hq + heads / 2) / heads);
+    cq = cq < 1 ? 1 : cq > kBwdGrid - 1 ? kBwdGrid - 1 : cq;
+    int ck = kBwdGrid - cq;
+    auto part = [&](int H, int &ctas) {
+        Units un = split_units(a.T, H, Layout<D, T>::kRows, ctas * kWarps, 8);
+        const int need = (int)(((long long)un.count + kWarps - 1) / kWarps);
+        ctas = need < ctas ? need : ctas;
+        un.stride = ctas * kWarps;
+        return un;
+    };
+    const Units uq = part(a.Hq, cq), uk = part(a.Hk, ck);
     float *partial = a.dgq || a.dgk ? static_cast<float *>(a.workspace) : nullptr;
-    GDR2_LAUNCH("attn_prologue_bwd", st,
-                (attn_prologue_bwd_kernel<D, T, kInter><<<grid, kThreads, 0, st>>>(a, tb, partial)));
-    cudaError_t e = cudaGetLastError();
+    GDR2_LAUNCH("attn_prologue_bwd", st, (kernel<<<cq + ck, kThreads, smem, st>>>(a, uq, uk, cq, partial)));
+    e = cudaGetLastError();
     if (e != cudaSuccess || partial == nullptr) return e;
     GDR2_LAUNCH("attn_prologue_reduce", st,
                 e = launch_dependent(attn_prologue_reduce_kernel<D>, dim3(2, D / 32), dim3(1024), 0, st,
-                                     (const float *)partial, grid, a.dgq, a.dgk));
+                                     (const float *)partial, cq, cq + ck, a.dgq, a.dgk));
     return e;
 }
 
 template <typename F> cudaError_t dispatch(const AttnPrologueArgs &a, F f) {
-    // without a rotation the interleaved form runs: it needs no exchange between lanes
-    const bool inter = a.interleaved || a.rot == 0;
+    const bool inter = a.interleaved;
     if (a.dtype == 1) {
         if (a.d == 128) return inter ? f.template operator()<128, __nv_bfloat16, true>() : f.template operator()<128, __nv_bfloat16, false>();
         return inter ? f.template operator()<64, __nv_bfloat16, true>() : f.template operator()<64, __nv_bfloat16, false>();
@@ -355,7 +577,9 @@ struct Fwd {
     const AttnPrologueArgs &a;
     bool cache;
     cudaStream_t st;
-    template <int D, typename T, bool I> cudaError_t operator()() const { return run_fwd<D, T, I>(a, cache, st); }
+    template <int D, typename T, bool I> cudaError_t operator()() const {
+        return cache ? run_fwd<D, T, I, true>(a, st) : run_fwd<D, T, I, false>(a, st);
+    }
 };
 struct Bwd {
     const AttnPrologueArgs &a;
@@ -365,7 +589,7 @@ struct Bwd {
 
 }  // namespace
 
-size_t attn_prologue_workspace_bytes(int d) { return (size_t)kBwdCtas * 2 * d * sizeof(float); }
+size_t attn_prologue_workspace_bytes(int d) { return (size_t)kBwdGrid * d * sizeof(float); }
 
 cudaError_t launch_attn_prologue_fwd(const AttnPrologueArgs &a, cudaStream_t st) { return dispatch(a, Fwd{a, false, st}); }
 cudaError_t launch_attn_prologue_cache(const AttnPrologueArgs &a, cudaStream_t st) { return dispatch(a, Fwd{a, true, st}); }

@@ -1,5 +1,6 @@
-// attn_vec.cuh -- eight consecutive elements of a row as one lane holds them: as loaded (bf16 packed two to a
-// register) until they are converted, so that several rows can be in flight without eight floats each.
+// attn_vec.cuh -- rows of the query / key prologue as lanes hold them: two 16-byte chunks of a row per lane, kept as
+// loaded (bf16 packed two to a register) until they are converted, and arithmetic on pairs of floats (one instruction
+// for two on sm_100).
 #pragma once
 
 #include <cuda_bf16.h>
@@ -7,49 +8,73 @@
 
 namespace gdr2 {
 
-template <typename T> struct Vec8;
+// Two floats in one 64-bit register pair.
+struct F2 {
+    uint64_t v;
+};
+__device__ __forceinline__ F2 f2(float a, float b) {
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void split(F2 x, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x.v)); }
+__device__ __forceinline__ F2 mul(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 fma(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+__device__ __forceinline__ F2 swap(F2 x) {
+    float a, b;
+    split(x, a, b);
+    return f2(b, a);
+}
+__device__ __forceinline__ F2 neg(F2 x) {
+    F2 r;
+    r.v = x.v ^ 0x8000000080000000ull;
+    return r;
+}
+__device__ __forceinline__ float sum2(F2 x) {
+    float a, b;
+    split(x, a, b);
+    return a + b;
+}
 
-template <> struct Vec8<__nv_bfloat16> {
+// One 16-byte chunk of a row: kPairs pairs of consecutive elements.
+template <typename T> struct Chunk {
+    static constexpr int kElems = 16 / sizeof(T), kPairs = kElems / 2;
     uint4 v;
     __device__ __forceinline__ void zero() { v = make_uint4(0, 0, 0, 0); }
-    __device__ __forceinline__ void load_stream(const __nv_bfloat16 *p) { v = __ldcs(reinterpret_cast<const uint4 *>(p)); }
-    __device__ __forceinline__ void put(__nv_bfloat16 *p) const { *reinterpret_cast<uint4 *>(p) = v; }
-    __device__ __forceinline__ void get(float (&x)[8]) const {
+    __device__ __forceinline__ void load_stream(const T *p) { v = __ldcs(reinterpret_cast<const uint4 *>(p)); }
+    __device__ __forceinline__ void put(T *p) const { *reinterpret_cast<uint4 *>(p) = v; }
+    __device__ __forceinline__ void get(F2 (&x)[kPairs]) const {
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&w[i]));
-            x[2 * i] = f.x, x[2 * i + 1] = f.y;
+        for (int i = 0; i < kPairs; ++i) {
+            if constexpr (sizeof(T) == 2)
+                x[i] = f2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+            else
+                x[i] = f2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
         }
     }
-    static __device__ __forceinline__ void store(__nv_bfloat16 *p, const float (&x)[8]) {
+    static __device__ __forceinline__ void store(T *p, const F2 (&x)[kPairs]) {
         uint32_t w[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-            w[i] = *reinterpret_cast<const uint32_t *>(&b);
+        for (int i = 0; i < kPairs; ++i) {
+            float a, b;
+            split(x[i], a, b);
+            if constexpr (sizeof(T) == 2) {
+                const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+                w[i] = *reinterpret_cast<const uint32_t *>(&h);
+            } else {
+                w[2 * i] = __float_as_uint(a), w[2 * i + 1] = __float_as_uint(b);
+            }
         }
         *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-    }
-};
-
-template <> struct Vec8<float> {
-    float4 a, b;
-    __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
-    __device__ __forceinline__ void load_stream(const float *p) {
-        a = __ldcs(reinterpret_cast<const float4 *>(p));
-        b = __ldcs(reinterpret_cast<const float4 *>(p) + 1);
-    }
-    __device__ __forceinline__ void put(float *p) const {
-        reinterpret_cast<float4 *>(p)[0] = a;
-        reinterpret_cast<float4 *>(p)[1] = b;
-    }
-    __device__ __forceinline__ void get(float (&x)[8]) const {
-        x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-    }
-    static __device__ __forceinline__ void store(float *p, const float (&x)[8]) {
-        reinterpret_cast<float4 *>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
-        reinterpret_cast<float4 *>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
     }
 };
 

@@ -54,15 +54,18 @@ Lists lists(void *ws, int R, int num_pages) {
 
 // A warp's strip of n items: [first, last), whole multiples of 32 long.
 struct Strip {
-    long long first, last;
+    int first, last;
 };
-__device__ __forceinline__ Strip strip(long long n, int warp, int warps) {
-    const long long len = ((n + warps - 1) / warps + 31) / 32 * 32;
+__device__ __forceinline__ int strip_length(int n, int warps) { return ((n + warps - 1) / warps + 31) / 32 * 32; }
+__device__ __forceinline__ Strip strip(int n, int warp, int warps) {
+    const int len = strip_length(n, warps);
     Strip s;
-    s.first = min(n, len * warp);
-    s.last = min(n, s.first + len);
+    s.first = (int)min((long long)n, (long long)len * warp);
+    s.last = (int)min((long long)n, (long long)s.first + len);
     return s;
 }
+
+constexpr int kAhead = 8;  // items of a lane whose loads are in flight together
 
 // Sum of t[0 .. warp) and of all t; every warp on its own. t was written before the cluster's last barrier.
 __device__ __forceinline__ void before(const int *t, int warp, int warps, int lane, int &pre, int &total) {
@@ -76,28 +79,33 @@ __device__ __forceinline__ void before(const int *t, int warp, int warps, int la
     total = __reduce_add_sync(0xffffffffu, b);
 }
 
-__device__ __forceinline__ int entry(const int *table, long long at, int num_pages) {
-    const int e = __ldcg(table + at);
-    return e >= 0 && e < num_pages ? e : -1;
-}
+__device__ __forceinline__ int valid(int e, int num_pages) { return e >= 0 && e < num_pages ? e : -1; }
+__device__ __forceinline__ int entry(const int *table, int at, int num_pages) { return valid(__ldcg(table + at), num_pages); }
 
 // The number of free pages in a strip, and the free pages of rank < most listed by rank.
 __device__ __forceinline__ int count_free(const int *ref, Strip s, int lane) {
     int c = 0;
-    for (long long b = s.first; b < s.last; b += 32) {
-        const long long i = b + lane;
-        c += __popc(__ballot_sync(0xffffffffu, i < s.last && __ldcg(ref + i) <= 0));
+    for (int b = s.first; b < s.last; b += 32 * kAhead) {
+        int n[kAhead];
+#pragma unroll
+        for (int x = 0; x < kAhead; ++x) n[x] = b + 32 * x + lane < s.last ? __ldcg(ref + b + 32 * x + lane) : 1;
+#pragma unroll
+        for (int x = 0; x < kAhead; ++x) c += n[x] <= 0;
     }
-    return c;
+    return __reduce_add_sync(0xffffffffu, c);
 }
 __device__ __forceinline__ void list_free(const int *ref, Strip s, int rank, int most, int *out, int lane) {
-    for (long long b = s.first; b < s.last && rank < most; b += 32) {
-        const long long i = b + lane;
-        const bool is = i < s.last && __ldcg(ref + i) <= 0;
-        const unsigned m = __ballot_sync(0xffffffffu, is);
-        const int at = rank + __popc(m & ((1u << lane) - 1));
-        if (is && at < most) out[at] = (int)i;
-        rank += __popc(m);
+    for (int b = s.first; b < s.last && rank < most; b += 32 * kAhead) {
+        int n[kAhead];
+#pragma unroll
+        for (int x = 0; x < kAhead; ++x) n[x] = b + 32 * x + lane < s.last ? __ldcg(ref + b + 32 * x + lane) : 1;
+#pragma unroll
+        for (int x = 0; x < kAhead; ++x) {
+            const unsigned m = __ballot_sync(0xffffffffu, n[x] <= 0);
+            const int at = rank + __popc(m & ((1u << lane) - 1));
+            if (n[x] <= 0 && at < most) out[at] = b + 32 * x + lane;
+            rank += __popc(m);
+        }
     }
 }
 
@@ -112,76 +120,103 @@ __device__ __forceinline__ Place place() {
     return t;
 }
 
-// Pages for want[r] tokens of every sequence that holds lens[r]: entries from the one of token lens[r] to the one of
-// token want[r] - 1 that are empty get a page. Before that, pages wholly behind the window of the token at lens[r]
-// are released. The grid is one cluster.
+// Pages for tokens [lens[r], want[r]) of every sequence: its entries from the one of token lens[r] to the one of token
+// want[r] - 1 that are empty get a page. Before that, pages wholly behind the window of the token at lens[r] are
+// released. The grid is one cluster.
 __global__ void __launch_bounds__(kThreads) kv_reserve_kernel(KvPagesArgs a, Lists w) {
     cg::cluster_group cl = cg::this_cluster();
     const Place t = place();
-    const long long E = (long long)a.R * a.P;
-    const int ps = a.page_size;
-    for (int i = t.gid; i < a.num_pages; i += t.threads) a.ref_out[i] = __ldcg(a.ref + i);
-    if (t.gid == 0) *a.count_out = 0;
-    cl.sync();
-    // entries: released, and counted where a page is needed
+    const int E = a.R * a.P, ps = a.page_size;
     const Strip es = strip(E, t.warp, t.warps), pg = strip(a.num_pages, t.warp, t.warps);
-    auto needs = [&](int r, int j, int e) {
-        if (e >= 0) return false;
-        const int len = max(a.lens[r], 0), want = a.want[r];
-        return j >= len / ps && want > 0 && j < (want - 1) / ps + 1;
-    };
-    int c = 0;
-    for (long long b = es.first; b < es.last; b += 32) {
-        const long long i = b + t.lane;
-        bool need = false;
-        if (i < es.last) {
-            const int r = (int)(i / a.P), j = (int)(i - (long long)r * a.P);
-            int e = entry(a.table, i, a.num_pages);
-            if (e >= 0 && a.window > 0 && (long long)(j + 1) * ps + a.window <= (long long)max(a.lens[r], 0) + 1) {
-                atomicSub(a.ref_out + e, 1);
-                e = -1;
-            }
-            a.table_out[i] = e;
-            need = needs(r, j, e);
+    // the counts are copied, and free pages counted on the way; a window's releases change them, so then count again
+    int nfree = 0;
+    for (int b = pg.first; b < pg.last; b += 32 * kAhead) {
+        int n[kAhead];
+#pragma unroll
+        for (int x = 0; x < kAhead; ++x) n[x] = b + 32 * x + t.lane < pg.last ? __ldcg(a.ref + b + 32 * x + t.lane) : 1;
+#pragma unroll
+        for (int x = 0; x < kAhead; ++x) {
+            nfree += n[x] <= 0;
+            if (b + 32 * x + t.lane < pg.last) a.ref_out[b + 32 * x + t.lane] = n[x];
         }
-        c += __popc(__ballot_sync(0xffffffffu, need));
     }
-    if (t.lane == 0) w.ta[t.warp] = c;
+    nfree = __reduce_add_sync(0xffffffffu, nfree);
+    if (t.gid == 0) *a.count_out = 0;
+    if (a.window > 0) cl.sync();
+    // entries: released, copied, and counted where a page is needed
+    int c = 0;
+    for (int b = es.first; b < es.last; b += 32 * kAhead) {
+        int e[kAhead], len[kAhead], want[kAhead], j[kAhead];
+#pragma unroll
+        for (int x = 0; x < kAhead; ++x) {
+            const int i = b + 32 * x + t.lane, r = i / a.P;
+            j[x] = i - r * a.P;
+            const bool in = i < es.last;
+            e[x] = in ? __ldcg(a.table + i) : 0;
+            len[x] = in ? __ldg(a.lens + r) : 0;
+            want[x] = in ? __ldg(a.want + r) : 0;
+        }
+#pragma unroll
+        for (int x = 0; x < kAhead; ++x) {
+            const int i = b + 32 * x + t.lane;
+            if (i < es.last) {
+                e[x] = valid(e[x], a.num_pages);
+                len[x] = max(len[x], 0);
+                if (e[x] >= 0 && a.window > 0 && (long long)(j[x] + 1) * ps + a.window <= (long long)len[x] + 1) {
+                    atomicSub(a.ref_out + e[x], 1);
+                    e[x] = -1;
+                }
+                a.table_out[i] = e[x];
+                c += e[x] < 0 && j[x] >= len[x] / ps && want[x] > 0 && j[x] <= (want[x] - 1) / ps;
+            }
+        }
+    }
+    c = __reduce_add_sync(0xffffffffu, c);
+    if (t.lane == 0) w.ta[t.warp] = c, w.tb[t.warp] = nfree;
     int over = 0;  // pages past the table's end
     for (int r = t.gid; r < a.R; r += t.threads) {
         const int want = a.want[r];
         if (want > 0) over += max(0, (want - 1) / ps + 1 - a.P);
     }
+    cl.sync();
+    if (a.window > 0) {
+        nfree = count_free(a.ref_out, pg, t.lane);
+        if (t.lane == 0) w.tb[t.warp] = nfree;
+    }
     over = __reduce_add_sync(0xffffffffu, over);
     if (t.lane == 0 && over) atomicAdd(a.count_out, over);
-    cl.sync();
-    c = count_free(a.ref_out, pg, t.lane);
-    if (t.lane == 0) w.tb[t.warp] = c;
-    cl.sync();
-    int need0, needed, free0, nfree;
+    if (a.window > 0) cl.sync();
+    int need0, needed, free0;
     before(w.ta, t.warp, t.warps, t.lane, need0, needed);
     before(w.tb, t.warp, t.warps, t.lane, free0, nfree);
     list_free(a.ref_out, pg, free0, needed, w.pages, t.lane);
+    if (t.gid == 0 && needed > nfree) atomicAdd(a.count_out, needed - nfree);
     cl.sync();
-    if (w.ta[t.warp] > 0) {
-        for (long long b = es.first; b < es.last; b += 32) {
-            const long long i = b + t.lane;
-            bool need = false;
-            if (i < es.last) {
-                const int r = (int)(i / a.P);
-                need = needs(r, (int)(i - (long long)r * a.P), __ldcg(a.table_out + i));
-            }
+    if (c == 0) return;
+    for (int b = es.first; b < es.last; b += 32 * kAhead) {
+        int e[kAhead], len[kAhead], want[kAhead], j[kAhead];
+#pragma unroll
+        for (int x = 0; x < kAhead; ++x) {
+            const int i = b + 32 * x + t.lane, r = i / a.P;
+            j[x] = i - r * a.P;
+            const bool in = i < es.last;
+            e[x] = in ? __ldcg(a.table_out + i) : 0;
+            len[x] = in ? __ldg(a.lens + r) : 0;
+            want[x] = in ? __ldg(a.want + r) : 0;
+        }
+#pragma unroll
+        for (int x = 0; x < kAhead; ++x) {
+            const bool need = e[x] < 0 && j[x] >= max(len[x], 0) / ps && want[x] > 0 && j[x] <= (want[x] - 1) / ps;
             const unsigned m = __ballot_sync(0xffffffffu, need);
             const int rank = need0 + __popc(m & ((1u << t.lane) - 1));
             if (need && rank < nfree) {
                 const int page = __ldcg(w.pages + rank);
-                a.table_out[i] = page;
+                a.table_out[b + 32 * x + t.lane] = page;
                 a.ref_out[page] = 1;
             }
             need0 += __popc(m);
         }
     }
-    if (t.gid == 0 && needed > nfree) atomicAdd(a.count_out, needed - nfree);
 }
 
 // Every sequence r takes over the content of sequence parent[r] as it was before the call (r itself: stays; outside
@@ -190,11 +225,18 @@ __global__ void __launch_bounds__(kThreads) kv_reserve_kernel(KvPagesArgs a, Lis
 __global__ void __launch_bounds__(kThreads) kv_fork_kernel(KvPagesArgs a, Lists w) {
     cg::cluster_group cl = cg::this_cluster();
     const Place t = place();
-    const long long E = (long long)a.R * a.P;
-    const int ps = a.page_size;
+    const int E = a.R * a.P, ps = a.page_size;
     cudaTriggerProgrammaticLaunchCompletion();
-    for (int i = t.gid; i < a.num_pages; i += t.threads) a.ref_out[i] = __ldcg(a.ref + i);
+    const Strip es = strip(E, t.warp, t.warps), pg = strip(a.num_pages, t.warp, t.warps), rs = strip(a.R, t.warp, t.warps);
     for (int r = t.gid; r < a.R; r += t.threads) w.owner[r] = a.R;
+    for (int b = pg.first; b < pg.last; b += 32 * kAhead) {
+        int n[kAhead];
+#pragma unroll
+        for (int x = 0; x < kAhead; ++x) n[x] = b + 32 * x + t.lane < pg.last ? __ldcg(a.ref + b + 32 * x + t.lane) : 0;
+#pragma unroll
+        for (int x = 0; x < kAhead; ++x)
+            if (b + 32 * x + t.lane < pg.last) a.ref_out[b + 32 * x + t.lane] = n[x];
+    }
     if (t.gid == 0) *a.count_out = 0;
     cl.sync();
     for (int r = t.gid; r < a.R; r += t.threads) {
@@ -202,33 +244,51 @@ __global__ void __launch_bounds__(kThreads) kv_fork_kernel(KvPagesArgs a, Lists 
         if (p >= 0 && p < a.R) atomicMin(w.owner + p, r == p ? -1 : r);
     }
     cl.sync();
-    auto length = [&](int p) { return (int)min((long long)max(a.lens[p], 0), (long long)a.P * ps); };
+    auto length = [&](int p) { return (int)min((long long)max(__ldg(a.lens + p), 0), (long long)a.P * ps); };
     auto owns = [&](int r, int p) { return __ldcg(w.owner + p) == (r == p ? -1 : r); };
-    const Strip es = strip(E, t.warp, t.warps), pg = strip(a.num_pages, t.warp, t.warps), rs = strip(a.R, t.warp, t.warps);
-    for (long long i = es.first + t.lane; i < es.last; i += 32) {
-        const int r = (int)(i / a.P), j = (int)(i - (long long)r * a.P), p = a.parent[r];
-        const int was = entry(a.table, i, a.num_pages);
-        int e = -1;
-        if (p == r) {
-            e = was;
-        } else {
-            if (p >= 0 && p < a.R && (owns(r, p) || j < length(p) / ps)) e = entry(a.table, (long long)p * a.P + j, a.num_pages);
-            if (was >= 0) atomicSub(a.ref_out + was, 1);
-            if (e >= 0) atomicAdd(a.ref_out + e, 1);
+    constexpr int kFew = 4;
+    for (int b = es.first; b < es.last; b += 32 * kFew) {
+        int was[kFew], took[kFew], r[kFew], j[kFew], p[kFew], len[kFew];
+        bool own[kFew];
+#pragma unroll
+        for (int x = 0; x < kFew; ++x) {
+            const int i = b + 32 * x + t.lane;
+            r[x] = i / a.P, j[x] = i - r[x] * a.P;
+            p[x] = i < es.last ? __ldg(a.parent + r[x]) : -1;
+            was[x] = i < es.last ? __ldcg(a.table + i) : -1;
+            if (p[x] >= a.R) p[x] = -1;
         }
-        a.table_out[i] = e;
-        if (j == 0) a.lens_out[r] = p >= 0 && p < a.R ? length(p) : 0;
+#pragma unroll
+        for (int x = 0; x < kFew; ++x) {
+            took[x] = p[x] >= 0 ? __ldcg(a.table + p[x] * a.P + j[x]) : -1;
+            len[x] = p[x] >= 0 ? length(p[x]) : 0;
+            own[x] = p[x] >= 0 && owns(r[x], p[x]);
+        }
+#pragma unroll
+        for (int x = 0; x < kFew; ++x) {
+            const int i = b + 32 * x + t.lane;
+            if (i < es.last) {
+                const int o = valid(was[x], a.num_pages);
+                const int e = own[x] || j[x] < len[x] / ps ? valid(took[x], a.num_pages) : -1;
+                if (p[x] != r[x]) {
+                    if (o >= 0) atomicSub(a.ref_out + o, 1);
+                    if (e >= 0) atomicAdd(a.ref_out + e, 1);
+                }
+                a.table_out[i] = e;
+                if (j[x] == 0) a.lens_out[r[x]] = len[x];
+            }
+        }
     }
-    // sequences that need a copy; source of the copy, or -1
-    auto source = [&](long long r) {
+    // sequences that need a copy: its source, or -1
+    auto source = [&](int r) {
         if (r >= rs.last) return -1;
         const int p = a.parent[r];
-        if (p < 0 || p >= a.R || owns((int)r, p)) return -1;
+        if (p < 0 || p >= a.R || owns(r, p)) return -1;
         const int len = length(p);
-        return len % ps ? entry(a.table, (long long)p * a.P + len / ps, a.num_pages) : -1;
+        return len % ps ? entry(a.table, p * a.P + len / ps, a.num_pages) : -1;
     };
     int c = 0;
-    for (long long b = rs.first; b < rs.last; b += 32) c += __popc(__ballot_sync(0xffffffffu, source(b + t.lane) >= 0));
+    for (int b = rs.first; b < rs.last; b += 32) c += __popc(__ballot_sync(0xffffffffu, source(b + t.lane) >= 0));
     if (t.lane == 0) w.ta[t.warp] = c;
     cl.sync();
     c = count_free(a.ref_out, pg, t.lane);
@@ -238,16 +298,20 @@ __global__ void __launch_bounds__(kThreads) kv_fork_kernel(KvPagesArgs a, Lists 
     before(w.ta, t.warp, t.warps, t.lane, need0, needed);
     before(w.tb, t.warp, t.warps, t.lane, free0, nfree);
     list_free(a.ref_out, pg, free0, needed, w.pages, t.lane);
+    if (t.gid == 0) {
+        w.ncopy[0] = min(needed, nfree);
+        if (needed > nfree) *a.count_out = needed - nfree;
+    }
     cl.sync();
-    for (long long b = rs.first; b < rs.last; b += 32) {
-        const int r = (int)b + t.lane, src = source(r);
+    for (int b = rs.first; b < rs.last; b += 32) {
+        const int r = b + t.lane, src = source(r);
         const unsigned m = __ballot_sync(0xffffffffu, src >= 0);
         const int rank = need0 + __popc(m & ((1u << t.lane) - 1));
         if (src >= 0) {
             const int len = length(a.parent[r]), j = len / ps;
             if (rank < nfree) {
                 const int page = __ldcg(w.pages + rank);
-                a.table_out[(long long)r * a.P + j] = page;
+                a.table_out[r * a.P + j] = page;
                 a.ref_out[page] = 1;
                 w.src[rank] = src, w.dst[rank] = page, w.rows[rank] = len - j * ps;
             } else {
@@ -256,55 +320,57 @@ __global__ void __launch_bounds__(kThreads) kv_fork_kernel(KvPagesArgs a, Lists 
         }
         need0 += __popc(m);
     }
-    if (t.gid == 0) {
-        w.ncopy[0] = min(needed, nfree);
-        if (needed > nfree) *a.count_out = needed - nfree;
-    }
 }
 
 // Live pages numbered live or above move to the free numbers below, in order; table and counts follow.
 __global__ void __launch_bounds__(kThreads) kv_compact_kernel(KvPagesArgs a, Lists w) {
     cg::cluster_group cl = cg::this_cluster();
     const Place t = place();
-    const long long E = (long long)a.R * a.P;
+    const int E = a.R * a.P;
     cudaTriggerProgrammaticLaunchCompletion();
     const Strip pg = strip(a.num_pages, t.warp, t.warps);
     const int nf = count_free(a.ref, pg, t.lane);
-    if (t.lane == 0) w.ta[t.warp] = (int)(pg.last - pg.first) - nf;
+    if (t.lane == 0) w.ta[t.warp] = pg.last - pg.first - nf;
     cl.sync();
     int live0, live;  // live pages before this strip, and in all
     before(w.ta, t.warp, t.warps, t.lane, live0, live);
     // live pages below number `live`: those of the strips before the one that holds it, and of its first part
-    const long long len = ((a.num_pages + t.warps - 1) / t.warps + 31) / 32 * 32;
-    const int mid = (int)(live / len);
+    const int len = strip_length(a.num_pages, t.warps), mid = live / len;
     int below, all;
     before(w.ta, mid, t.warps, t.lane, below, all);
-    for (long long b = mid * len; b < live; b += 32) {
-        const long long i = b + t.lane;
-        below += __popc(__ballot_sync(0xffffffffu, i < live && __ldcg(a.ref + i) > 0));
-    }
+    const Strip part{mid * len, live};
+    below += live - part.first - count_free(a.ref, part, t.lane);
     const int moves = live - below;  // as many live above as free below
-    for (long long b = pg.first; b < pg.last; b += 32) {
-        const long long i = b + t.lane;
-        const int n = i < pg.last ? __ldcg(a.ref + i) : 0;
-        const bool is = n > 0;
-        const unsigned m = __ballot_sync(0xffffffffu, is);
-        const int lb = live0 + __popc(m & ((1u << t.lane) - 1));  // live pages before i
-        if (i < pg.last) {
-            if (i < live) {
-                if (is)
-                    a.ref_out[i] = n;
-                else
-                    w.pages[i - lb] = (int)i;
-            } else {
-                w.rank[i] = is ? lb - below : -1;
-                if (is)
-                    w.high[lb - below] = (int)i;
-                else
-                    a.ref_out[i] = 0;
+    for (int b = pg.first; b < pg.last; b += 32 * kAhead) {
+        int n[kAhead];
+#pragma unroll
+        for (int x = 0; x < kAhead; ++x) n[x] = b + 32 * x + t.lane < pg.last ? __ldcg(a.ref + b + 32 * x + t.lane) : 0;
+#pragma unroll
+        for (int x = 0; x < kAhead; ++x) {
+            const int i = b + 32 * x + t.lane;
+            const bool is = n[x] > 0;
+            const unsigned m = __ballot_sync(0xffffffffu, is);
+            const int lb = live0 + __popc(m & ((1u << t.lane) - 1));  // live pages before i
+            if (i < pg.last) {
+                if (i < live) {
+                    if (is)
+                        a.ref_out[i] = n[x];
+                    else
+                        w.pages[i - lb] = i;
+                } else {
+                    w.rank[i] = is ? lb - below : -1;
+                    if (is)
+                        w.high[lb - below] = i;
+                    else
+                        a.ref_out[i] = 0;
+                }
             }
+            live0 += __popc(m);
         }
-        live0 += __popc(m);
+    }
+    if (t.gid == 0) {
+        w.ncopy[0] = moves;
+        *a.count_out = live;
     }
     cl.sync();
     for (int k = t.gid; k < moves; k += t.threads) {
@@ -313,17 +379,18 @@ __global__ void __launch_bounds__(kThreads) kv_compact_kernel(KvPagesArgs a, Lis
         a.ref_out[dst] = n;
         a.ref_out[src] = 0;
     }
-    for (long long i = t.gid; i < E; i += t.threads) {
-        int e = entry(a.table, i, a.num_pages);
-        if (e >= live) {
-            const int k = __ldcg(w.rank + e);
-            if (k >= 0) e = __ldcg(w.pages + k);
+    const Strip es = strip(E, t.warp, t.warps);
+    for (int b = es.first; b < es.last; b += 32 * kAhead) {
+        int e[kAhead], k[kAhead];
+#pragma unroll
+        for (int x = 0; x < kAhead; ++x) e[x] = b + 32 * x + t.lane < es.last ? entry(a.table, b + 32 * x + t.lane, a.num_pages) : -1;
+#pragma unroll
+        for (int x = 0; x < kAhead; ++x) k[x] = e[x] >= live ? __ldcg(w.rank + e[x]) : -1;
+#pragma unroll
+        for (int x = 0; x < kAhead; ++x) {
+            if (k[x] >= 0) e[x] = __ldcg(w.pages + k[x]);
+            if (b + 32 * x + t.lane < es.last) a.table_out[b + 32 * x + t.lane] = e[x];
         }
-        a.table_out[i] = e;
-    }
-    if (t.gid == 0) {
-        w.ncopy[0] = moves;
-        *a.count_out = live;
     }
 }
 
@@ -335,12 +402,10 @@ __global__ void __launch_bounds__(256) kv_copy_kernel(const int *ncopy, const in
     constexpr int kPiece = 4096;
     const int lane = threadIdx.x & 31;
     const long long block = (long long)page_size * row_bytes;
-    const int pieces = (int)((block + kPiece - 1) / kPiece);
-    const long long items = (long long)__ldcg(ncopy) * Hk * 2 * pieces;
-    for (long long x = (long long)blockIdx.x * 8 + (threadIdx.x >> 5); x < items; x += (long long)gridDim.x * 8) {
-        const int piece = (int)(x % pieces);
-        const long long y = x / pieces;
-        const int hh = (int)(y % (2 * Hk)), i = (int)(y / (2 * Hk)), h = hh >> 1;
+    const uint32_t pieces = (uint32_t)((block + kPiece - 1) / kPiece), heads = 2 * Hk;
+    const uint32_t items = (uint32_t)__ldcg(ncopy) * heads * pieces;  // below 2^32: checked for the whole pool
+    for (uint32_t x = blockIdx.x * 8 + (threadIdx.x >> 5); x < items; x += gridDim.x * 8) {
+        const uint32_t y = x / pieces, piece = x - y * pieces, i = y / heads, hh = y - i * heads, h = hh >> 1;
         const long long bytes = rows ? (long long)__ldcg(rows + i) * row_bytes : block;
         uint8_t *pool = hh & 1 ? v : k;
         const uint8_t *s = pool + ((long long)__ldcg(src + i) * Hk + h) * block;

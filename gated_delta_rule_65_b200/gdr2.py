@@ -489,82 +489,93 @@ ROPE_PLAIN, ROPE_LINEAR, ROPE_BASE, ROPE_PARTS = range(4)
 _ROPE = {"none": ROPE_PLAIN, "linear": ROPE_LINEAR, "base": ROPE_BASE, "parts": ROPE_PARTS}
 
 
+# A decode step makes several of these calls a layer, and a call's kernels take a few microseconds: the helpers below
+# look at each tensor once, without intermediate objects.
+
+
 def _shaped(name, t, shape, dtype):
-    """`t` contiguous, of this shape and dtype (its device is looked at where its pointer is taken)."""
-    if tuple(t.shape) != tuple(shape):
+    """`t` contiguous, of this shape (a tuple) and dtype; its device is looked at by _device."""
+    if t.shape != shape:
         raise ValueError(f"gdr2: {name} has shape {tuple(t.shape)}, not {tuple(shape)}")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"gdr2: {name} is {t.dtype}, not {dtype}")
     if not t.is_contiguous():
         raise ValueError(f"gdr2: {name} must be contiguous")
     return t
 
 
-def _token_rows(name, x, dtype=None):
+def _token_rows(name, x, dtype):
     """Token rows [T, H, d] or [B, T, H, d] with contiguous heads and channels and one stride from token to token
     (a view of a fused projection may have a larger one): (tokens, heads, channels, stride in elements)."""
-    if x.dim() not in (3, 4):
-        raise ValueError(f"gdr2: {name} must be [T, H, d] or [B, T, H, d]")
-    if dtype is not None and x.dtype != dtype:
-        raise TypeError(f"gdr2: {name} is {x.dtype}, not {dtype}")
-    H, d = x.shape[-2], x.shape[-1]
-    T = x.numel() // (H * d) if H * d else 0
-    if T == 0:
-        raise ValueError(f"gdr2: {name} is empty")
-    if (d > 1 and x.stride(-1) != 1) or (H > 1 and x.stride(-2) != d):
-        raise ValueError(f"gdr2: heads and channels of {name} must be contiguous")
-    n = x.shape[-3]
-    if n > 1:
-        stride = x.stride(-3)
-        if x.dim() == 4 and x.shape[0] > 1 and x.stride(0) != n * stride:
+    shape, strides = x.shape, x.stride()
+    if len(shape) == 3:
+        T, H, d = shape
+        step = strides[0]
+    elif len(shape) == 4:
+        B, n, H, d = shape
+        T = B * n
+        if B > 1 and n > 1 and strides[0] != n * strides[1]:
             raise ValueError(f"gdr2: the tokens of {name} must have one stride across the batch")
-    elif T > 1:
-        stride = x.stride(0)
+        step = strides[1] if n > 1 else strides[0]
     else:
-        stride = H * d
-    return T, H, d, stride
+        raise ValueError(f"gdr2: {name} must be [T, H, d] or [B, T, H, d]")
+    if x.dtype is not dtype:
+        raise TypeError(f"gdr2: {name} is {x.dtype}, not {dtype}")
+    if T * H * d == 0:
+        raise ValueError(f"gdr2: {name} is empty")
+    if (d > 1 and strides[-1] != 1) or (H > 1 and strides[-2] != d):
+        raise ValueError(f"gdr2: heads and channels of {name} must be contiguous")
+    return T, H, d, step if T > 1 else H * d
 
 
 def _device(*tensors):
-    """Every tensor on the current CUDA device, which is where the library launches."""
-    dev = tensors[0].device
-    if dev.type != "cuda":
+    """The index of the current CUDA device, where every tensor has to be: the library launches there."""
+    index = tensors[0].get_device()
+    if index < 0:
         raise ValueError("gdr2: tensors must live on a CUDA device")
     for t in tensors:
-        if t is not None and t.device != dev:
-            raise ValueError(f"gdr2: tensors on different devices ({dev} and {t.device})")
-    if dev.index != torch.cuda.current_device():
-        raise ValueError(f"gdr2: tensors on {dev}, which is not the current CUDA device")
-    return dev
+        if t is not None and t.get_device() != index:
+            raise ValueError(f"gdr2: tensors on different devices ({tensors[0].device} and {t.device})")
+    if index != torch._C._cuda_getDevice():
+        raise ValueError(f"gdr2: tensors on {tensors[0].device}, which is not the current CUDA device")
+    return index
 
 
 def _p(t):
     return None if t is None else t.data_ptr()
 
 
-def _scratch(n, dev, stream):
-    """Workspace of one call; with an explicit stream it is kept until that stream has passed the call."""
-    return _kept(torch.empty(n, dtype=torch.uint8, device=dev), stream)
-
-
 def _kept(t, stream):
+    """A fresh tensor that an explicit stream is about to use: its memory is not handed out again before that stream
+    has passed the call."""
     if stream is not None:
         t.record_stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream)))
     return t
 
 
-def _raw_stream(stream):
+def _raw_stream(stream, index):
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        return torch._C._cuda_getCurrentRawStream(index)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
-def _workspace(workspace, need, dev, stream):
+def _workspace(workspace, need, like, stream):
     if workspace is None:
-        workspace = _scratch(need, dev, stream)
-    elif workspace.device != dev or not workspace.is_contiguous():
+        return _kept(like.new_empty(need, dtype=torch.uint8), stream), need
+    if workspace.get_device() != like.get_device() or not workspace.is_contiguous():
         raise ValueError("gdr2: the workspace must be contiguous and on the tensors' device")
     return workspace, workspace.numel() * workspace.element_size()
+
+
+_sizes = {}
+
+
+def _bytes(name, *args):
+    """A workspace query's answer, at least 16 bytes; it depends on its arguments alone."""
+    n = _sizes.get((name, args))
+    if n is None:
+        n = _sizes[(name, args)] = max(16, int(getattr(lib(), name)(*args)))
+    return n
 
 
 def rope_freqs(rot, base=10000.0, *, scaling="none", factor=1.0, orig_len=0, turns_low=1.0, turns_high=32.0,
@@ -581,33 +592,26 @@ def rope_freqs(rot, base=10000.0, *, scaling="none", factor=1.0, orig_len=0, tur
     return torch.tensor(list(buf), dtype=torch.float64, device=device), float(mag.value)
 
 
-def _gains(gq, gk, norm, d):
-    if not norm and (gq is not None or gk is not None):
-        raise ValueError("gdr2: gq and gk are gains of the norm; pass None without it")
-    for name, g in (("gq", gq), ("gk", gk)):
-        if g is not None:
-            _shaped(name, g, (d,), torch.float32)
-
-
-def _rope_args(pos, freqs, T, d):
-    """(tokens' positions, frequencies, rot)"""
-    if freqs is None:
-        return 0
-    if freqs.dtype != torch.float64 or freqs.dim() != 1 or not freqs.is_contiguous():
-        raise TypeError("gdr2: freqs must be a contiguous 1-D float64 tensor")
-    if pos is None or pos.dtype != torch.int32 or pos.numel() != T or not pos.is_contiguous():
-        raise ValueError("gdr2: pos must hold one int32 position for each token")
-    return 2 * freqs.numel()
-
-
 def _prologue_checks(xq, xk, gq, gk, pos, freqs, norm):
-    T, Hq, d, sq = _token_rows("xq", xq)
+    dt = _dtype_code(xq)
+    T, Hq, d, sq = _token_rows("xq", xq, xq.dtype)
     Tk, Hk, dk, sk = _token_rows("xk", xk, xq.dtype)
     if Tk != T or dk != d:
         raise ValueError("gdr2: xq and xk must have the same tokens and channels")
-    dt = _dtype_code(xq)
-    _gains(gq, gk, norm, d)
-    return T, Hq, Hk, d, sq, sk, dt, _rope_args(pos, freqs, T, d)
+    if gq is not None:
+        _shaped("gq", gq, (d,), torch.float32)
+    if gk is not None:
+        _shaped("gk", gk, (d,), torch.float32)
+    if not norm and (gq is not None or gk is not None):
+        raise ValueError("gdr2: gq and gk are gains of the norm; pass None without it")
+    rot = 0
+    if freqs is not None:
+        if freqs.dtype is not torch.float64 or freqs.dim() != 1 or not freqs.is_contiguous():
+            raise TypeError("gdr2: freqs must be a contiguous 1-D float64 tensor")
+        if pos is None or pos.dtype is not torch.int32 or pos.numel() != T or not pos.is_contiguous():
+            raise ValueError("gdr2: pos must hold one int32 position for each token")
+        rot = 2 * freqs.shape[0]
+    return T, Hq, Hk, d, sq, sk, dt, rot
 
 
 def attn_prologue_fwd(xq, xk, gq=None, gk=None, pos=None, freqs=None, *, norm=True, eps=1e-6, mag=1.0,
@@ -616,17 +620,16 @@ def attn_prologue_fwd(xq, xk, gq=None, gk=None, pos=None, freqs=None, *, norm=Tr
     rotary positions of xq [.., T, Hq, d] and xk [.., T, Hk, d] (views of a fused projection allowed), pos int32 for
     each token and freqs float64 (rope_freqs; None: no rotation). Returns a dict q, k (contiguous)."""
     T, Hq, Hk, d, sq, sk, dt, rot = _prologue_checks(xq, xk, gq, gk, pos, freqs, norm)
-    dev = _device(xq, xk, gq, gk, pos, freqs)
     if out is None:
-        out = {"q": torch.empty(xq.shape, dtype=xq.dtype, device=dev),
-               "k": torch.empty(xk.shape, dtype=xq.dtype, device=dev)}
-        _kept(out["q"], stream), _kept(out["k"], stream)
+        index = _device(xq, xk, gq, gk, pos, freqs)
+        out = {"q": _kept(xq.new_empty(xq.shape), stream), "k": _kept(xk.new_empty(xk.shape), stream)}
     else:
         _shaped("q", out["q"], xq.shape, xq.dtype), _shaped("k", out["k"], xk.shape, xq.dtype)
-        _device(xq, out["q"], out["k"])
-    st = lib().gdr2_attn_prologue_fwd(_p(xq), _p(xk), _p(gq), _p(gk), int(norm), eps, _p(pos), _p(freqs), mag, rot,
-                                      int(interleaved), _p(out["q"]), _p(out["k"]), T, Hq, Hk, d, dt, sq, sk,
-                                      _raw_stream(stream))
+        index = _device(xq, xk, gq, gk, pos, freqs, out["q"], out["k"])
+    st = (_lib or lib()).gdr2_attn_prologue_fwd(
+        xq.data_ptr(), xk.data_ptr(), _p(gq), _p(gk), 1 if norm else 0, eps, _p(pos), _p(freqs), mag, rot,
+        1 if interleaved else 0, out["q"].data_ptr(), out["k"].data_ptr(), T, Hq, Hk, d, dt, sq, sk,
+        _raw_stream(stream, index))
     _check("gdr2_attn_prologue_fwd", st)
     return out
 
@@ -638,48 +641,50 @@ def attn_prologue_bwd(xq, xk, gq, gk, pos, freqs, dq, dk, *, norm=True, eps=1e-6
     leave dgq, dgk out or None when they are not wanted."""
     T, Hq, Hk, d, sq, sk, dt, rot = _prologue_checks(xq, xk, gq, gk, pos, freqs, norm)
     _shaped("dq", dq, xq.shape, xq.dtype), _shaped("dk", dk, xk.shape, xq.dtype)
-    dev = _device(xq, xk, gq, gk, pos, freqs, dq, dk)
+    index = _device(xq, xk, gq, gk, pos, freqs, dq, dk)
     if out is None:
-        out = {"dxq": torch.empty(xq.shape, dtype=xq.dtype, device=dev),
-               "dxk": torch.empty(xk.shape, dtype=xq.dtype, device=dev)}
+        out = {"dxq": _kept(xq.new_empty(xq.shape), stream), "dxk": _kept(xk.new_empty(xk.shape), stream)}
+        sdq, sdk = Hq * d, Hk * d
         if norm:
-            out["dgq"] = torch.empty(d, dtype=torch.float32, device=dev)
-            out["dgk"] = torch.empty(d, dtype=torch.float32, device=dev)
-        for t in out.values():
-            _kept(t, stream)
-    dgq, dgk = out.get("dgq"), out.get("dgk")
-    Tq, hq, eq, sdq = _token_rows("dxq", out["dxq"], xq.dtype)
-    Tk, hk, ek, sdk = _token_rows("dxk", out["dxk"], xq.dtype)
-    if (Tq, hq, eq) != (T, Hq, d) or (Tk, hk, ek) != (T, Hk, d):
-        raise ValueError("gdr2: dxq and dxk must have the shapes of xq and xk")
-    for name, g in (("dgq", dgq), ("dgk", dgk)):
-        if g is not None:
-            _shaped(name, g, (d,), torch.float32)
-    _device(xq, out["dxq"], out["dxk"], dgq, dgk)
+            out["dgq"] = _kept(xq.new_empty(d, dtype=torch.float32), stream)
+            out["dgk"] = _kept(xq.new_empty(d, dtype=torch.float32), stream)
+        dgq, dgk = out.get("dgq"), out.get("dgk")
+    else:
+        dgq, dgk = out.get("dgq"), out.get("dgk")
+        Tq, hq, eq, sdq = _token_rows("dxq", out["dxq"], xq.dtype)
+        Tk, hk, ek, sdk = _token_rows("dxk", out["dxk"], xq.dtype)
+        if (Tq, hq, eq) != (T, Hq, d) or (Tk, hk, ek) != (T, Hk, d):
+            raise ValueError("gdr2: dxq and dxk must have the shapes of xq and xk")
+        for name, g in (("dgq", dgq), ("dgk", dgk)):
+            if g is not None:
+                _shaped(name, g, (d,), torch.float32)
+        _device(xq, out["dxq"], out["dxk"], dgq, dgk)
     nbytes = 0
     if dgq is not None or dgk is not None:
-        workspace, nbytes = _workspace(workspace, max(16, int(lib().gdr2_attn_prologue_workspace_bytes(d))), dev, stream)
-    st = lib().gdr2_attn_prologue_bwd(_p(xq), _p(xk), _p(gq), _p(gk), int(norm), eps, _p(pos), _p(freqs), mag, rot,
-                                      int(interleaved), _p(dq), _p(dk), _p(out["dxq"]), _p(out["dxk"]), _p(dgq),
-                                      _p(dgk), T, Hq, Hk, d, dt, sq, sk, sdq, sdk, _p(workspace), nbytes,
-                                      _raw_stream(stream))
+        workspace, nbytes = _workspace(workspace, _bytes("gdr2_attn_prologue_workspace_bytes", d), xq, stream)
+    st = (_lib or lib()).gdr2_attn_prologue_bwd(
+        xq.data_ptr(), xk.data_ptr(), _p(gq), _p(gk), 1 if norm else 0, eps, _p(pos), _p(freqs), mag, rot,
+        1 if interleaved else 0, dq.data_ptr(), dk.data_ptr(), out["dxq"].data_ptr(), out["dxk"].data_ptr(), _p(dgq),
+        _p(dgk), T, Hq, Hk, d, dt, sq, sk, sdq, sdk, _p(workspace), nbytes, _raw_stream(stream, index))
     _check("gdr2_attn_prologue_bwd", st)
     return out
 
 
 def _pools(k_pages, v_pages):
-    if k_pages.dim() != 4:
+    shape = k_pages.shape
+    if len(shape) != 4:
         raise ValueError("gdr2: k_pages must be [num_pages, Hk, page_size, d]")
-    _shaped("k_pages", k_pages, k_pages.shape, k_pages.dtype)
-    _shaped("v_pages", v_pages, k_pages.shape, k_pages.dtype)
-    return k_pages.shape
+    _shaped("k_pages", k_pages, shape, k_pages.dtype)
+    _shaped("v_pages", v_pages, shape, k_pages.dtype)
+    return shape
 
 
 def _table(table):
-    if table.dim() != 2:
+    shape = table.shape
+    if len(shape) != 2:
         raise ValueError("gdr2: table must be [R, P]")
-    _shaped("table", table, table.shape, torch.int32)
-    return table.shape
+    _shaped("table", table, shape, torch.int32)
+    return shape
 
 
 def attn_prologue_cache(xq, xk, xv, gq, gk, seq, pos, freqs, k_pages, v_pages, table, *, norm=True, eps=1e-6,
@@ -691,19 +696,23 @@ def attn_prologue_cache(xq, xk, xv, gq, gk, seq, pos, freqs, k_pages, v_pages, t
     Tv, Hv, dv, sv = _token_rows("xv", xv, xq.dtype)
     num, Hp, ps, dp = _pools(k_pages, v_pages)
     R, P = _table(table)
-    if (Tv, Hv, dv) != (T, Hk, d) or (Hp, dp) != (Hk, d) or k_pages.dtype != xq.dtype:
-        raise ValueError("gdr2: xk, xv and the pools must agree in heads, channels and dtype")
+    if Tv != T or Hv != Hk or dv != d or Hp != Hk or dp != d or k_pages.dtype is not xq.dtype:
+        raise ValueError("gdr2: xk, xv and the pools must agree in tokens, heads, channels and dtype")
     if pos is None:
         raise ValueError("gdr2: pos is needed to find a token's page")
-    _shaped("seq", seq, (T,), torch.int32), _shaped("pos", pos.view(-1), (T,), torch.int32)
-    dev = _device(xq, xk, xv, gq, gk, seq, pos, freqs, k_pages, v_pages, table, q)
+    if freqs is None and (pos.dtype is not torch.int32 or pos.numel() != T or not pos.is_contiguous()):
+        raise ValueError("gdr2: pos must hold one int32 position for each token")
+    _shaped("seq", seq, (T,), torch.int32)
     if q is None:
-        q = _kept(torch.empty(xq.shape, dtype=xq.dtype, device=dev), stream)
+        index = _device(xq, xk, xv, gq, gk, seq, pos, freqs, k_pages, v_pages, table)
+        q = _kept(xq.new_empty(xq.shape), stream)
     else:
         _shaped("q", q, xq.shape, xq.dtype)
-    st = lib().gdr2_attn_prologue_cache(_p(xq), _p(xk), _p(xv), _p(gq), _p(gk), int(norm), eps, _p(seq), _p(pos),
-                                        _p(freqs), mag, rot, int(interleaved), _p(q), _p(k_pages), _p(v_pages),
-                                        _p(table), T, Hq, Hk, d, R, P, ps, num, dt, sq, sk, sv, _raw_stream(stream))
+        index = _device(xq, xk, xv, gq, gk, seq, pos, freqs, k_pages, v_pages, table, q)
+    st = (_lib or lib()).gdr2_attn_prologue_cache(
+        xq.data_ptr(), xk.data_ptr(), xv.data_ptr(), _p(gq), _p(gk), 1 if norm else 0, eps, seq.data_ptr(),
+        pos.data_ptr(), _p(freqs), mag, rot, 1 if interleaved else 0, q.data_ptr(), k_pages.data_ptr(),
+        v_pages.data_ptr(), table.data_ptr(), T, Hq, Hk, d, R, P, ps, num, dt, sq, sk, sv, _raw_stream(stream, index))
     _check("gdr2_attn_prologue_cache", st)
     return q
 
@@ -713,47 +722,46 @@ def attn_decode(q, k_pages, v_pages, table, lens, seq=None, *, scale=None, windo
     """gdr2_attn_decode: attention of one new token for each row of q [N, Hq, d] over sequence seq[n] (int32 [N];
     None: n) of the cache, its last `window` tokens (0: all), lens int32 [R] with the new token counted. scale: by
     default d^-1/2. Returns o [N, Hq, d], or (o, lse fp32 [N, Hq]) with want_lse or a given lse."""
-    if q.dim() != 3:
+    shape = q.shape
+    if len(shape) != 3:
         raise ValueError("gdr2: q must be [N, Hq, d]")
-    N, Hq, d = _shaped("q", q, q.shape, q.dtype).shape
+    _shaped("q", q, shape, q.dtype)
+    N, Hq, d = shape
     num, Hk, ps, dp = _pools(k_pages, v_pages)
     R, P = _table(table)
-    if dp != d or k_pages.dtype != q.dtype:
+    if dp != d or k_pages.dtype is not q.dtype:
         raise ValueError("gdr2: q and the pools must agree in channels and dtype")
     _shaped("lens", lens, (R,), torch.int32)
     if seq is not None:
         _shaped("seq", seq, (N,), torch.int32)
     dt = _dtype_code(q)
-    dev = _device(q, k_pages, v_pages, table, lens, seq, o, lse)
+    index = _device(q, k_pages, v_pages, table, lens, seq, o, lse)
     if o is None:
-        o = _kept(torch.empty_like(q), stream)
+        o = _kept(q.new_empty(shape), stream)
     else:
-        _shaped("o", o, q.shape, q.dtype)
+        _shaped("o", o, shape, q.dtype)
     if lse is not None:
         _shaped("lse", lse, (N, Hq), torch.float32)
     elif want_lse:
-        lse = _kept(torch.empty((N, Hq), dtype=torch.float32, device=dev), stream)
-    L = lib()
-    workspace, nbytes = _workspace(workspace, max(16, int(L.gdr2_attn_decode_workspace_bytes(d))), dev, stream)
-    st = L.gdr2_attn_decode(_p(q), _p(k_pages), _p(v_pages), _p(table), _p(lens), _p(seq),
-                            d ** -0.5 if scale is None else scale, window, _p(o), _p(lse), N, Hq, Hk, d, R, P, ps,
-                            num, dt, _p(workspace), nbytes, _raw_stream(stream))
+        lse = _kept(q.new_empty((N, Hq), dtype=torch.float32), stream)
+    workspace, nbytes = _workspace(workspace, _bytes("gdr2_attn_decode_workspace_bytes", d), q, stream)
+    st = (_lib or lib()).gdr2_attn_decode(
+        q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), table.data_ptr(), lens.data_ptr(), _p(seq),
+        d ** -0.5 if scale is None else scale, window, o.data_ptr(), _p(lse), N, Hq, Hk, d, R, P, ps, num, dt,
+        workspace.data_ptr(), nbytes, _raw_stream(stream, index))
     _check("gdr2_attn_decode", st)
     return o if lse is None else (o, lse)
 
 
-def _kv_outs(names, given, likes, dev, stream):
-    """The bookkeeping outputs, given in `out` or fresh."""
-    got = []
-    for name, (shape, like) in zip(names, likes):
-        t = None if given is None else given.get(name)
-        if t is None:
-            t = _kept(torch.empty(shape, dtype=torch.int32, device=dev), stream)
-        else:
-            _shaped(name, t, shape, torch.int32)
-            _device(like, t)
-        got.append(t)
-    return got
+def _int_out(out, name, like, shape, stream):
+    """A bookkeeping output: the one given in `out`, or a fresh one."""
+    t = None if out is None else out.get(name)
+    if t is None:
+        return _kept(like.new_empty(shape), stream)
+    _shaped(name, t, shape, torch.int32)
+    if t.get_device() != like.get_device():
+        raise ValueError(f"gdr2: {name} on another device")
+    return t
 
 
 def kv_reserve(table, lens, want, ref, *, page_size, window=0, out=None, workspace=None, stream=None):
@@ -761,13 +769,15 @@ def kv_reserve(table, lens, want, ref, *, page_size, window=0, out=None, workspa
     first). Returns (table, ref, missing int32 [1]) after the call; `out` may name them (also the inputs)."""
     R, P = _table(table)
     _shaped("lens", lens, (R,), torch.int32), _shaped("want", want, (R,), torch.int32)
-    num = _shaped("ref", ref, (ref.numel(),), torch.int32).numel()
-    dev = _device(table, lens, want, ref)
-    t, r, m = _kv_outs(("table", "ref", "missing"), out, (((R, P), table), ((num,), ref), ((1,), ref)), dev, stream)
-    L = lib()
-    workspace, nbytes = _workspace(workspace, max(16, int(L.gdr2_kv_workspace_bytes(R, num))), dev, stream)
-    st = L.gdr2_kv_reserve(_p(table), _p(lens), _p(want), _p(ref), _p(t), _p(r), _p(m), R, P, page_size, num, window,
-                           _p(workspace), nbytes, _raw_stream(stream))
+    num = ref.numel()
+    _shaped("ref", ref, (num,), torch.int32)
+    index = _device(table, lens, want, ref)
+    t, r = _int_out(out, "table", table, (R, P), stream), _int_out(out, "ref", ref, (num,), stream)
+    m = _int_out(out, "missing", ref, (1,), stream)
+    workspace, nbytes = _workspace(workspace, _bytes("gdr2_kv_workspace_bytes", R, num), ref, stream)
+    st = (_lib or lib()).gdr2_kv_reserve(
+        table.data_ptr(), lens.data_ptr(), want.data_ptr(), ref.data_ptr(), t.data_ptr(), r.data_ptr(), m.data_ptr(),
+        R, P, page_size, num, window, workspace.data_ptr(), nbytes, _raw_stream(stream, index))
     _check("gdr2_kv_reserve", st)
     return t, r, m
 
@@ -780,13 +790,14 @@ def kv_fork(table, lens, ref, parent, k_pages, v_pages, *, out=None, workspace=N
     _shaped("lens", lens, (R,), torch.int32), _shaped("parent", parent, (R,), torch.int32)
     _shaped("ref", ref, (num,), torch.int32)
     dt = _dtype_code(k_pages)
-    dev = _device(table, lens, ref, parent, k_pages, v_pages)
-    t, n, r, m = _kv_outs(("table", "lens", "ref", "missing"), out,
-                          (((R, P), table), ((R,), lens), ((num,), ref), ((1,), ref)), dev, stream)
-    L = lib()
-    workspace, nbytes = _workspace(workspace, max(16, int(L.gdr2_kv_workspace_bytes(R, num))), dev, stream)
-    st = L.gdr2_kv_fork(_p(table), _p(lens), _p(ref), _p(parent), _p(t), _p(n), _p(r), _p(m), _p(k_pages),
-                        _p(v_pages), R, P, Hk, ps, d, num, dt, _p(workspace), nbytes, _raw_stream(stream))
+    index = _device(table, lens, ref, parent, k_pages, v_pages)
+    t, n = _int_out(out, "table", table, (R, P), stream), _int_out(out, "lens", lens, (R,), stream)
+    r, m = _int_out(out, "ref", ref, (num,), stream), _int_out(out, "missing", ref, (1,), stream)
+    workspace, nbytes = _workspace(workspace, _bytes("gdr2_kv_workspace_bytes", R, num), ref, stream)
+    st = (_lib or lib()).gdr2_kv_fork(
+        table.data_ptr(), lens.data_ptr(), ref.data_ptr(), parent.data_ptr(), t.data_ptr(), n.data_ptr(), r.data_ptr(),
+        m.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), R, P, Hk, ps, d, num, dt, workspace.data_ptr(), nbytes,
+        _raw_stream(stream, index))
     _check("gdr2_kv_fork", st)
     return t, n, r, m
 
@@ -797,12 +808,13 @@ def kv_compact(table, ref, k_pages, v_pages, *, out=None, workspace=None, stream
     num, Hk, ps, d = _pools(k_pages, v_pages)
     _shaped("ref", ref, (num,), torch.int32)
     dt = _dtype_code(k_pages)
-    dev = _device(table, ref, k_pages, v_pages)
-    t, r, m = _kv_outs(("table", "ref", "live"), out, (((R, P), table), ((num,), ref), ((1,), ref)), dev, stream)
-    L = lib()
-    workspace, nbytes = _workspace(workspace, max(16, int(L.gdr2_kv_workspace_bytes(R, num))), dev, stream)
-    st = L.gdr2_kv_compact(_p(table), _p(ref), _p(t), _p(r), _p(m), _p(k_pages), _p(v_pages), R, P, Hk, ps, d, num,
-                           dt, _p(workspace), nbytes, _raw_stream(stream))
+    index = _device(table, ref, k_pages, v_pages)
+    t, r = _int_out(out, "table", table, (R, P), stream), _int_out(out, "ref", ref, (num,), stream)
+    m = _int_out(out, "live", ref, (1,), stream)
+    workspace, nbytes = _workspace(workspace, _bytes("gdr2_kv_workspace_bytes", R, num), ref, stream)
+    st = (_lib or lib()).gdr2_kv_compact(
+        table.data_ptr(), ref.data_ptr(), t.data_ptr(), r.data_ptr(), m.data_ptr(), k_pages.data_ptr(),
+        v_pages.data_ptr(), R, P, Hk, ps, d, num, dt, workspace.data_ptr(), nbytes, _raw_stream(stream, index))
     _check("gdr2_kv_compact", st)
     return t, r, m
 
