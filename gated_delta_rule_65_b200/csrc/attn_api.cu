@@ -160,7 +160,10 @@ int gdr2_attn_decode(const void *q, const void *k_pages, const void *v_pages, co
     if (st == GDR2_OK) st = check_pages(R, P, page_size, num_pages);
     if (st != GDR2_OK) return st;
     if (N <= 0 || Hq % Hk != 0 || window < 0 || (seq == nullptr && N > R)) return GDR2_ERR_INVALID_ARG;
-    if ((long long)N * Hq > 0x7fffffffLL) return GDR2_ERR_UNSUPPORTED;
+    // rows of the work and token rows of the pool are counted in 32 bits
+    if ((long long)N * Hq > 0x7fffffffLL || (long long)Hk * page_size > 0x7fffffffLL ||
+        (long long)Hk * page_size * num_pages > 0xffffffffLL)
+        return GDR2_ERR_UNSUPPORTED;
     if (!ok_ptr(q) || !ok_ptr(k_pages) || !ok_ptr(v_pages) || !ok_num(table) || !ok_num(lens) || !opt_num(seq) ||
         !ok_ptr(o) || !opt_num(lse))
         return GDR2_ERR_INVALID_ARG;

@@ -30,24 +30,28 @@
 namespace gdr2 {
 namespace {
 
-constexpr int kCtas = 2 * kAttnSms;  // CTAs of the line: two resident per SM
+constexpr int kMaxCtas = 3 * kAttnSms;  // CTAs of the line: two or three resident on an SM
 constexpr int kWarps = 4, kThreads = 32 * kWarps;
-constexpr int kRing = 24 * 1024;     // bytes of a warp's stages
-constexpr int kMaxRows = 16;         // query heads of a row of the line
+constexpr int kRing = 16 * 1024;        // bytes of a warp's stages
+constexpr int kMaxRows = 16;            // query heads of a row of the line
+constexpr int kWholeTiles = 8;          // rows of at most so many tiles are not cut
 constexpr float kLn2 = 0.69314718055994530942f, kLog2e = 1.4426950408889634074f;
 
 // Workspace: per CTA two partial rows (0: a row begun by an earlier CTA, 1: a row that goes on in the next) with their
-// (m, l) pairs, and the ids of those rows (-1: none).
+// (m, l) pairs; and the rows that borders cut, (row, CTA where it begins, its CTAs), row -1: none. Their list is kept
+// by row where the line has fewer rows than CTAs, else by the CTA where a row begins (at most one each).
 struct Partials {
     float *o, *ml;
-    int *row;
+    int4 *cut;
+    int by_row;
 };
-__host__ __device__ inline size_t partial_floats(int d) { return (size_t)kCtas * 2 * kMaxRows * d; }
+__host__ __device__ inline size_t partial_floats(int d) { return (size_t)kMaxCtas * 2 * kMaxRows * d; }
 inline Partials partials(void *ws, int d) {
     Partials w;
     w.o = static_cast<float *>(ws);
     w.ml = w.o + partial_floats(d);
-    w.row = reinterpret_cast<int *>(w.ml + (size_t)kCtas * 2 * kMaxRows * 2);
+    w.cut = reinterpret_cast<int4 *>(w.ml + (size_t)kMaxCtas * 2 * kMaxRows * 2);
+    w.by_row = 0;
     return w;
 }
 
@@ -77,105 +81,132 @@ __device__ __forceinline__ uint32_t pack2(float x, float y) {
 __device__ __forceinline__ float2 unpack2(uint32_t w) { return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&w)); }
 // 2^(x - m) with m = -inf standing for "no token yet" (then x = -inf too, and the result is 0, not NaN).
 __device__ __forceinline__ float pow2_rel(float x, float m) { return exp2f(x - (m == -INFINITY ? 0.f : m)); }
+// 2^x for the main loop: 2 steps of fp32, results below 2^-126 are zero (next to a maximum of 1 they are nothing).
+__device__ __forceinline__ float pow2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 
 // What the line is made of. A row: (sequence n, KV head h, block of up to `rows` of its query heads).
 struct Line {
-    int G, nb, HG, rows;  // query heads of a KV head, blocks of them, rows of a sequence, heads of a block
+    int G, nb, rows;        // query heads of a KV head, blocks of them, heads of a block
+    int whole;              // no row is cut
+    uint32_t magic, shift;  // x / page_size = x * magic >> shift for x < 2^31
 };
+__host__ inline void set_divisor(Line &ln, uint32_t d) {  // magic = floor(2^(31 + s) / d) + 1 with 2^s >= d
+    uint32_t s = 0;
+    while ((1ull << s) < d) ++s;
+    ln.shift = 31 + s;
+    ln.magic = (uint32_t)((1ull << ln.shift) / d + 1);
+}
 
 // The span of sequence n that is attended: tokens [start, len); false for a slot without a sequence.
 __device__ __forceinline__ bool span_of(const AttnDecodeArgs &p, int n, int &s, int &start, int &len) {
     s = p.seq ? p.seq[n] : n;
     start = len = 0;
     if (s < 0 || s >= p.R) return false;
-    const long long cap = (long long)p.P * p.page_size;
-    long long x = p.lens[s];
-    x = x < 0 ? 0 : x > cap ? cap : x;
-    len = (int)x;
+    len = min(max(p.lens[s], 0), p.P * p.page_size);
     start = p.window > 0 && len > p.window ? len - p.window : 0;
     return true;
 }
 
-// A place on the line: tile t of the nt tiles of row hg of sequence n.
+// A place on the line: the tile of tokens [first, first + TILE) of block blk of KV head h of sequence n.
 template <int TILE> struct Place {
-    int n, hg, t, nt, start, len;
+    int n, h, blk, first, start, len;
     const int *pages;
     __device__ __forceinline__ void enter(const AttnDecodeArgs &p) {
         int s;
         span_of(p, n, s, start, len);
-        nt = (len - start + TILE - 1) / TILE;
-        pages = p.table + (size_t)(nt > 0 ? s : 0) * p.P;
+        pages = p.table + (len > start ? (size_t)s * p.P : 0);
+        first = start;
     }
-    __device__ __forceinline__ void next(const AttnDecodeArgs &p, int HG) {  // not past the line's end
-        if (++t < nt) return;
-        t = 0;
-        if (++hg < HG) return;
-        hg = 0;
+    __device__ __forceinline__ bool last() const { return first + TILE >= len; }
+    __device__ __forceinline__ void next(const AttnDecodeArgs &p, const Line &ln) {  // not past the line's end
+        first += TILE;
+        if (first < len) return;
+        first = start;
+        if (++blk < ln.nb) return;
+        blk = 0;
+        if (++h < p.Hk) return;
+        h = 0;
         do {
-            ++n;
-            if (n >= p.N) return;
+            if (++n >= p.N) return;
             enter(p);
-        } while (nt == 0);
+        } while (len == start);
     }
 };
 
-// The products of one warp's tile, bf16: rows of 16 query heads against 16 tokens.
+// The products of one warp's tile, bf16: rows of 16 query heads against 16 tokens. m is the largest q.k so far (of the
+// queries with the scale's sign), ms = m sc, p = 2^(q.k sc - ms) with sc = |scale| log2(e).
 template <int D, bool kPacked> struct Bf16Math {
     using T = __nv_bfloat16;
-    static constexpr int kTok = 16, kRows = kPacked ? 8 : 16, kRowBytes = 2 * D;
+    static constexpr int kTok = 16, kRows = kPacked ? 8 : 16, kRowBytes = 2 * D, kStats = kPacked ? 1 : 2, kPerSm = 2;
     uint32_t a[D / 16][4];
-    float o[D / 8][4], m[2], l[2];
+    float o[D / 8][4], m[kStats], ms[kStats], l[kStats];
     static __device__ __forceinline__ int swizzle(int row) { return row & 7; }
-    __device__ __forceinline__ void begin(const T *q, int heads, float *, int lane) {
+    __device__ __forceinline__ void begin(const T *q, int heads, float scale, float *, int lane) {
         const int g = lane >> 2, t = lane & 3;
+        const uint32_t sign = scale < 0.f ? 0x80008000u : 0u;
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks)
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
                 const int row = g + (x & 1) * 8, k = ks * 16 + (x >> 1) * 8 + 2 * t;
-                a[ks][x] = row < heads ? *reinterpret_cast<const uint32_t *>(q + (size_t)row * D + k) : 0u;
+                a[ks][x] = 0u;
+                if (!(kPacked && (x & 1)) && row < heads && scale != 0.f)
+                    a[ks][x] = *reinterpret_cast<const uint32_t *>(q + (size_t)row * D + k) ^ sign;
             }
 #pragma unroll
         for (int j = 0; j < D / 8; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
-        m[0] = m[1] = -INFINITY;
-        l[0] = l[1] = 0.f;
-    }
-    __device__ __forceinline__ void step(uint32_t sk, uint32_t sv, uint32_t on, float sc, const float *, float *, int lane) {
-        const int t = lane & 3, mi = lane >> 3, r = lane & 7;
-        float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-        {
-            const int tok = (mi >> 1) * 8 + r;
-            const uint32_t base = sk + tok * kRowBytes;
 #pragma unroll
-            for (int ks = 0; ks < D / 16; ++ks) {
-                uint32_t b[4];
-                ldsm4(base + (((2 * ks + (mi & 1)) ^ swizzle(tok)) << 4), b);
-                mma(s[0], a[ks], b[0], b[1]);
-                mma(s[1], a[ks], b[2], b[3]);
-            }
+        for (int h = 0; h < kStats; ++h) m[h] = -INFINITY, ms[h] = 0.f, l[h] = 0.f;
+    }
+    __device__ __forceinline__ void step(uint32_t stage, uint32_t on, float sc, const float *, float *, int lane) {
+        const int t = lane & 3, mi = lane >> 3, r = lane & 7;
+        // stages start at multiples of 256 bytes, so a chunk's place is an exclusive or away from the lane's first one
+        const uint32_t ka = stage + ((mi >> 1) * 8 + r) * kRowBytes + (((mi & 1) ^ r) << 4);
+        const uint32_t va = stage + kTok * kRowBytes + ((mi & 1) * 8 + r) * kRowBytes + (((mi >> 1) ^ r) << 4);
+        float s[2][4], s2[2][4];  // two chains of products: their latency, not their rate, would show
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) s[j][x] = s2[j][x] = 0.f;
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+            uint32_t b[4];
+            ldsm4(ka ^ (ks << 5), b);
+            mma(ks & 1 ? s2[0] : s[0], a[ks], b[0], b[1]);
+            mma(ks & 1 ? s2[1] : s[1], a[ks], b[2], b[3]);
         }
 #pragma unroll
         for (int j = 0; j < 2; ++j)
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                s[j][x] *= sc;
-                if (!(on >> (8 * j + 2 * t + (x & 1)) & 1)) s[j][x] = -INFINITY;
-            }
+            for (int x = 0; x < 2 * kStats; ++x) s[j][x] += s2[j][x];
+        if (on != 0xffffu) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int x = 0; x < 2 * kStats; ++x)
+                    if (!(on >> (8 * j + 2 * t + (x & 1)) & 1)) s[j][x] = -INFINITY;
+        }
         uint32_t hi[4], lo[4];
         float al[2];
 #pragma unroll
-        for (int h = 0; h < (kPacked ? 1 : 2); ++h) {
+        for (int h = 0; h < kStats; ++h) {
             float mx = fmaxf(fmaxf(s[0][2 * h], s[0][2 * h + 1]), fmaxf(s[1][2 * h], s[1][2 * h + 1]));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
             mx = fmaxf(mx, m[h]);
-            al[h] = pow2_rel(m[h], mx);
+            const float was = m[h] == -INFINITY ? -INFINITY : ms[h];
             m[h] = mx;
+            ms[h] = mx == -INFINITY ? 0.f : mx * sc;
+            al[h] = pow2(was - ms[h]);
             float pr[4];
 #pragma unroll
             for (int j = 0; j < 2; ++j)
 #pragma unroll
-                for (int x = 0; x < 2; ++x) pr[2 * j + x] = pow2_rel(s[j][2 * h + x], mx);
+                for (int x = 0; x < 2; ++x) pr[2 * j + x] = pow2(fmaf(s[j][2 * h + x], sc, -ms[h]));
             l[h] = l[h] * al[h] + ((pr[0] + pr[1]) + (pr[2] + pr[3]));
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
@@ -197,12 +228,10 @@ template <int D, bool kPacked> struct Bf16Math {
                 o[j][2] *= al[1], o[j][3] *= al[1];
             }
         }
-        const int tok = (mi & 1) * 8 + r;
-        const uint32_t base = sv + tok * kRowBytes;
 #pragma unroll
         for (int j = 0; j < D / 16; ++j) {
             uint32_t b[4];
-            ldsm4t(base + (((2 * j + (mi >> 1)) ^ swizzle(tok)) << 4), b);
+            ldsm4t(va ^ (j << 5), b);
             mma(o[2 * j], hi, b[0], b[1]);
             mma(o[2 * j + 1], hi, b[2], b[3]);
             if constexpr (!kPacked) {
@@ -211,15 +240,15 @@ template <int D, bool kPacked> struct Bf16Math {
             }
         }
     }
-    // The warp's statistics and columns [c0, c0 + D / 2) of its output, for the merge: wo [kRows][D / 2].
+    // The warp's statistics (m in units of log2), and half of its output's columns, for the merge: wo [kRows][D / 2].
     __device__ __forceinline__ void stats(float *wm, float *wl, int lane) {
         const int g = lane >> 2, t = lane & 3;
 #pragma unroll
-        for (int h = 0; h < (kPacked ? 1 : 2); ++h) {
+        for (int h = 0; h < kStats; ++h) {
             float x = l[h];
             x += __shfl_xor_sync(0xffffffffu, x, 1);
             x += __shfl_xor_sync(0xffffffffu, x, 2);
-            if (t == 0) wm[g + 8 * h] = m[h], wl[g + 8 * h] = x;
+            if (t == 0) wm[g + 8 * h] = m[h] == -INFINITY ? -INFINITY : ms[h], wl[g + 8 * h] = x;
         }
     }
     template <int HALF> __device__ __forceinline__ void put(float *wo, int lane) {
@@ -237,83 +266,118 @@ template <int D, bool kPacked> struct Bf16Math {
     }
 };
 
-// The products of one warp's tile, fp32: GB query heads against 8 tokens. Scores: four lanes of a token take 16-byte
-// chunks t, t + 4, ... of its row. Output: a lane owns four channels (d = 64: for every other token).
+// The products of one warp's tile, fp32: GB query heads against kTok tokens (4 KB of K). Scores: four lanes of a token
+// take 16-byte chunks t, t + 4, ... of its row, each lane one token of every eight. Output: a lane owns four channels
+// (d = 64: of every other token).
 template <int D, int GB> struct F32Math {
     using T = float;
-    static constexpr int kTok = 8, kRows = GB, kRowBytes = 4 * D;
-    static constexpr int kPer = (GB + 3) / 4;   // heads whose statistics a lane keeps: t, t + 4
-    static constexpr int kLanes = D / 4;        // lanes of an output row
+    static constexpr int kTok = 1024 / D, kRows = GB, kRowBytes = 4 * D, kPer = kTok / 8, kPerSm = GB <= 4 ? 3 : 2;
+    static constexpr int kHeads = (GB + 3) / 4;  // heads whose statistics a lane keeps: t, t + 4
+    static constexpr int kLanes = D / 4;         // lanes of an output row
     float4 o[GB];
-    float m[kPer], l[kPer];
+    float m[kHeads], ms[kHeads], l[kHeads];
     // rows 2 i and 2 i + 1 share a quarter-warp's access to four neighbouring chunks: bit 2 keeps them apart
     static __device__ __forceinline__ int swizzle(int row) { return ((row & 1) << 2) | ((row >> 1) & 3); }
-    __device__ __forceinline__ void begin(const T *q, int heads, float *sq, int) {
-        for (int x = threadIdx.x; x < GB * D; x += kThreads) sq[x] = x / D < heads ? q[x] : 0.f;
+    __device__ __forceinline__ void begin(const T *q, int heads, float scale, float *sq, int) {
+        const float sign = scale < 0.f ? -1.f : scale == 0.f ? 0.f : 1.f;
+        for (int x = threadIdx.x; x < GB * D; x += kThreads) sq[x] = x / D < heads && scale != 0.f ? sign * q[x] : 0.f;
 #pragma unroll
         for (int h = 0; h < GB; ++h) o[h] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) m[i] = -INFINITY, l[i] = 0.f;
+        for (int i = 0; i < kHeads; ++i) m[i] = -INFINITY, ms[i] = 0.f, l[i] = 0.f;
         __syncthreads();
     }
-    // sp: the warp's [GB][8] probabilities and [GB] factors
-    __device__ __forceinline__ void step(uint32_t sk, uint32_t sv, uint32_t on, float sc, const float *sq, float *sp, int lane) {
+    // sp: the warp's probabilities [kTok][GB] and factors [GB]
+    __device__ __forceinline__ void step(uint32_t stage, uint32_t on, float sc, const float *sq, float *sp, int lane) {
         const int g = lane >> 2, t = lane & 3;
-        const char *k = reinterpret_cast<const char *>(__cvta_shared_to_generic(sk)) + g * kRowBytes;
-        const char *v = reinterpret_cast<const char *>(__cvta_shared_to_generic(sv));
-        float s[GB];
+        const char *k = reinterpret_cast<const char *>(__cvta_shared_to_generic(stage)) + g * kRowBytes;
+        const char *v = reinterpret_cast<const char *>(__cvta_shared_to_generic(stage)) + kTok * kRowBytes;
+        float s[kPer][GB];
 #pragma unroll
-        for (int h = 0; h < GB; ++h) s[h] = 0.f;
+        for (int y = 0; y < kPer; ++y)
+#pragma unroll
+            for (int h = 0; h < GB; ++h) s[y][h] = 0.f;
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) {
-            const float4 kk = *reinterpret_cast<const float4 *>(k + (((t + 4 * i) ^ swizzle(g)) << 4));
+            float4 kk[kPer];
+#pragma unroll
+            for (int y = 0; y < kPer; ++y)
+                kk[y] = *reinterpret_cast<const float4 *>(k + y * 8 * kRowBytes + (((t + 4 * i) ^ swizzle(g)) << 4));
 #pragma unroll
             for (int h = 0; h < GB; ++h) {
                 const float4 qq = *reinterpret_cast<const float4 *>(sq + h * D + 4 * (t + 4 * i));
-                s[h] = fmaf(qq.x, kk.x, fmaf(qq.y, kk.y, fmaf(qq.z, kk.z, fmaf(qq.w, kk.w, s[h]))));
+#pragma unroll
+                for (int y = 0; y < kPer; ++y)
+                    s[y][h] = fmaf(qq.x, kk[y].x, fmaf(qq.y, kk[y].y, fmaf(qq.z, kk[y].z, fmaf(qq.w, kk[y].w, s[y][h]))));
             }
         }
 #pragma unroll
-        for (int h = 0; h < GB; ++h) {
-            s[h] += __shfl_xor_sync(0xffffffffu, s[h], 1);
-            s[h] += __shfl_xor_sync(0xffffffffu, s[h], 2);
-        }
-        const bool seen = on >> g & 1;
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            float x = -INFINITY;
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-                if (4 * i + c < GB && t == c) x = s[4 * i + c < GB ? 4 * i + c : 0] * sc;
-            if (!seen) x = -INFINITY;
-            float mx = x;
-#pragma unroll
-            for (int w = 4; w < 32; w <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
-            mx = fmaxf(mx, m[i]);
-            const float al = pow2_rel(m[i], mx), pr = pow2_rel(x, mx);
-            m[i] = mx;
-            l[i] = l[i] * al + pr;
-            if (4 * i + t < GB) {
-                sp[(4 * i + t) * 8 + g] = pr;
-                if (g == 0) sp[GB * 8 + 4 * i + t] = al;
-            }
-        }
-        __syncwarp();
-        const int c = lane % kLanes, sub = lane / kLanes;
-#pragma unroll
-        for (int h = 0; h < GB; ++h) {
-            const float al = sp[GB * 8 + h];
-            o[h].x *= al, o[h].y *= al, o[h].z *= al, o[h].w *= al;
-        }
-#pragma unroll
-        for (int i = 0; i < 8; i += 32 / kLanes) {
-            const int tok = i + sub;
-            const float4 vv = *reinterpret_cast<const float4 *>(v + tok * kRowBytes + ((c ^ swizzle(tok)) << 4));
+        for (int y = 0; y < kPer; ++y)
 #pragma unroll
             for (int h = 0; h < GB; ++h) {
-                const float pr = sp[h * 8 + tok];
-                o[h].x = fmaf(pr, vv.x, o[h].x), o[h].y = fmaf(pr, vv.y, o[h].y);
-                o[h].z = fmaf(pr, vv.z, o[h].z), o[h].w = fmaf(pr, vv.w, o[h].w);
+                s[y][h] += __shfl_xor_sync(0xffffffffu, s[y][h], 1);
+                s[y][h] += __shfl_xor_sync(0xffffffffu, s[y][h], 2);
+            }
+        bool moved = false;
+#pragma unroll
+        for (int i = 0; i < kHeads; ++i) {
+            float x[kPer];
+            float mx = m[i];
+#pragma unroll
+            for (int y = 0; y < kPer; ++y) {
+                x[y] = -INFINITY;
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    if (4 * i + c < GB && t == c) x[y] = s[y][4 * i + c < GB ? 4 * i + c : 0];
+                if (!(on >> (8 * y + g) & 1)) x[y] = -INFINITY;
+                mx = fmaxf(mx, x[y]);
+            }
+#pragma unroll
+            for (int w = 4; w < 32; w <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
+            const float was = m[i] == -INFINITY ? -INFINITY : ms[i];
+            m[i] = mx;
+            ms[i] = mx == -INFINITY ? 0.f : mx * sc;
+            const float al = pow2(was - ms[i]);
+            moved |= 4 * i + t < GB && al != 1.f;
+            l[i] *= al;
+#pragma unroll
+            for (int y = 0; y < kPer; ++y) {
+                const float pr = pow2(fmaf(x[y], sc, -ms[i]));
+                l[i] += pr;
+                if (4 * i + t < GB) sp[(8 * y + g) * GB + 4 * i + t] = pr;
+            }
+            if (4 * i + t < GB && g == 0) sp[kTok * GB + 4 * i + t] = al;
+        }
+        __syncwarp();
+        if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+            for (int h = 0; h < GB; ++h) {
+                const float al = sp[kTok * GB + h];
+                o[h].x *= al, o[h].y *= al, o[h].z *= al, o[h].w *= al;
+            }
+        }
+        const int c = lane % kLanes, sub = lane / kLanes;
+#pragma unroll
+        for (int i = 0; i < kTok; i += 32 / kLanes) {
+            const int tok = i + sub;
+            const float4 vv = *reinterpret_cast<const float4 *>(v + tok * kRowBytes + ((c ^ swizzle(tok & 7)) << 4));
+            float pr[GB];
+            if constexpr (GB == 1) {
+                pr[0] = sp[tok];
+            } else if constexpr (GB == 2) {
+                const float2 f = *reinterpret_cast<const float2 *>(sp + tok * 2);
+                pr[0] = f.x, pr[1] = f.y;
+            } else {
+#pragma unroll
+                for (int h = 0; h < GB; h += 4) {
+                    const float4 f = *reinterpret_cast<const float4 *>(sp + tok * GB + h);
+                    pr[h] = f.x, pr[h + 1] = f.y, pr[h + 2] = f.z, pr[h + 3] = f.w;
+                }
+            }
+#pragma unroll
+            for (int h = 0; h < GB; ++h) {
+                o[h].x = fmaf(pr[h], vv.x, o[h].x), o[h].y = fmaf(pr[h], vv.y, o[h].y);
+                o[h].z = fmaf(pr[h], vv.z, o[h].z), o[h].w = fmaf(pr[h], vv.w, o[h].w);
             }
         }
         __syncwarp();
@@ -321,11 +385,11 @@ template <int D, int GB> struct F32Math {
     __device__ __forceinline__ void stats(float *wm, float *wl, int lane) {
         const int g = lane >> 2, t = lane & 3;
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) {
+        for (int i = 0; i < kHeads; ++i) {
             float x = l[i];
 #pragma unroll
             for (int w = 4; w < 32; w <<= 1) x += __shfl_xor_sync(0xffffffffu, x, w);
-            if (g == 0 && 4 * i + t < GB) wm[4 * i + t] = m[i], wl[4 * i + t] = x;
+            if (g == 0 && 4 * i + t < GB) wm[4 * i + t] = m[i] == -INFINITY ? -INFINITY : ms[i], wl[4 * i + t] = x;
         }
         if constexpr (D == 64) {
 #pragma unroll
@@ -347,15 +411,15 @@ template <int D, int GB> struct F32Math {
 
 template <int D, typename M> struct Shared {
     static constexpr int kStage = 2 * M::kTok * M::kRowBytes, kStages = kRing / kStage;
-    alignas(128) uint8_t ring[kWarps][kStages][kStage];
-    float merge[kWarps][M::kRows][D / 2];
+    alignas(1024) uint8_t ring[kWarps][kStages][kStage];
+    alignas(16) float merge[kWarps][M::kRows][D / 2];
     float wm[kWarps][M::kRows], wl[kWarps][M::kRows];
     uint32_t on[kWarps][kStages];
-    float q[sizeof(typename M::T) == 4 ? M::kRows * D : 4];
-    float p[sizeof(typename M::T) == 4 ? kWarps : 1][sizeof(typename M::T) == 4 ? M::kRows * 9 : 1];
+    alignas(16) float q[sizeof(typename M::T) == 4 ? M::kRows * D : 4];
+    alignas(16) float p[sizeof(typename M::T) == 4 ? kWarps : 1][sizeof(typename M::T) == 4 ? M::kRows * (M::kTok + 4) : 4];
     long long scan[kWarps];
-    long long at;
-    int n0;
+    long long at[2];
+    int n0[2], nt0[2];
 };
 
 template <typename T> __device__ __forceinline__ void store_out(T *p, float4 v) { store4(p, v); }
@@ -396,14 +460,18 @@ __device__ __forceinline__ void merge_half(Shared<D, M> &sh, M &math, typename M
 }
 
 template <int D, typename M>
-__global__ void __launch_bounds__(kThreads, 2) attn_decode_kernel(AttnDecodeArgs p, Line ln, Partials w) {
+__global__ void __launch_bounds__(kThreads, M::kPerSm) attn_decode_kernel(AttnDecodeArgs p, Line ln, Partials w) {
     using T = typename M::T;
     using S = Shared<D, M>;
     constexpr int TILE = M::kTok * kWarps, CH = M::kRowBytes / 16;
-    extern __shared__ __align__(128) uint8_t raw[];
+    extern __shared__ __align__(1024) uint8_t raw[];
     S &sh = *reinterpret_cast<S *>(raw);
-    cudaTriggerProgrammaticLaunchCompletion();
+    follow();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    {  // the table's way to L2 overlaps that of the lengths, which say where in it a CTA begins
+        const size_t line = ((size_t)blockIdx.x * kThreads + tid) * 32;
+        if (line < (size_t)p.R * p.P) asm volatile("prefetch.global.L2 [%0];" ::"l"(p.table + line));
+    }
 
     // this CTA's run [begin, end) of the line: a prefix sum of the sequences' tiles, each thread a run of sequences
     const int per = (p.N + kThreads - 1) / kThreads;
@@ -413,7 +481,8 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode_kernel(AttnDecodeArgs
         int s, a, b;
         if (span_of(p, n, s, a, b)) mine += (b - a + TILE - 1) / TILE;
     }
-    mine *= ln.HG;
+    const int HG = p.Hk * ln.nb;  // rows of a sequence
+    mine *= HG;
     long long pre = mine;
 #pragma unroll
     for (int x = 1; x < 32; x <<= 1) {
@@ -430,74 +499,104 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode_kernel(AttnDecodeArgs
     }
     // (with fewer tiles than CTAs the first ones take one each: the join expects no empty CTA between two parts)
     const long long parts = min((long long)gridDim.x, total);
-    const long long begin = blockIdx.x < parts ? total * blockIdx.x / parts : total;
-    const long long end = blockIdx.x < parts ? total * (blockIdx.x + 1) / parts : total;
-    if (begin < end && begin < pre && begin >= pre - mine) {
-        long long at = pre - mine;
-        for (int n = na; n < ne; ++n) {
-            int s, a, b;
-            if (!span_of(p, n, s, a, b)) continue;
-            const long long nt = (long long)((b - a + TILE - 1) / TILE) * ln.HG;
-            if (begin < at + nt) {
-                sh.n0 = n;
-                sh.at = begin - at;
-                break;
+    long long edge[2];
+    edge[0] = blockIdx.x < parts ? total * blockIdx.x / parts : total;
+    edge[1] = blockIdx.x < parts ? total * (blockIdx.x + 1) / parts : total;
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+        if (edge[x] < total && edge[x] < pre && edge[x] >= pre - mine) {
+            long long at = pre - mine;
+            for (int n = na; n < ne; ++n) {
+                int s, a, b;
+                if (!span_of(p, n, s, a, b)) continue;
+                const int nt = (b - a + TILE - 1) / TILE;
+                if (edge[x] < at + (long long)nt * HG) {
+                    sh.n0[x] = n, sh.nt0[x] = nt, sh.at[x] = edge[x] - at;
+                    break;
+                }
+                at += (long long)nt * HG;
             }
-            at += nt;
         }
+        if (x == 0 && !ln.whole) break;  // the end of the run is looked up only to be moved
     }
-    // sequences with nothing to attend
+    // sequences with nothing to attend, and slots without a sequence
     for (int n = blockIdx.x; n < p.N; n += gridDim.x) {
         int s, a, b;
-        if (!span_of(p, n, s, a, b) || b > a) continue;
+        const bool any = span_of(p, n, s, a, b);
+        if (b > a) continue;
+        if (w.by_row)
+            for (int x = tid; x < HG; x += kThreads) w.cut[n * HG + x].x = -1;
+        if (!any) continue;
         for (int x = tid; x < p.Hq * D / 4; x += kThreads)
             store_out(static_cast<T *>(p.o) + (size_t)n * p.Hq * D + 4 * x, make_float4(0.f, 0.f, 0.f, 0.f));
         if (p.lse)
             for (int x = tid; x < p.Hq; x += kThreads) p.lse[(size_t)n * p.Hq + x] = -INFINITY;
     }
     __syncthreads();
+    int head_start = edge[0] < total ? (int)(sh.at[0] % sh.nt0[0]) : 0;  // tiles of its row before the run
+    if (ln.whole) {  // a row belongs to the run that its first tile lies in
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+            if (edge[x] < total) {
+                const int before = (int)(sh.at[x] % sh.nt0[x]);
+                if (before) edge[x] += sh.nt0[x] - before;
+            }
+    }
+    const long long begin = edge[0], end = edge[1];
     if (begin >= end) {
-        if (tid < 2) w.row[2 * blockIdx.x + tid] = -1;
+        if (tid == 0 && !ln.whole && !w.by_row) w.cut[blockIdx.x].x = -1;
         return;
     }
 
     Place<TILE> cur;
-    cur.n = sh.n0;
+    cur.n = sh.n0[0];
     cur.enter(p);
-    cur.hg = (int)(sh.at / cur.nt);
-    cur.t = (int)(sh.at - (long long)cur.hg * cur.nt);
+    {
+        const int hg = (int)(sh.at[0] / sh.nt0[0]);
+        cur.h = hg / ln.nb;
+        cur.blk = hg - cur.h * ln.nb;
+        cur.first = cur.start + head_start * TILE;
+        if (ln.whole && head_start) {
+            cur.first = cur.len - 1;  // past the row that belongs to the run before
+            cur.next(p, ln);
+            head_start = 0;
+        }
+    }
     Place<TILE> ahead = cur;
     long long xa = begin;  // the next tile to load
-    int page = 0;          // the page of this lane's token of that tile, fetched one tile early
+    int page = -1, off = 0;  // the page of this lane's token of that tile, fetched one tile early, and its place there
     auto fetch = [&]() {
         page = -1;
-        if (xa < end && lane < M::kTok) {
-            const int tok = ahead.start + ahead.t * TILE + warp * M::kTok + lane;
-            if (tok < ahead.len) page = __ldg(ahead.pages + tok / p.page_size);
+        const int tok = ahead.first + warp * M::kTok + lane;
+        if (xa < end && lane < M::kTok && tok < ahead.len) {
+            const uint32_t j = (uint32_t)((uint64_t)(uint32_t)tok * ln.magic >> ln.shift);
+            page = __ldg(ahead.pages + j);
+            off = tok - (int)j * p.page_size;
         }
     };
-    const T *kp = static_cast<const T *>(p.k_pages), *vp = static_cast<const T *>(p.v_pages);
+    // a lane copies chunk cl of rows r0, r0 + 32 / CH, ...: their places in a stage differ by constants
+    const int cl = lane % CH, r0 = lane / CH;
+    const uint8_t *kp = static_cast<const uint8_t *>(p.k_pages) + cl * 16, *vp = static_cast<const uint8_t *>(p.v_pages) + cl * 16;
+    const uint32_t ring = sptr(&sh.ring[warp][0][0]) + r0 * M::kRowBytes;
     auto issue = [&](int stage) {
         if (xa < end) {
-            const int tok = ahead.start + ahead.t * TILE + warp * M::kTok + lane;
             const bool on = page >= 0 && page < p.num_pages;
             const uint32_t mask = __ballot_sync(0xffffffffu, on);
             if (lane == 0) sh.on[warp][stage] = mask;
-            const int h = ahead.hg / ln.nb;
-            const long long row = on ? ((long long)page * p.Hk + h) * p.page_size + tok % p.page_size : 0;
-            const uint32_t dst = sptr(&sh.ring[warp][stage][0]);
+            const uint32_t row = on ? ((uint32_t)page * p.Hk + ahead.h) * p.page_size + off : 0u;  // below 2^32: checked
+            const uint32_t dst = ring + stage * S::kStage;
 #pragma unroll
             for (int i = 0; i < M::kTok * CH / 32; ++i) {
-                const int x = i * 32 + lane, r = x / CH, c = x % CH;
-                const long long rr = __shfl_sync(0xffffffffu, row, r);
+                constexpr int kStep = 32 / CH;
+                const int r = i * kStep + r0;
+                const uint32_t rr = __shfl_sync(0xffffffffu, row, r);
                 const int bytes = mask >> r & 1 ? 16 : 0;
-                const size_t off = (size_t)rr * D + c * (16 / sizeof(T));
-                const uint32_t d = dst + r * M::kRowBytes + ((c ^ M::swizzle(r)) << 4);
-                cp16(d, kp + off, bytes);
-                cp16(d + M::kTok * M::kRowBytes, vp + off, bytes);
+                const uint32_t d = dst + i * kStep * M::kRowBytes + ((cl ^ M::swizzle(r & 7)) << 4);
+                cp16(d, kp + (uint64_t)rr * M::kRowBytes, bytes);
+                cp16(d + M::kTok * M::kRowBytes, vp + (uint64_t)rr * M::kRowBytes, bytes);
             }
             ++xa;
-            if (xa < end) ahead.next(p, ln.HG);
+            if (xa < end) ahead.next(p, ln);
             fetch();
         }
         cp_commit();
@@ -507,29 +606,36 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode_kernel(AttnDecodeArgs
     for (int s = 0; s < S::kStages; ++s) issue(s);
 
     M math;
-    const float sc = p.scale * kLog2e;
-    int stage = 0, row0 = -1, row1 = -1, t0 = cur.t;
-    bool fresh = true;
+    const float sc = p.scale == 0.f ? 1.f : fabsf(p.scale) * kLog2e;
+    int stage = 0, heads = 0, j0 = 0;
+    int4 cut = make_int4(-1, 0, 0, 0);
+    bool fresh = true, head_of_row = false;
     for (long long x = begin; x < end; ++x) {
-        const int h = cur.hg / ln.nb, blk = cur.hg - h * ln.nb;
-        const int heads = min(ln.rows, ln.G - blk * ln.rows), j0 = h * ln.G + blk * ln.rows;
         if (fresh) {
-            math.begin(static_cast<const T *>(p.q) + ((size_t)cur.n * p.Hq + j0) * D, heads, sh.q, lane);
-            t0 = cur.t;
+            heads = min(ln.rows, ln.G - cur.blk * ln.rows);
+            j0 = cur.h * ln.G + cur.blk * ln.rows;
+            head_of_row = cur.first == cur.start;
+            math.begin(static_cast<const T *>(p.q) + ((size_t)cur.n * p.Hq + j0) * D, heads, p.scale, sh.q, lane);
             fresh = false;
         }
         cp_wait<S::kStages - 1>();
         __syncwarp();
-        const uint32_t sk = sptr(&sh.ring[warp][stage][0]);
-        math.step(sk, sk + M::kTok * M::kRowBytes, sh.on[warp][stage], sc, sh.q,
+        math.step(sptr(&sh.ring[warp][0][0]) + stage * S::kStage, sh.on[warp][stage], sc, sh.q,
                   sh.p[sizeof(T) == 4 ? warp : 0], lane);
         __syncwarp();
         issue(stage);
         if (++stage == S::kStages) stage = 0;
-        if (cur.t + 1 == cur.nt || x + 1 == end) {
-            const bool whole = t0 == 0 && cur.t + 1 == cur.nt;
-            const int slot = 2 * blockIdx.x + (t0 == 0);
-            if (!whole) (t0 == 0 ? row1 : row0) = cur.n * ln.HG + cur.hg;
+        if (cur.last() || x + 1 == end) {
+            const bool whole = head_of_row && cur.last();
+            const int slot = 2 * blockIdx.x + head_of_row;
+            const int row = (cur.n * p.Hk + cur.h) * ln.nb + cur.blk;
+            if (head_of_row && !whole && tid == 0) {
+                // the CTA that its last tile falls to: the smallest k with total (k + 1) / parts >= the row's end
+                const int done = (cur.first - cur.start) / TILE, nt = (cur.len - cur.start + TILE - 1) / TILE;
+                const long long e = (x - done + nt) * parts, k = (e + total - 1) / total - 1;
+                cut = make_int4(row, blockIdx.x, (int)(k - blockIdx.x) + 1, 0);
+            }
+            if (head_of_row && w.by_row && tid == 0) w.cut[row] = whole ? make_int4(-1, 0, 0, 0) : cut;
             T *o = static_cast<T *>(p.o) + ((size_t)cur.n * p.Hq + j0) * D;
             float *lse = p.lse ? p.lse + (size_t)cur.n * p.Hq + j0 : nullptr;
             float *part = w.o + (size_t)slot * kMaxRows * D, *ml = w.ml + (size_t)slot * kMaxRows * 2;
@@ -537,59 +643,71 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode_kernel(AttnDecodeArgs
             merge_half<D, M, 1>(sh, math, o, lse, heads, whole, part, ml, warp, lane);
             fresh = true;
         }
-        if (x + 1 < end) cur.next(p, ln.HG);
+        if (x + 1 < end) cur.next(p, ln);
     }
     cp_wait<0>();
-    if (tid == 0) {
-        w.row[2 * blockIdx.x] = row0;
-        w.row[2 * blockIdx.x + 1] = row1;
-    }
+    if (tid == 0 && !ln.whole && !w.by_row) w.cut[blockIdx.x] = cut;
 }
 
-// Joins the parts of the row that begins in CTA blockIdx.x of the line and goes on in the next ones; block y takes
-// one of its query heads. 256 threads: D / 4 lanes of four channels, 1024 / D groups that share the parts.
+// Joins the rows of the line that borders of CTAs cut: block (x, y) takes query heads y hb .. of entry x of their list;
+// the row's parts are the second slot of the CTA where it begins and the first slots of the CTAs that follow. D / 4
+// lanes of four channels for each of hb heads, the parts shared by the groups of lanes that remain.
+constexpr int kJoinThreads = 512;
+
 template <int D, typename T>
-__global__ void __launch_bounds__(256) attn_decode_join_kernel(AttnDecodeArgs p, Line ln, Partials w, int ctas) {
-    constexpr int LN = D / 4, NG = 256 / LN;
+__global__ void __launch_bounds__(kJoinThreads) attn_decode_join_kernel(AttnDecodeArgs p, Line ln, Partials w, int hb) {
+    constexpr int LN = D / 4, NG = kJoinThreads / LN;
     __shared__ float4 so[NG][LN];
     __shared__ float sm[NG], sl[NG];
-    __shared__ int last;
-    cudaGridDependencySynchronize();
-    const int c = blockIdx.x, head = blockIdx.y;
-    const int row = __ldcg(w.row + 2 * c + 1);
+    const int tid = threadIdx.x, lane = tid % LN, rest = tid / LN, grp = rest / hb, ng = NG / hb;
+    const int head = blockIdx.y * hb + rest - grp * hb;
+    follow();
+    const int4 cut = __ldcg(w.cut + blockIdx.x);
+    const int row = cut.x, c = cut.y, cnt = cut.z;
     if (row < 0) return;
-    const int n = row / ln.HG, hg = row - n * ln.HG, h = hg / ln.nb, blk = hg - h * ln.nb;
-    if (head >= min(ln.rows, ln.G - blk * ln.rows)) return;
-    // the parts: CTA c's second slot, then the first slots of the CTAs that follow with the same row
-    if (threadIdx.x == 0) last = ctas;
-    __syncthreads();
-    for (int k = c + 1 + threadIdx.x; k < ctas; k += 256)
-        if (__ldcg(w.row + 2 * k) != row) {
-            atomicMin(&last, k);
-            break;
-        }
-    __syncthreads();
-    const int cnt = last - c, lane = threadIdx.x % LN, grp = threadIdx.x / LN;
+    const int nh = row / ln.nb, blk = row - nh * ln.nb, n = nh / p.Hk, h = nh - n * p.Hk;
+    const bool on = head < min(ln.rows, ln.G - blk * ln.rows);
     float m = -INFINITY, l = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    auto add = [&](float m1, float l1, const float4 &o1) {
-        const float mx = fmaxf(m, m1), f = pow2_rel(m, mx), g = pow2_rel(m1, mx);
-        o.x = o.x * f + o1.x * g, o.y = o.y * f + o1.y * g, o.z = o.z * f + o1.z * g, o.w = o.w * f + o1.w * g;
-        l = l * f + l1 * g;
-        m = mx;
-    };
-#pragma unroll 4
-    for (int i = grp; i < cnt; i += NG) {
-        const size_t slot = (size_t)2 * (c + i) + (i == 0);
-        const float2 ml = __ldcg(reinterpret_cast<const float2 *>(w.ml + (slot * kMaxRows + head) * 2));
-        add(ml.x, ml.y, __ldcg(reinterpret_cast<const float4 *>(w.o + (slot * kMaxRows + head) * D + 4 * lane)));
-    }
-    so[grp][lane] = o;
-    if (lane == 0) sm[grp] = m, sl[grp] = l;
-    __syncthreads();
-    if (grp != 0) return;
+    for (int i0 = grp; on && i0 < cnt; i0 += 4 * ng) {
+        float2 ml[4];
+        float4 v[4];
 #pragma unroll
-    for (int g = 1; g < NG; ++g) add(sm[g], sl[g], so[g][lane]);
+        for (int u = 0; u < 4; ++u) {
+            const int i = i0 + u * ng;
+            const size_t at = ((size_t)2 * (c + i) + (i == 0)) * kMaxRows + head;
+            ml[u] = make_float2(-INFINITY, 0.f);
+            v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (i < cnt) {
+                ml[u] = __ldcg(reinterpret_cast<const float2 *>(w.ml) + at);
+                v[u] = __ldcg(reinterpret_cast<const float4 *>(w.o + at * D) + lane);
+            }
+        }
+        const float mx = fmaxf(fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x)), m), f = pow2_rel(m, mx);
+        o.x *= f, o.y *= f, o.z *= f, o.w *= f, l *= f;
+        m = mx;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const float g = pow2_rel(ml[u].x, mx);
+            o.x = fmaf(v[u].x, g, o.x), o.y = fmaf(v[u].y, g, o.y), o.z = fmaf(v[u].z, g, o.z), o.w = fmaf(v[u].w, g, o.w);
+            l = fmaf(ml[u].y, g, l);
+        }
+    }
+    so[rest][lane] = o;
+    if (lane == 0) sm[rest] = m, sl[rest] = l;
+    __syncthreads();
+    if (grp != 0 || !on) return;
+    const int parts = min(ng, cnt);
+    for (int g = 1; g < parts; ++g) m = fmaxf(m, sm[g * hb + rest]);
+    o = make_float4(0.f, 0.f, 0.f, 0.f);
+    l = 0.f;
+#pragma unroll 4
+    for (int g = 0; g < parts; ++g) {
+        const float f = pow2_rel(sm[g * hb + rest], m);
+        const float4 v = so[g * hb + rest][lane];
+        o.x = fmaf(v.x, f, o.x), o.y = fmaf(v.y, f, o.y), o.z = fmaf(v.z, f, o.z), o.w = fmaf(v.w, f, o.w);
+        l = fmaf(sl[g * hb + rest], f, l);
+    }
     const size_t j = (size_t)n * p.Hq + h * ln.G + blk * ln.rows + head;
     const float i = l == 0.f ? 0.f : 1.f / l;
     store_out(static_cast<T *>(p.o) + j * D + 4 * lane, make_float4(o.x * i, o.y * i, o.z * i, o.w * i));
@@ -600,26 +718,36 @@ template <int D, typename M> cudaError_t run(const AttnDecodeArgs &a, cudaStream
     using T = typename M::T;
     constexpr int TILE = M::kTok * kWarps;
     constexpr int smem = (int)sizeof(Shared<D, M>);
-    static_assert(smem <= 113 * 1024, "two CTAs on an SM");
+    static_assert(smem * M::kPerSm <= (227 - M::kPerSm) * 1024, "they fit an SM together");
+    constexpr int full = M::kPerSm * kAttnSms;
+    static Allowed allowed;
+    cudaError_t e = allowed(attn_decode_kernel<D, M>, smem);
+    if (e != cudaSuccess) return e;
     Line ln;
     ln.G = a.Hq / a.Hk;
     ln.rows = M::kRows;
     ln.nb = (ln.G + M::kRows - 1) / M::kRows;
-    ln.HG = a.Hk * ln.nb;
-    cudaError_t e = cudaFuncSetAttribute(attn_decode_kernel<D, M>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-    // no more CTAs than the largest possible line has tiles
+    set_divisor(ln, a.page_size);
+    // no more CTAs than the largest possible line has tiles, no more blocks to join than it has rows or borders
     long long span = (long long)a.P * a.page_size;
     if (a.window > 0 && a.window < span) span = a.window;
-    const long long tiles = (long long)a.N * ln.HG * ((span + TILE - 1) / TILE);
-    const int ctas = tiles < kCtas ? (int)tiles : kCtas;
-    const Partials w = partials(a.workspace, D);
-    GDR2_LAUNCH("attn_decode", st, (attn_decode_kernel<D, M><<<ctas, kThreads, smem, st>>>(a, ln, w)));
-    e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-    const int heads = ln.G < ln.rows ? ln.G : ln.rows;
+    const long long rows = (long long)a.N * a.Hk * ln.nb, each = (span + TILE - 1) / TILE, tiles = rows * each;
+    // short rows are left whole: there is nothing to join then, and a few tiles more or less make no CTA late
+    ln.whole = each <= kWholeTiles;
+    const long long most = ln.whole ? rows : tiles;
+    const int ctas = most < full ? (int)most : full;
+    Partials w = partials(a.workspace, D);
+    w.by_row = !ln.whole && rows < ctas;
+    GDR2_LAUNCH("attn_decode", st, e = launch(attn_decode_kernel<D, M>, dim3(ctas), dim3(kThreads), smem, 0, st, a, ln, w));
+    if (e != cudaSuccess || ln.whole || ctas == 1) return e;
+    const int entries = w.by_row ? (int)rows : ctas, heads = ln.G < ln.rows ? ln.G : ln.rows;
+    // few rows have many parts: a block for each head, all its groups on the parts. Many rows have few: one block a row.
+    int hb = 1;
+    if (entries * heads > kAttnSms)
+        while (hb < heads) hb *= 2;
     GDR2_LAUNCH("attn_decode_join", st,
-                e = launch_dependent(attn_decode_join_kernel<D, T>, dim3(ctas, heads), dim3(256), 0, st, a, ln, w, ctas));
+                e = launch(attn_decode_join_kernel<D, T>, dim3(entries, (heads + hb - 1) / hb), dim3(kJoinThreads), 0, 0, st,
+                           a, ln, w, hb));
     return e;
 }
 
@@ -635,7 +763,7 @@ template <int D> cudaError_t dispatch(const AttnDecodeArgs &a, cudaStream_t st) 
 }  // namespace
 
 size_t attn_decode_workspace_bytes(int d) {
-    return (partial_floats(d) + (size_t)kCtas * 2 * kMaxRows * 2) * sizeof(float) + (size_t)kCtas * 2 * sizeof(int);
+    return (partial_floats(d) + (size_t)kMaxCtas * 2 * kMaxRows * 2) * sizeof(float) + (size_t)kMaxCtas * sizeof(int4);
 }
 
 cudaError_t launch_attn_decode(const AttnDecodeArgs &a, cudaStream_t st) {

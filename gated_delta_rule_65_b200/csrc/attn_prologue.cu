@@ -194,6 +194,7 @@ __global__ void __launch_bounds__(kThreads, kFwdCtas) attn_prologue_fwd_kernel(A
     const int step = un.parts * Y::kRows;
     const int tq = (p.Hq + step - 1) / step, tk = (p.Hk + step - 1) / step;
     int u = blockIdx.x * kWarps + warp;
+    follow();
 
     // the ring: what this lane fetches next is row `src` (head ha of ea) of tensor seg of unit ua, `left` rows of it
     // remaining, its own the first of each step
@@ -348,7 +349,6 @@ __global__ void __launch_bounds__(kThreads, kBwdCtas) attn_prologue_bwd_kernel(A
     constexpr int N = Y::kPairs;
     extern __shared__ __align__(16) uint8_t raw[];
     BwdShared<D> &sh = *reinterpret_cast<BwdShared<D> *>(raw);
-    cudaTriggerProgrammaticLaunchCompletion();
     const bool keys = blockIdx.x >= cq;
     const Units un = keys ? uk : uq;
     const T *x = static_cast<const T *>(keys ? p.xk : p.xq), *dy = static_cast<const T *>(keys ? p.dk : p.dq);
@@ -359,6 +359,7 @@ __global__ void __launch_bounds__(kThreads, kBwdCtas) attn_prologue_bwd_kernel(A
     const Slot<D, T, kInter> w(l, p.rot);
     const int step = un.parts * Y::kRows, rows = (H + step - 1) / step;
     int u = (blockIdx.x - (keys ? cq : 0)) * kWarps + warp;
+    follow();
     int ua = u, left = 0, ha = 0;  // as in the forward: the row this lane fetches next
     const T *sd = nullptr, *sr = nullptr;
     auto enter = [&]() {
@@ -490,7 +491,7 @@ __global__ void __launch_bounds__(1024) attn_prologue_reduce_kernel(const float 
     __shared__ float red[32][33];
     const int which = blockIdx.x, c = blockIdx.y * 32 + threadIdx.x % 32, sl = threadIdx.x / 32;
     float *out = which ? dgk : dgq;
-    cudaGridDependencySynchronize();
+    follow();
     if (out == nullptr) return;
     const int a = which ? cq : 0, e = which ? ctas : cq;
     float v = 0.f;
@@ -517,28 +518,26 @@ Units split_units(int T, int most, int rows, int warps, int fill) {
     return un;
 }
 
-template <typename K> cudaError_t allow_shared(K *kernel, size_t bytes) {
-    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-}
-
 template <int D, typename T, bool kInter, bool kCache>
 cudaError_t run_fwd(const AttnPrologueArgs &a, cudaStream_t st) {
     constexpr int smem = sizeof(FwdShared<D>), full = kFwdCtas * kAttnSms;
     const auto kernel = attn_prologue_fwd_kernel<D, T, kInter, kCache>;
-    cudaError_t e = allow_shared(kernel, smem);
+    static Allowed allowed;
+    cudaError_t e = allowed(kernel, smem);
     if (e != cudaSuccess) return e;
     Units un = split_units(a.T, a.Hq > a.Hk ? a.Hq : a.Hk, Layout<D, T>::kRows, full * kWarps, 2);
     const int need = (int)(((long long)un.count + kWarps - 1) / kWarps), grid = need < full ? need : full;
     un.stride = grid * kWarps;
-    GDR2_LAUNCH(kCache ? "attn_prologue_cache" : "attn_prologue_fwd", st, (kernel<<<grid, kThreads, smem, st>>>(a, un)));
-    return cudaGetLastError();
+    GDR2_LAUNCH(kCache ? "attn_prologue_cache" : "attn_prologue_fwd", st, e = launch(kernel, dim3(grid), dim3(kThreads), smem, 0, st, a, un));
+    return e;
 }
 
 template <int D, typename T, bool kInter>
 cudaError_t run_bwd(const AttnPrologueArgs &a, cudaStream_t st) {
     constexpr int smem = sizeof(BwdShared<D>);
     const auto kernel = attn_prologue_bwd_kernel<D, T, kInter>;
-    cudaError_t e = allow_shared(kernel, smem);
+    static Allowed allowed;
+    cudaError_t e = allowed(kernel, smem);
     if (e != cudaSuccess) return e;
     // CTAs in proportion to the heads, at least one each
     const long long heads = (long long)a.Hq + a.Hk;
@@ -554,11 +553,10 @@ cudaError_t run_bwd(const AttnPrologueArgs &a, cudaStream_t st) {
     };
     const Units uq = part(a.Hq, cq), uk = part(a.Hk, ck);
     float *partial = a.dgq || a.dgk ? static_cast<float *>(a.workspace) : nullptr;
-    GDR2_LAUNCH("attn_prologue_bwd", st, (kernel<<<cq + ck, kThreads, smem, st>>>(a, uq, uk, cq, partial)));
-    e = cudaGetLastError();
+    GDR2_LAUNCH("attn_prologue_bwd", st, e = launch(kernel, dim3(cq + ck), dim3(kThreads), smem, 0, st, a, uq, uk, cq, partial));
     if (e != cudaSuccess || partial == nullptr) return e;
     GDR2_LAUNCH("attn_prologue_reduce", st,
-                e = launch_dependent(attn_prologue_reduce_kernel<D>, dim3(2, D / 32), dim3(1024), 0, st,
+                e = launch(attn_prologue_reduce_kernel<D>, dim3(2, D / 32), dim3(1024), 0, 0, st,
                                      (const float *)partial, cq, cq + ck, a.dgq, a.dgk));
     return e;
 }
