@@ -47,7 +47,7 @@ struct AttnDecodeArgs {
     int N, Hq, Hk, d, R, P, page_size, num_pages, dtype;
     void *workspace;
 };
-size_t attn_decode_workspace_bytes(int d);
+size_t attn_decode_workspace_bytes(const AttnDecodeArgs &a);  // of the sizes in it; 0 where nothing is cut
 cudaError_t launch_attn_decode(const AttnDecodeArgs &a, cudaStream_t st);
 
 struct KvPagesArgs {

@@ -48,6 +48,18 @@ int check_pages(int R, int P, int page_size, int num_pages) {
     return GDR2_OK;
 }
 
+int check_decode(const gdr2::AttnDecodeArgs &a, int R) {
+    int st = check_heads(a.Hq, a.Hk, a.d, a.dtype);
+    if (st == GDR2_OK) st = check_pages(R, a.P, a.page_size, a.num_pages);
+    if (st != GDR2_OK) return st;
+    if (a.N <= 0 || a.Hq % a.Hk != 0 || a.window < 0) return GDR2_ERR_INVALID_ARG;
+    // rows of the work and token rows of the pool are counted in 32 bits
+    if ((long long)a.N * a.Hq > 0x7fffffffLL || (long long)a.Hk * a.page_size > 0x7fffffffLL ||
+        (long long)a.Hk * a.page_size * a.num_pages > 0xffffffffLL)
+        return GDR2_ERR_UNSUPPORTED;
+    return GDR2_OK;
+}
+
 // The copies of kv_fork and kv_compact count 4 KB pieces of a page's heads in 32 bits.
 bool copies_fit(int Hk, int page_size, int d, int num_pages, int dtype) {
     const long long pieces = ((long long)page_size * d * (dtype == GDR2_BF16 ? 2 : 4) + 4095) / 4096;
@@ -150,29 +162,30 @@ int gdr2_attn_prologue_cache(const void *xq, const void *xk, const void *xv, con
     return done(gdr2::launch_attn_prologue_cache(a, (cudaStream_t)stream));
 }
 
-size_t gdr2_attn_decode_workspace_bytes(int d) { return d == 64 || d == 128 ? gdr2::attn_decode_workspace_bytes(d) : 0; }
+size_t gdr2_attn_decode_workspace_bytes(int N, int Hq, int Hk, int d, int P, int page_size, int window, int dtype) {
+    gdr2::AttnDecodeArgs a{};
+    a.N = N; a.Hq = Hq; a.Hk = Hk; a.d = d; a.P = P; a.page_size = page_size; a.num_pages = 1; a.window = window;
+    a.dtype = dtype;
+    return check_decode(a, N) == GDR2_OK ? gdr2::attn_decode_workspace_bytes(a) : 0;
+}
 
 int gdr2_attn_decode(const void *q, const void *k_pages, const void *v_pages, const int *table, const int *lens,
                      const int *seq, float scale, int window, void *o, float *lse, int N, int Hq, int Hk, int d, int R,
                      int P, int page_size, int num_pages, int dtype, void *workspace, size_t workspace_bytes,
                      void *stream) {
-    int st = check_heads(Hq, Hk, d, dtype);
-    if (st == GDR2_OK) st = check_pages(R, P, page_size, num_pages);
-    if (st != GDR2_OK) return st;
-    if (N <= 0 || Hq % Hk != 0 || window < 0 || (seq == nullptr && N > R)) return GDR2_ERR_INVALID_ARG;
-    // rows of the work and token rows of the pool are counted in 32 bits
-    if ((long long)N * Hq > 0x7fffffffLL || (long long)Hk * page_size > 0x7fffffffLL ||
-        (long long)Hk * page_size * num_pages > 0xffffffffLL)
-        return GDR2_ERR_UNSUPPORTED;
-    if (!ok_ptr(q) || !ok_ptr(k_pages) || !ok_ptr(v_pages) || !ok_num(table) || !ok_num(lens) || !opt_num(seq) ||
-        !ok_ptr(o) || !opt_num(lse))
-        return GDR2_ERR_INVALID_ARG;
-    if (!ok_ptr(workspace) || workspace_bytes < gdr2::attn_decode_workspace_bytes(d)) return GDR2_ERR_WORKSPACE;
     gdr2::AttnDecodeArgs a{};
     a.q = q; a.k_pages = k_pages; a.v_pages = v_pages; a.table = table; a.lens = lens; a.seq = seq;
     a.scale = scale; a.window = window; a.o = o; a.lse = lse;
     a.N = N; a.Hq = Hq; a.Hk = Hk; a.d = d; a.R = R; a.P = P; a.page_size = page_size; a.num_pages = num_pages;
     a.dtype = dtype; a.workspace = workspace;
+    const int st = check_decode(a, R);
+    if (st != GDR2_OK) return st;
+    if (seq == nullptr && N > R) return GDR2_ERR_INVALID_ARG;
+    if (!ok_ptr(q) || !ok_ptr(k_pages) || !ok_ptr(v_pages) || !ok_num(table) || !ok_num(lens) || !opt_num(seq) ||
+        !ok_ptr(o) || !opt_num(lse))
+        return GDR2_ERR_INVALID_ARG;
+    const size_t need = gdr2::attn_decode_workspace_bytes(a);
+    if (need > 0 && (!ok_ptr(workspace) || workspace_bytes < need)) return GDR2_ERR_WORKSPACE;
     return done(gdr2::launch_attn_decode(a, (cudaStream_t)stream));
 }
 

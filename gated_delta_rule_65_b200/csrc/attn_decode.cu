@@ -714,28 +714,42 @@ __global__ void __launch_bounds__(kJoinThreads) attn_decode_join_kernel(AttnDeco
     if (lane == 0 && p.lse) p.lse[j] = (m + log2f(l)) * kLn2;
 }
 
+// How a call's line is cut: from its sizes alone, so that a workspace query and the call agree.
+struct Plan {
+    Line ln;
+    long long rows;
+    int ctas;
+};
+template <int D, typename M> Plan plan(const AttnDecodeArgs &a) {
+    constexpr int TILE = M::kTok * kWarps, full = M::kPerSm * kAttnSms;
+    Plan p;
+    p.ln.G = a.Hq / a.Hk;
+    p.ln.rows = M::kRows;
+    p.ln.nb = (p.ln.G + M::kRows - 1) / M::kRows;
+    set_divisor(p.ln, a.page_size);
+    // no more CTAs than the largest possible line has tiles, or rows if they stay whole: short ones do, as there is
+    // nothing to join then, and a few tiles more or less make no CTA late
+    long long span = (long long)a.P * a.page_size;
+    if (a.window > 0 && a.window < span) span = a.window;
+    const long long each = (span + TILE - 1) / TILE;
+    p.rows = (long long)a.N * a.Hk * p.ln.nb;
+    p.ln.whole = each <= kWholeTiles;
+    const long long most = p.ln.whole ? p.rows : p.rows * each;
+    p.ctas = most < full ? (int)most : full;
+    return p;
+}
+
 template <int D, typename M> cudaError_t run(const AttnDecodeArgs &a, cudaStream_t st) {
     using T = typename M::T;
-    constexpr int TILE = M::kTok * kWarps;
     constexpr int smem = (int)sizeof(Shared<D, M>);
     static_assert(smem * M::kPerSm <= (227 - M::kPerSm) * 1024, "they fit an SM together");
-    constexpr int full = M::kPerSm * kAttnSms;
     static Allowed allowed;
     cudaError_t e = allowed(attn_decode_kernel<D, M>, smem);
     if (e != cudaSuccess) return e;
-    Line ln;
-    ln.G = a.Hq / a.Hk;
-    ln.rows = M::kRows;
-    ln.nb = (ln.G + M::kRows - 1) / M::kRows;
-    set_divisor(ln, a.page_size);
-    // no more CTAs than the largest possible line has tiles, no more blocks to join than it has rows or borders
-    long long span = (long long)a.P * a.page_size;
-    if (a.window > 0 && a.window < span) span = a.window;
-    const long long rows = (long long)a.N * a.Hk * ln.nb, each = (span + TILE - 1) / TILE, tiles = rows * each;
-    // short rows are left whole: there is nothing to join then, and a few tiles more or less make no CTA late
-    ln.whole = each <= kWholeTiles;
-    const long long most = ln.whole ? rows : tiles;
-    const int ctas = most < full ? (int)most : full;
+    const Plan pl = plan<D, M>(a);
+    const Line ln = pl.ln;
+    const long long rows = pl.rows;
+    const int ctas = pl.ctas;
     Partials w = partials(a.workspace, D);
     w.by_row = !ln.whole && rows < ctas;
     GDR2_LAUNCH("attn_decode", st, e = launch(attn_decode_kernel<D, M>, dim3(ctas), dim3(kThreads), smem, 0, st, a, ln, w));
@@ -751,23 +765,38 @@ template <int D, typename M> cudaError_t run(const AttnDecodeArgs &a, cudaStream
     return e;
 }
 
-template <int D> cudaError_t dispatch(const AttnDecodeArgs &a, cudaStream_t st) {
+// f.template operator()<D, Math>() for the call's types and heads
+template <int D, typename F> auto dispatch(const AttnDecodeArgs &a, F f) {
     const int G = a.Hq / a.Hk;
-    if (a.dtype == 1) return G <= 8 ? run<D, Bf16Math<D, true>>(a, st) : run<D, Bf16Math<D, false>>(a, st);
-    if (G == 1) return run<D, F32Math<D, 1>>(a, st);
-    if (G == 2) return run<D, F32Math<D, 2>>(a, st);
-    if (G <= 4) return run<D, F32Math<D, 4>>(a, st);
-    return run<D, F32Math<D, 8>>(a, st);
+    if (a.dtype == 1) return G <= 8 ? f.template operator()<D, Bf16Math<D, true>>() : f.template operator()<D, Bf16Math<D, false>>();
+    if (G == 1) return f.template operator()<D, F32Math<D, 1>>();
+    if (G == 2) return f.template operator()<D, F32Math<D, 2>>();
+    if (G <= 4) return f.template operator()<D, F32Math<D, 4>>();
+    return f.template operator()<D, F32Math<D, 8>>();
 }
+
+struct Run {
+    const AttnDecodeArgs &a;
+    cudaStream_t st;
+    template <int D, typename M> cudaError_t operator()() const { return run<D, M>(a, st); }
+};
+struct Bytes {
+    const AttnDecodeArgs &a;
+    template <int D, typename M> size_t operator()() const {
+        return plan<D, M>(a).ln.whole ? 0
+                                      : (partial_floats(D) + (size_t)kMaxCtas * 2 * kMaxRows * 2) * sizeof(float) +
+                                            (size_t)kMaxCtas * sizeof(int4);
+    }
+};
 
 }  // namespace
 
-size_t attn_decode_workspace_bytes(int d) {
-    return (partial_floats(d) + (size_t)kMaxCtas * 2 * kMaxRows * 2) * sizeof(float) + (size_t)kMaxCtas * sizeof(int4);
+size_t attn_decode_workspace_bytes(const AttnDecodeArgs &a) {
+    return a.d == 128 ? dispatch<128>(a, Bytes{a}) : dispatch<64>(a, Bytes{a});
 }
 
 cudaError_t launch_attn_decode(const AttnDecodeArgs &a, cudaStream_t st) {
-    return a.d == 128 ? dispatch<128>(a, st) : dispatch<64>(a, st);
+    return a.d == 128 ? dispatch<128>(a, Run{a, st}) : dispatch<64>(a, Run{a, st});
 }
 
 }  // namespace gdr2

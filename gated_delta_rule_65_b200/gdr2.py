@@ -128,7 +128,7 @@ def lib(build_if_missing: bool = True) -> ctypes.CDLL:
             L.gdr2_attn_prologue_cache.argtypes = ([_VP] * 5 + [_I, _F, _VP, _VP, _VP, _F, _I, _I] + [_VP] * 4 +
                                                    [_I] * 9 + [_LL] * 3 + [_VP])
             L.gdr2_attn_decode_workspace_bytes.restype = ctypes.c_size_t
-            L.gdr2_attn_decode_workspace_bytes.argtypes = [_I]
+            L.gdr2_attn_decode_workspace_bytes.argtypes = [_I] * 8
             L.gdr2_attn_decode.restype = _I
             L.gdr2_attn_decode.argtypes = ([_VP] * 6 + [_F, _I, _VP, _VP] + [_I] * 9 + [_VP, ctypes.c_size_t, _VP])
             L.gdr2_kv_workspace_bytes.restype = ctypes.c_size_t
@@ -489,8 +489,9 @@ ROPE_PLAIN, ROPE_LINEAR, ROPE_BASE, ROPE_PARTS = range(4)
 _ROPE = {"none": ROPE_PLAIN, "linear": ROPE_LINEAR, "base": ROPE_BASE, "parts": ROPE_PARTS}
 
 
-# A decode step makes several of these calls a layer, and a call's kernels take a few microseconds: the helpers below
-# look at each tensor once, without intermediate objects.
+# A decode step makes several of these calls a layer, and a call's kernels take a few microseconds. So each binding
+# below tests its arguments in one expression and names the fault (through the helpers that raise) only when it fails.
+_I32, _F32, _F64 = torch.int32, torch.float32, torch.float64
 
 
 def _shaped(name, t, shape, dtype):
@@ -507,24 +508,27 @@ def _shaped(name, t, shape, dtype):
 def _token_rows(name, x, dtype):
     """Token rows [T, H, d] or [B, T, H, d] with contiguous heads and channels and one stride from token to token
     (a view of a fused projection may have a larger one): (tokens, heads, channels, stride in elements)."""
-    shape, strides = x.shape, x.stride()
-    if len(shape) == 3:
-        T, H, d = shape
-        step = strides[0]
-    elif len(shape) == 4:
-        B, n, H, d = shape
-        T = B * n
-        if B > 1 and n > 1 and strides[0] != n * strides[1]:
-            raise ValueError(f"gdr2: the tokens of {name} must have one stride across the batch")
-        step = strides[1] if n > 1 else strides[0]
-    else:
-        raise ValueError(f"gdr2: {name} must be [T, H, d] or [B, T, H, d]")
     if x.dtype is not dtype:
         raise TypeError(f"gdr2: {name} is {x.dtype}, not {dtype}")
+    shape = x.shape
+    if len(shape) == 3:
+        T, H, d = shape
+    elif len(shape) == 4:
+        T, H, d = shape[0] * shape[1], shape[2], shape[3]
+    else:
+        raise ValueError(f"gdr2: {name} must be [T, H, d] or [B, T, H, d]")
     if T * H * d == 0:
         raise ValueError(f"gdr2: {name} is empty")
+    if x.is_contiguous():
+        return T, H, d, H * d
+    strides = x.stride()
     if (d > 1 and strides[-1] != 1) or (H > 1 and strides[-2] != d):
         raise ValueError(f"gdr2: heads and channels of {name} must be contiguous")
+    step = strides[0]
+    if len(shape) == 4 and shape[1] > 1:
+        step = strides[1]
+        if shape[0] > 1 and strides[0] != shape[1] * step:
+            raise ValueError(f"gdr2: the tokens of {name} must have one stride across the batch")
     return T, H, d, step if T > 1 else H * d
 
 
@@ -545,12 +549,13 @@ def _p(t):
     return None if t is None else t.data_ptr()
 
 
-def _kept(t, stream):
-    """A fresh tensor that an explicit stream is about to use: its memory is not handed out again before that stream
+def _keep(stream, *tensors):
+    """Fresh tensors that an explicit stream is about to use: their memory is not handed out again before that stream
     has passed the call."""
-    if stream is not None:
-        t.record_stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream)))
-    return t
+    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
+    for t in tensors:
+        if t is not None:
+            t.record_stream(s)
 
 
 def _raw_stream(stream, index):
@@ -559,23 +564,25 @@ def _raw_stream(stream, index):
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
-def _workspace(workspace, need, like, stream):
-    if workspace is None:
-        return _kept(like.new_empty(need, dtype=torch.uint8), stream), need
-    if workspace.get_device() != like.get_device() or not workspace.is_contiguous():
-        raise ValueError("gdr2: the workspace must be contiguous and on the tensors' device")
-    return workspace, workspace.numel() * workspace.element_size()
-
-
 _sizes = {}
 
 
-def _bytes(name, *args):
-    """A workspace query's answer, at least 16 bytes; it depends on its arguments alone."""
+def _scratch(like, workspace, stream, name, *args):
+    """(workspace or None, its bytes): the one given, or a fresh one of the size that the query `name` gives for these
+    arguments (it depends on them alone); None where the call needs none."""
+    if workspace is not None:
+        if workspace.get_device() != like.get_device() or not workspace.is_contiguous():
+            raise ValueError("gdr2: the workspace must be contiguous and on the tensors' device")
+        return workspace, workspace.numel() * workspace.element_size()
     n = _sizes.get((name, args))
     if n is None:
-        n = _sizes[(name, args)] = max(16, int(getattr(lib(), name)(*args)))
-    return n
+        n = _sizes[(name, args)] = int(getattr(lib(), name)(*args))
+    if n == 0:
+        return None, 0
+    workspace = like.new_empty(-(-n // like.element_size()))
+    if stream is not None:
+        _keep(stream, workspace)
+    return workspace, n
 
 
 def rope_freqs(rot, base=10000.0, *, scaling="none", factor=1.0, orig_len=0, turns_low=1.0, turns_high=32.0,
@@ -593,25 +600,23 @@ def rope_freqs(rot, base=10000.0, *, scaling="none", factor=1.0, orig_len=0, tur
 
 
 def _prologue_checks(xq, xk, gq, gk, pos, freqs, norm):
+    dtype = xq.dtype
     dt = _dtype_code(xq)
-    T, Hq, d, sq = _token_rows("xq", xq, xq.dtype)
-    Tk, Hk, dk, sk = _token_rows("xk", xk, xq.dtype)
+    T, Hq, d, sq = _token_rows("xq", xq, dtype)
+    Tk, Hk, dk, sk = _token_rows("xk", xk, dtype)
     if Tk != T or dk != d:
         raise ValueError("gdr2: xq and xk must have the same tokens and channels")
-    if gq is not None:
-        _shaped("gq", gq, (d,), torch.float32)
-    if gk is not None:
-        _shaped("gk", gk, (d,), torch.float32)
-    if not norm and (gq is not None or gk is not None):
-        raise ValueError("gdr2: gq and gk are gains of the norm; pass None without it")
-    rot = 0
-    if freqs is not None:
-        if freqs.dtype is not torch.float64 or freqs.dim() != 1 or not freqs.is_contiguous():
-            raise TypeError("gdr2: freqs must be a contiguous 1-D float64 tensor")
-        if pos is None or pos.dtype is not torch.int32 or pos.numel() != T or not pos.is_contiguous():
-            raise ValueError("gdr2: pos must hold one int32 position for each token")
-        rot = 2 * freqs.shape[0]
-    return T, Hq, Hk, d, sq, sk, dt, rot
+    for name, g in (("gq", gq), ("gk", gk)):
+        if g is not None and not (g.shape == (d,) and g.dtype is _F32 and g.is_contiguous() and norm):
+            _shaped(name, g, (d,), _F32)
+            raise ValueError("gdr2: gq and gk are gains of the norm; pass None without it")
+    if freqs is None:
+        return T, Hq, Hk, d, sq, sk, dt, 0
+    if freqs.dtype is not _F64 or freqs.dim() != 1 or not freqs.is_contiguous():
+        raise TypeError("gdr2: freqs must be a contiguous 1-D float64 tensor")
+    if pos is None or pos.dtype is not _I32 or pos.numel() != T or not pos.is_contiguous():
+        raise ValueError("gdr2: pos must hold one int32 position for each token")
+    return T, Hq, Hk, d, sq, sk, dt, 2 * freqs.shape[0]
 
 
 def attn_prologue_fwd(xq, xk, gq=None, gk=None, pos=None, freqs=None, *, norm=True, eps=1e-6, mag=1.0,
@@ -622,15 +627,18 @@ def attn_prologue_fwd(xq, xk, gq=None, gk=None, pos=None, freqs=None, *, norm=Tr
     T, Hq, Hk, d, sq, sk, dt, rot = _prologue_checks(xq, xk, gq, gk, pos, freqs, norm)
     if out is None:
         index = _device(xq, xk, gq, gk, pos, freqs)
-        out = {"q": _kept(xq.new_empty(xq.shape), stream), "k": _kept(xk.new_empty(xk.shape), stream)}
+        q, k = xq.new_empty(xq.shape), xk.new_empty(xk.shape)
+        out = {"q": q, "k": k}
+        if stream is not None:
+            _keep(stream, q, k)
     else:
-        _shaped("q", out["q"], xq.shape, xq.dtype), _shaped("k", out["k"], xk.shape, xq.dtype)
-        index = _device(xq, xk, gq, gk, pos, freqs, out["q"], out["k"])
+        q, k = _shaped("q", out["q"], xq.shape, xq.dtype), _shaped("k", out["k"], xk.shape, xq.dtype)
+        index = _device(xq, xk, gq, gk, pos, freqs, q, k)
     st = (_lib or lib()).gdr2_attn_prologue_fwd(
         xq.data_ptr(), xk.data_ptr(), _p(gq), _p(gk), 1 if norm else 0, eps, _p(pos), _p(freqs), mag, rot,
-        1 if interleaved else 0, out["q"].data_ptr(), out["k"].data_ptr(), T, Hq, Hk, d, dt, sq, sk,
-        _raw_stream(stream, index))
-    _check("gdr2_attn_prologue_fwd", st)
+        1 if interleaved else 0, q.data_ptr(), k.data_ptr(), T, Hq, Hk, d, dt, sq, sk, _raw_stream(stream, index))
+    if st != OK:
+        raise GDR2Error("gdr2_attn_prologue_fwd", st)
     return out
 
 
@@ -640,33 +648,40 @@ def attn_prologue_bwd(xq, xk, gq, gk, pos, freqs, dq, dk, *, norm=True, eps=1e-6
     None too, as the gradient of a gain of ones). `out` may hold dxq, dxk as views of one fused gradient, and may
     leave dgq, dgk out or None when they are not wanted."""
     T, Hq, Hk, d, sq, sk, dt, rot = _prologue_checks(xq, xk, gq, gk, pos, freqs, norm)
-    _shaped("dq", dq, xq.shape, xq.dtype), _shaped("dk", dk, xk.shape, xq.dtype)
+    dtype = xq.dtype
+    if not (dq.shape == xq.shape and dq.dtype is dtype and dq.is_contiguous() and dk.shape == xk.shape and
+            dk.dtype is dtype and dk.is_contiguous()):
+        _shaped("dq", dq, xq.shape, dtype), _shaped("dk", dk, xk.shape, dtype)
     index = _device(xq, xk, gq, gk, pos, freqs, dq, dk)
     if out is None:
-        out = {"dxq": _kept(xq.new_empty(xq.shape), stream), "dxk": _kept(xk.new_empty(xk.shape), stream)}
+        dxq, dxk = torch.empty_like(dq), torch.empty_like(dk)
         sdq, sdk = Hq * d, Hk * d
+        out = {"dxq": dxq, "dxk": dxk}
+        dgq = dgk = None
         if norm:
-            out["dgq"] = _kept(xq.new_empty(d, dtype=torch.float32), stream)
-            out["dgk"] = _kept(xq.new_empty(d, dtype=torch.float32), stream)
-        dgq, dgk = out.get("dgq"), out.get("dgk")
+            dgq, dgk = xq.new_empty(d, dtype=_F32), xq.new_empty(d, dtype=_F32)
+            out["dgq"], out["dgk"] = dgq, dgk
+        if stream is not None:
+            _keep(stream, dxq, dxk, dgq, dgk)
     else:
-        dgq, dgk = out.get("dgq"), out.get("dgk")
-        Tq, hq, eq, sdq = _token_rows("dxq", out["dxq"], xq.dtype)
-        Tk, hk, ek, sdk = _token_rows("dxk", out["dxk"], xq.dtype)
+        dxq, dxk, dgq, dgk = out["dxq"], out["dxk"], out.get("dgq"), out.get("dgk")
+        Tq, hq, eq, sdq = _token_rows("dxq", dxq, dtype)
+        Tk, hk, ek, sdk = _token_rows("dxk", dxk, dtype)
         if (Tq, hq, eq) != (T, Hq, d) or (Tk, hk, ek) != (T, Hk, d):
             raise ValueError("gdr2: dxq and dxk must have the shapes of xq and xk")
         for name, g in (("dgq", dgq), ("dgk", dgk)):
             if g is not None:
-                _shaped(name, g, (d,), torch.float32)
-        _device(xq, out["dxq"], out["dxk"], dgq, dgk)
+                _shaped(name, g, (d,), _F32)
+        _device(xq, dxq, dxk, dgq, dgk)
     nbytes = 0
     if dgq is not None or dgk is not None:
-        workspace, nbytes = _workspace(workspace, _bytes("gdr2_attn_prologue_workspace_bytes", d), xq, stream)
+        workspace, nbytes = _scratch(xq, workspace, stream, "gdr2_attn_prologue_workspace_bytes", d)
     st = (_lib or lib()).gdr2_attn_prologue_bwd(
         xq.data_ptr(), xk.data_ptr(), _p(gq), _p(gk), 1 if norm else 0, eps, _p(pos), _p(freqs), mag, rot,
-        1 if interleaved else 0, dq.data_ptr(), dk.data_ptr(), out["dxq"].data_ptr(), out["dxk"].data_ptr(), _p(dgq),
-        _p(dgk), T, Hq, Hk, d, dt, sq, sk, sdq, sdk, _p(workspace), nbytes, _raw_stream(stream, index))
-    _check("gdr2_attn_prologue_bwd", st)
+        1 if interleaved else 0, dq.data_ptr(), dk.data_ptr(), dxq.data_ptr(), dxk.data_ptr(), _p(dgq), _p(dgk), T, Hq,
+        Hk, d, dt, sq, sk, sdq, sdk, _p(workspace), nbytes, _raw_stream(stream, index))
+    if st != OK:
+        raise GDR2Error("gdr2_attn_prologue_bwd", st)
     return out
 
 
@@ -674,8 +689,9 @@ def _pools(k_pages, v_pages):
     shape = k_pages.shape
     if len(shape) != 4:
         raise ValueError("gdr2: k_pages must be [num_pages, Hk, page_size, d]")
-    _shaped("k_pages", k_pages, shape, k_pages.dtype)
-    _shaped("v_pages", v_pages, shape, k_pages.dtype)
+    if not (v_pages.shape == shape and v_pages.dtype is k_pages.dtype and k_pages.is_contiguous() and
+            v_pages.is_contiguous()):
+        _shaped("k_pages", k_pages, shape, k_pages.dtype), _shaped("v_pages", v_pages, shape, k_pages.dtype)
     return shape
 
 
@@ -683,8 +699,16 @@ def _table(table):
     shape = table.shape
     if len(shape) != 2:
         raise ValueError("gdr2: table must be [R, P]")
-    _shaped("table", table, shape, torch.int32)
+    if table.dtype is not _I32 or not table.is_contiguous():
+        _shaped("table", table, shape, _I32)
     return shape
+
+
+def _ints(n, **arrays):
+    """int32 arrays of n values each."""
+    for name, t in arrays.items():
+        if not (t.shape == (n,) and t.dtype is _I32 and t.is_contiguous()):
+            _shaped(name, t, (n,), _I32)
 
 
 def attn_prologue_cache(xq, xk, xv, gq, gk, seq, pos, freqs, k_pages, v_pages, table, *, norm=True, eps=1e-6,
@@ -700,12 +724,14 @@ def attn_prologue_cache(xq, xk, xv, gq, gk, seq, pos, freqs, k_pages, v_pages, t
         raise ValueError("gdr2: xk, xv and the pools must agree in tokens, heads, channels and dtype")
     if pos is None:
         raise ValueError("gdr2: pos is needed to find a token's page")
-    if freqs is None and (pos.dtype is not torch.int32 or pos.numel() != T or not pos.is_contiguous()):
+    if freqs is None and (pos.dtype is not _I32 or pos.numel() != T or not pos.is_contiguous()):
         raise ValueError("gdr2: pos must hold one int32 position for each token")
-    _shaped("seq", seq, (T,), torch.int32)
+    _ints(T, seq=seq)
     if q is None:
         index = _device(xq, xk, xv, gq, gk, seq, pos, freqs, k_pages, v_pages, table)
-        q = _kept(xq.new_empty(xq.shape), stream)
+        q = xq.new_empty(xq.shape)
+        if stream is not None:
+            _keep(stream, q)
     else:
         _shaped("q", q, xq.shape, xq.dtype)
         index = _device(xq, xk, xv, gq, gk, seq, pos, freqs, k_pages, v_pages, table, q)
@@ -713,7 +739,8 @@ def attn_prologue_cache(xq, xk, xv, gq, gk, seq, pos, freqs, k_pages, v_pages, t
         xq.data_ptr(), xk.data_ptr(), xv.data_ptr(), _p(gq), _p(gk), 1 if norm else 0, eps, seq.data_ptr(),
         pos.data_ptr(), _p(freqs), mag, rot, 1 if interleaved else 0, q.data_ptr(), k_pages.data_ptr(),
         v_pages.data_ptr(), table.data_ptr(), T, Hq, Hk, d, R, P, ps, num, dt, sq, sk, sv, _raw_stream(stream, index))
-    _check("gdr2_attn_prologue_cache", st)
+    if st != OK:
+        raise GDR2Error("gdr2_attn_prologue_cache", st)
     return q
 
 
@@ -722,45 +749,48 @@ def attn_decode(q, k_pages, v_pages, table, lens, seq=None, *, scale=None, windo
     """gdr2_attn_decode: attention of one new token for each row of q [N, Hq, d] over sequence seq[n] (int32 [N];
     None: n) of the cache, its last `window` tokens (0: all), lens int32 [R] with the new token counted. scale: by
     default d^-1/2. Returns o [N, Hq, d], or (o, lse fp32 [N, Hq]) with want_lse or a given lse."""
-    shape = q.shape
-    if len(shape) != 3:
-        raise ValueError("gdr2: q must be [N, Hq, d]")
-    _shaped("q", q, shape, q.dtype)
+    shape, dtype = q.shape, q.dtype
+    dt = _dtype_code(q)
+    if len(shape) != 3 or not q.is_contiguous():
+        raise ValueError("gdr2: q must be a contiguous [N, Hq, d]")
     N, Hq, d = shape
     num, Hk, ps, dp = _pools(k_pages, v_pages)
     R, P = _table(table)
-    if dp != d or k_pages.dtype is not q.dtype:
+    if dp != d or k_pages.dtype is not dtype:
         raise ValueError("gdr2: q and the pools must agree in channels and dtype")
-    _shaped("lens", lens, (R,), torch.int32)
+    _ints(R, lens=lens)
     if seq is not None:
-        _shaped("seq", seq, (N,), torch.int32)
-    dt = _dtype_code(q)
+        _ints(N, seq=seq)
     index = _device(q, k_pages, v_pages, table, lens, seq, o, lse)
     if o is None:
-        o = _kept(q.new_empty(shape), stream)
+        o = torch.empty_like(q)
+        if stream is not None:
+            _keep(stream, o)
     else:
-        _shaped("o", o, shape, q.dtype)
+        _shaped("o", o, shape, dtype)
     if lse is not None:
-        _shaped("lse", lse, (N, Hq), torch.float32)
+        _shaped("lse", lse, (N, Hq), _F32)
     elif want_lse:
-        lse = _kept(q.new_empty((N, Hq), dtype=torch.float32), stream)
-    workspace, nbytes = _workspace(workspace, _bytes("gdr2_attn_decode_workspace_bytes", d), q, stream)
+        lse = q.new_empty((N, Hq), dtype=_F32)
+        if stream is not None:
+            _keep(stream, lse)
+    workspace, nbytes = _scratch(q, workspace, stream, "gdr2_attn_decode_workspace_bytes", N, Hq, Hk, d, P, ps, window, dt)
     st = (_lib or lib()).gdr2_attn_decode(
         q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), table.data_ptr(), lens.data_ptr(), _p(seq),
         d ** -0.5 if scale is None else scale, window, o.data_ptr(), _p(lse), N, Hq, Hk, d, R, P, ps, num, dt,
-        workspace.data_ptr(), nbytes, _raw_stream(stream, index))
-    _check("gdr2_attn_decode", st)
+        _p(workspace), nbytes, _raw_stream(stream, index))
+    if st != OK:
+        raise GDR2Error("gdr2_attn_decode", st)
     return o if lse is None else (o, lse)
 
 
-def _int_out(out, name, like, shape, stream):
-    """A bookkeeping output: the one given in `out`, or a fresh one."""
-    t = None if out is None else out.get(name)
-    if t is None:
-        return _kept(like.new_empty(shape), stream)
-    _shaped(name, t, shape, torch.int32)
-    if t.get_device() != like.get_device():
-        raise ValueError(f"gdr2: {name} on another device")
+def _given(out, name, like, shape):
+    """The bookkeeping output that the caller gave for `name`, or None."""
+    t = out.get(name)
+    if t is not None:
+        _shaped(name, t, shape, _I32)
+        if t.get_device() != like.get_device():
+            raise ValueError(f"gdr2: {name} is on another device")
     return t
 
 
@@ -768,17 +798,24 @@ def kv_reserve(table, lens, want, ref, *, page_size, window=0, out=None, workspa
     """gdr2_kv_reserve: pages for tokens [lens[r], want[r]) of every sequence (pages behind the window released
     first). Returns (table, ref, missing int32 [1]) after the call; `out` may name them (also the inputs)."""
     R, P = _table(table)
-    _shaped("lens", lens, (R,), torch.int32), _shaped("want", want, (R,), torch.int32)
+    _ints(R, lens=lens, want=want)
     num = ref.numel()
-    _shaped("ref", ref, (num,), torch.int32)
+    _ints(num, ref=ref)
     index = _device(table, lens, want, ref)
-    t, r = _int_out(out, "table", table, (R, P), stream), _int_out(out, "ref", ref, (num,), stream)
-    m = _int_out(out, "missing", ref, (1,), stream)
-    workspace, nbytes = _workspace(workspace, _bytes("gdr2_kv_workspace_bytes", R, num), ref, stream)
+    t = r = m = None
+    if out is not None:
+        t, r, m = _given(out, "table", ref, (R, P)), _given(out, "ref", ref, (num,)), _given(out, "missing", ref, (1,))
+    t = torch.empty_like(table) if t is None else t
+    r = torch.empty_like(ref) if r is None else r
+    m = ref.new_empty(1) if m is None else m
+    if stream is not None:
+        _keep(stream, t, r, m)
+    workspace, nbytes = _scratch(ref, workspace, stream, "gdr2_kv_workspace_bytes", R, num)
     st = (_lib or lib()).gdr2_kv_reserve(
         table.data_ptr(), lens.data_ptr(), want.data_ptr(), ref.data_ptr(), t.data_ptr(), r.data_ptr(), m.data_ptr(),
-        R, P, page_size, num, window, workspace.data_ptr(), nbytes, _raw_stream(stream, index))
-    _check("gdr2_kv_reserve", st)
+        R, P, page_size, num, window, _p(workspace), nbytes, _raw_stream(stream, index))
+    if st != OK:
+        raise GDR2Error("gdr2_kv_reserve", st)
     return t, r, m
 
 
@@ -787,18 +824,27 @@ def kv_fork(table, lens, ref, parent, k_pages, v_pages, *, out=None, workspace=N
     released). Partly filled last pages are copied in the pools. Returns (table, lens, ref, missing int32 [1])."""
     R, P = _table(table)
     num, Hk, ps, d = _pools(k_pages, v_pages)
-    _shaped("lens", lens, (R,), torch.int32), _shaped("parent", parent, (R,), torch.int32)
-    _shaped("ref", ref, (num,), torch.int32)
+    _ints(R, lens=lens, parent=parent)
+    _ints(num, ref=ref)
     dt = _dtype_code(k_pages)
     index = _device(table, lens, ref, parent, k_pages, v_pages)
-    t, n = _int_out(out, "table", table, (R, P), stream), _int_out(out, "lens", lens, (R,), stream)
-    r, m = _int_out(out, "ref", ref, (num,), stream), _int_out(out, "missing", ref, (1,), stream)
-    workspace, nbytes = _workspace(workspace, _bytes("gdr2_kv_workspace_bytes", R, num), ref, stream)
+    t = n = r = m = None
+    if out is not None:
+        t, n = _given(out, "table", ref, (R, P)), _given(out, "lens", ref, (R,))
+        r, m = _given(out, "ref", ref, (num,)), _given(out, "missing", ref, (1,))
+    t = torch.empty_like(table) if t is None else t
+    n = torch.empty_like(lens) if n is None else n
+    r = torch.empty_like(ref) if r is None else r
+    m = ref.new_empty(1) if m is None else m
+    if stream is not None:
+        _keep(stream, t, n, r, m)
+    workspace, nbytes = _scratch(ref, workspace, stream, "gdr2_kv_workspace_bytes", R, num)
     st = (_lib or lib()).gdr2_kv_fork(
         table.data_ptr(), lens.data_ptr(), ref.data_ptr(), parent.data_ptr(), t.data_ptr(), n.data_ptr(), r.data_ptr(),
-        m.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), R, P, Hk, ps, d, num, dt, workspace.data_ptr(), nbytes,
+        m.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), R, P, Hk, ps, d, num, dt, _p(workspace), nbytes,
         _raw_stream(stream, index))
-    _check("gdr2_kv_fork", st)
+    if st != OK:
+        raise GDR2Error("gdr2_kv_fork", st)
     return t, n, r, m
 
 
@@ -806,16 +852,23 @@ def kv_compact(table, ref, k_pages, v_pages, *, out=None, workspace=None, stream
     """gdr2_kv_compact: the live pages moved to [0, live). Returns (table, ref, live int32 [1])."""
     R, P = _table(table)
     num, Hk, ps, d = _pools(k_pages, v_pages)
-    _shaped("ref", ref, (num,), torch.int32)
+    _ints(num, ref=ref)
     dt = _dtype_code(k_pages)
     index = _device(table, ref, k_pages, v_pages)
-    t, r = _int_out(out, "table", table, (R, P), stream), _int_out(out, "ref", ref, (num,), stream)
-    m = _int_out(out, "live", ref, (1,), stream)
-    workspace, nbytes = _workspace(workspace, _bytes("gdr2_kv_workspace_bytes", R, num), ref, stream)
+    t = r = m = None
+    if out is not None:
+        t, r, m = _given(out, "table", ref, (R, P)), _given(out, "ref", ref, (num,)), _given(out, "live", ref, (1,))
+    t = torch.empty_like(table) if t is None else t
+    r = torch.empty_like(ref) if r is None else r
+    m = ref.new_empty(1) if m is None else m
+    if stream is not None:
+        _keep(stream, t, r, m)
+    workspace, nbytes = _scratch(ref, workspace, stream, "gdr2_kv_workspace_bytes", R, num)
     st = (_lib or lib()).gdr2_kv_compact(
         table.data_ptr(), ref.data_ptr(), t.data_ptr(), r.data_ptr(), m.data_ptr(), k_pages.data_ptr(),
-        v_pages.data_ptr(), R, P, Hk, ps, d, num, dt, workspace.data_ptr(), nbytes, _raw_stream(stream, index))
-    _check("gdr2_kv_compact", st)
+        v_pages.data_ptr(), R, P, Hk, ps, d, num, dt, _p(workspace), nbytes, _raw_stream(stream, index))
+    if st != OK:
+        raise GDR2Error("gdr2_kv_compact", st)
     return t, r, m
 
 

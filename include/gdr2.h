@@ -454,9 +454,11 @@ GDR2_API int gdr2_attn_prologue_cache(const void *xq, const void *xk, const void
  * With no token left o = 0 and lse = -inf. A slot whose seq is outside [0, R) is padding: its rows of o and lse are
  * left as they were. What lies in the pools outside the tokens read (NaN included) has no effect. Statistics and sums
  * are fp32; a finite v is assumed. Repeated calls give identical bits. The lengths are read on the stream, so a
- * captured call stays valid as sequences grow.
+ * captured call stays valid as sequences grow. The workspace query returns 0 for sizes that need none (short tables
+ * or windows) and for invalid ones.
  */
-GDR2_API size_t gdr2_attn_decode_workspace_bytes(int d);
+GDR2_API size_t gdr2_attn_decode_workspace_bytes(int N, int Hq, int Hk, int d, int P, int page_size, int window,
+                                                 int dtype);
 
 GDR2_API int gdr2_attn_decode(const void *q, const void *k_pages, const void *v_pages, const int *table,
                               const int *lens, const int *seq, float scale, int window, void *o, float *lse, int N,

@@ -325,7 +325,8 @@ def test_decode_replayed_as_sequences_grow_and_two_graphs():
     qs = [randn(g, 2, 16, 128, dtype=torch.bfloat16) for _ in range(2)]
     ln = torch.tensor([5, 0], dtype=torch.int32, device="cuda")
     graphs, outs = [], []
-    need = int(gdr2.lib().gdr2_attn_decode_workspace_bytes(128))
+    need = int(gdr2.lib().gdr2_attn_decode_workspace_bytes(2, 16, 2, 128, table.shape[1], 16, 0, gdr2.GDR2_BF16))
+    assert need > 0
     for q in qs:
         ws = torch.empty(need, dtype=torch.uint8, device="cuda")
         o, lse = torch.empty_like(q), torch.empty(2, 16, device="cuda")

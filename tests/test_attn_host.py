@@ -64,7 +64,7 @@ def test_prologue_cache_refusals(over, status):
 
 
 DECODE = dict(q=FAKE, kp=FAKE, vp=FAKE, table=FAKE, lens=FAKE, seq=None, scale=0.1, window=0, o=FAKE, lse=None, N=3, Hq=4,
-              Hk=2, d=64, R=3, P=5, ps=16, num=9, dtype=1, ws=FAKE, wsb=1 << 30, stream=None)
+              Hk=2, d=64, R=3, P=200, ps=16, num=9, dtype=1, ws=FAKE, wsb=1 << 30, stream=None)
 
 
 @pytest.mark.parametrize("over,status", [
@@ -72,7 +72,7 @@ DECODE = dict(q=FAKE, kp=FAKE, vp=FAKE, table=FAKE, lens=FAKE, seq=None, scale=0
     (dict(seq=ODD), ARG), (dict(o=None), ARG), (dict(lse=ODD), ARG), (dict(window=-1), ARG), (dict(N=0), ARG),
     (dict(N=4), ARG), (dict(Hq=5), ARG), (dict(Hq=1), ARG), (dict(d=32), UNS), (dict(dtype=-1), ARG), (dict(R=0), ARG),
     (dict(ps=-4), ARG), (dict(P=1 << 30), UNS), (dict(N=1 << 30, seq=FAKE), UNS), (dict(ws=None), WS),
-    (dict(wsb=1000), WS)], ids=str)
+    (dict(wsb=1000), WS), (dict(num=1 << 30, ps=16, P=200), UNS)], ids=str)
 def test_decode_refusals(over, status):
     assert call("gdr2_attn_decode", DECODE, **over) == status
 
@@ -107,8 +107,13 @@ def test_compact_refusals(over, status):
 
 def test_workspace_sizes():
     L = gdr2.lib()
-    for f in (L.gdr2_attn_prologue_workspace_bytes, L.gdr2_attn_decode_workspace_bytes):
-        assert 0 < f(64) < f(128) < 1 << 24 and f(96) == 0
+    f = L.gdr2_attn_prologue_workspace_bytes
+    assert 0 < f(64) < f(128) < 1 << 24 and f(96) == 0
+    f = L.gdr2_attn_decode_workspace_bytes  # N, Hq, Hk, d, P, page_size, window, dtype
+    assert 0 < f(3, 8, 2, 64, 1000, 16, 0, 1) < f(3, 8, 2, 128, 1000, 16, 0, 1) < 1 << 24
+    assert f(3, 8, 2, 64, 4, 16, 0, 1) == 0 and f(3, 8, 2, 64, 1000, 16, 64, 1) == 0  # short rows stay whole
+    assert f(0, 8, 2, 64, 1000, 16, 0, 1) == 0 and f(3, 7, 2, 64, 1000, 16, 0, 1) == 0
+    assert f(3, 8, 2, 96, 1000, 16, 0, 1) == 0 and f(3, 8, 2, 64, 1000, 16, -1, 1) == 0
     assert L.gdr2_kv_workspace_bytes(3, 100) > 0
     assert L.gdr2_kv_workspace_bytes(0, 100) == 0 and L.gdr2_kv_workspace_bytes(3, -1) == 0
     assert L.gdr2_kv_workspace_bytes(1 << 20, 1 << 30) > 1 << 33  # more than 32 bits of bytes
