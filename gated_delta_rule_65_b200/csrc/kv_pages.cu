@@ -135,6 +135,37 @@ __device__ __forceinline__ Place place() {
     return t;
 }
 
+// The blocks that copies move: the rows of one head of a page, page_size of them of row_bytes each, in both pools.
+struct Blocks {
+    uint8_t *k, *v;
+    int Hk, page_size, row_bytes;
+};
+
+// Copies the first rows[i] (null: all) token rows of every head of page src[i] to page dst[i], i < n. A warp moves up to
+// 4 KB of one block, eight 16-byte loads a lane in flight; the caller's warps are warp, warp + warps, ...
+__device__ __forceinline__ void copy_rows(int n, const int *src, const int *dst, const int *rows, const Blocks &bl, uint32_t warp,
+                                          uint32_t warps, int lane) {
+    constexpr int kPiece = 4096;
+    const long long block = (long long)bl.page_size * bl.row_bytes;
+    const uint32_t pieces = (uint32_t)((block + kPiece - 1) / kPiece), heads = 2 * bl.Hk;
+    const uint32_t items = (uint32_t)n * heads * pieces;  // below 2^32: checked for the whole pool
+    for (uint32_t x = warp; x < items; x += warps) {
+        const uint32_t y = x / pieces, piece = x - y * pieces, i = y / heads, hh = y - i * heads, h = hh >> 1;
+        const long long bytes = rows ? (long long)__ldcg(rows + i) * bl.row_bytes : block;
+        uint8_t *pool = hh & 1 ? bl.v : bl.k;
+        const uint8_t *s = pool + ((long long)__ldcg(src + i) * bl.Hk + h) * block;
+        uint8_t *d = pool + ((long long)__ldcg(dst + i) * bl.Hk + h) * block;
+        const long long base = (long long)piece * kPiece + lane * 16;
+        uint4 r[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+            if (base + u * 512 < bytes) r[u] = __ldcs(reinterpret_cast<const uint4 *>(s + base + u * 512));
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+            if (base + u * 512 < bytes) *reinterpret_cast<uint4 *>(d + base + u * 512) = r[u];
+    }
+}
+
 // Pages for tokens [lens[r], want[r]) of every sequence: its entries from the one of token lens[r] to the one of token
 // want[r] - 1 that are empty get a page. Before that, pages wholly behind the window of the token at lens[r] are
 // released. The grid is one cluster.
@@ -242,7 +273,7 @@ __global__ void __launch_bounds__(kThreads) kv_reserve_kernel(KvPagesArgs a, Lis
 // Every sequence r takes over the content of sequence parent[r] as it was before the call (r itself: stays; outside
 // [0, R): released). Full pages are shared. The partly filled last page stays with one taker, the parent itself if it
 // is one, else the first; every other taker gets a copy of its tokens on a fresh page. The grid is one cluster.
-__global__ void __launch_bounds__(kThreads) kv_fork_kernel(KvPagesArgs a, Lists w) {
+__global__ void __launch_bounds__(kThreads) kv_fork_kernel(KvPagesArgs a, Lists w, Blocks bl, int copy) {
     cg::cluster_group cl = cg::this_cluster();
     const Place t = place();
     const int E = a.R * a.P, ps = a.page_size;
@@ -342,10 +373,14 @@ __global__ void __launch_bounds__(kThreads) kv_fork_kernel(KvPagesArgs a, Lists 
         }
         need0 += __popc(m);
     }
+    if (copy) {
+        cl.sync();
+        copy_rows(min(needed, nfree), w.src, w.dst, w.rows, bl, t.warp, t.warps, t.lane);
+    }
 }
 
 // Live pages numbered live or above move to the free numbers below, in order; table and counts follow.
-__global__ void __launch_bounds__(kThreads) kv_compact_kernel(KvPagesArgs a, Lists w) {
+__global__ void __launch_bounds__(kThreads) kv_compact_kernel(KvPagesArgs a, Lists w, Blocks bl, int copy) {
     cg::cluster_group cl = cg::this_cluster();
     const Place t = place();
     const int E = a.R * a.P;
@@ -414,58 +449,43 @@ __global__ void __launch_bounds__(kThreads) kv_compact_kernel(KvPagesArgs a, Lis
             if (b + 32 * x + t.lane < es.last) a.table_out[b + 32 * x + t.lane] = e[x];
         }
     }
+    if (copy) copy_rows(moves, w.high, w.pages, nullptr, bl, t.warp, t.warps, t.lane);
 }
 
-// Copies the first rows[i] (null: all) token rows of every head of page src[i] to page dst[i], in both pools. A warp
-// moves up to 4 KB of one head's rows, eight 16-byte loads a lane in flight.
-__global__ void __launch_bounds__(256) kv_copy_kernel(const int *ncopy, const int *src, const int *dst, const int *rows,
-                                                      uint8_t *k, uint8_t *v, int Hk, int page_size, int row_bytes) {
+// The same by a kernel of its own over the whole GPU.
+__global__ void __launch_bounds__(256) kv_copy_kernel(const int *ncopy, const int *src, const int *dst, const int *rows, Blocks bl) {
     follow();
-    constexpr int kPiece = 4096;
-    const int lane = threadIdx.x & 31;
-    const long long block = (long long)page_size * row_bytes;
-    const uint32_t pieces = (uint32_t)((block + kPiece - 1) / kPiece), heads = 2 * Hk;
-    const uint32_t items = (uint32_t)__ldcg(ncopy) * heads * pieces;  // below 2^32: checked for the whole pool
-    for (uint32_t x = blockIdx.x * 8 + (threadIdx.x >> 5); x < items; x += gridDim.x * 8) {
-        const uint32_t y = x / pieces, piece = x - y * pieces, i = y / heads, hh = y - i * heads, h = hh >> 1;
-        const long long bytes = rows ? (long long)__ldcg(rows + i) * row_bytes : block;
-        uint8_t *pool = hh & 1 ? v : k;
-        const uint8_t *s = pool + ((long long)__ldcg(src + i) * Hk + h) * block;
-        uint8_t *d = pool + ((long long)__ldcg(dst + i) * Hk + h) * block;
-        const long long base = (long long)piece * kPiece + lane * 16;
-        uint4 r[8];
-#pragma unroll
-        for (int u = 0; u < 8; ++u)
-            if (base + u * 512 < bytes) r[u] = __ldcs(reinterpret_cast<const uint4 *>(s + base + u * 512));
-#pragma unroll
-        for (int u = 0; u < 8; ++u)
-            if (base + u * 512 < bytes) *reinterpret_cast<uint4 *>(d + base + u * 512) = r[u];
-    }
+    copy_rows(__ldcg(ncopy), src, dst, rows, bl, blockIdx.x * 8 + (threadIdx.x >> 5), gridDim.x * 8, threadIdx.x & 31);
 }
 
-// CTAs of the cluster: one while each of its threads has a few items, the largest portable cluster above that.
-int cluster_size(const KvPagesArgs &a) {
+// CTAs of the cluster: one while each of its threads has a few items, the largest portable cluster above that, or when
+// it copies pages too.
+int cluster_size(const KvPagesArgs &a, bool copy) {
     const long long items = (long long)a.R * a.P + a.num_pages;
-    int c = 1;
+    int c = copy ? kMaxCluster : 1;
     while (c < kMaxCluster && items > 4LL * c * kThreads) c *= 2;
     return c;
 }
 
-cudaError_t launch_cluster(void (*kernel)(KvPagesArgs, Lists), const KvPagesArgs &a, const Lists &w, cudaStream_t st) {
-    const int c = cluster_size(a);
-    return launch(kernel, dim3(c), dim3(kThreads), 0, c, st, a, w);
+Blocks blocks(const KvPagesArgs &a) {
+    return Blocks{(uint8_t *)a.k_pages, (uint8_t *)a.v_pages, a.Hk, a.page_size, a.d * (a.dtype == 1 ? 2 : 4)};
 }
 
-cudaError_t launch_copy(const KvPagesArgs &a, const Lists &w, const int *src, const int *dst, const int *rows, long long most,
+// Up to so many bytes of pages (the most that a call can move) the cluster copies them itself: eight SMs move them in
+// the time that another launch takes.
+constexpr long long kOwnCopy = 4 << 20;
+bool own_copy(const Blocks &bl, long long most) {
+    return most * 2 * bl.Hk * bl.page_size * bl.row_bytes <= kOwnCopy;  // most < 2^31, the block's bytes < 2^32
+}
+
+cudaError_t launch_copy(const Lists &w, const int *src, const int *dst, const int *rows, const Blocks &bl, long long most,
                         cudaStream_t st) {
-    const int row_bytes = a.d * (a.dtype == 1 ? 2 : 4);
-    const long long pieces = ((long long)a.page_size * row_bytes + 4095) / 4096;
-    const long long want = (most * a.Hk * 2 * pieces + 7) / 8, full = 8LL * kAttnSms;
+    const long long pieces = ((long long)bl.page_size * bl.row_bytes + 4095) / 4096;
+    const long long want = (most * bl.Hk * 2 * pieces + 7) / 8, full = 8LL * kAttnSms;
     const int grid = (int)(want < full ? want : full);
     cudaError_t e;
     GDR2_LAUNCH("kv_copy", st,
-                e = launch(kv_copy_kernel, dim3(grid), dim3(256), 0, 0, st, (const int *)w.ncopy, src, dst, rows,
-                                     (uint8_t *)a.k_pages, (uint8_t *)a.v_pages, a.Hk, a.page_size, row_bytes));
+                e = launch(kv_copy_kernel, dim3(grid), dim3(256), 0, 0, st, (const int *)w.ncopy, src, dst, rows, bl));
     return e;
 }
 
@@ -477,25 +497,32 @@ size_t kv_workspace_bytes(int R, int num_pages) {
 }
 
 cudaError_t launch_kv_reserve(const KvPagesArgs &a, cudaStream_t st) {
+    const int c = cluster_size(a, false);
     cudaError_t e;
-    GDR2_LAUNCH("kv_reserve", st, e = launch_cluster(kv_reserve_kernel, a, lists(a.workspace, a.R, a.num_pages), st));
+    GDR2_LAUNCH("kv_reserve", st,
+                e = launch(kv_reserve_kernel, dim3(c), dim3(kThreads), 0, c, st, a, lists(a.workspace, a.R, a.num_pages)));
     return e;
 }
 
 cudaError_t launch_kv_fork(const KvPagesArgs &a, cudaStream_t st) {
     const Lists w = lists(a.workspace, a.R, a.num_pages);
+    const Blocks bl = blocks(a);
+    const bool own = own_copy(bl, a.R);
+    const int c = cluster_size(a, own);
     cudaError_t e;
-    GDR2_LAUNCH("kv_fork", st, e = launch_cluster(kv_fork_kernel, a, w, st));
-    if (e != cudaSuccess) return e;
-    return launch_copy(a, w, w.src, w.dst, w.rows, a.R, st);
+    GDR2_LAUNCH("kv_fork", st, e = launch(kv_fork_kernel, dim3(c), dim3(kThreads), 0, c, st, a, w, bl, (int)own));
+    return e != cudaSuccess || own ? e : launch_copy(w, w.src, w.dst, w.rows, bl, a.R, st);
 }
 
 cudaError_t launch_kv_compact(const KvPagesArgs &a, cudaStream_t st) {
     const Lists w = lists(a.workspace, a.R, a.num_pages);
+    const Blocks bl = blocks(a);
+    const long long most = a.num_pages / 2;  // a live page above for each free one below
+    const bool own = own_copy(bl, most);
+    const int c = cluster_size(a, own);
     cudaError_t e;
-    GDR2_LAUNCH("kv_compact", st, e = launch_cluster(kv_compact_kernel, a, w, st));
-    if (e != cudaSuccess) return e;
-    return launch_copy(a, w, w.high, w.pages, nullptr, (a.num_pages + 1) / 2, st);
+    GDR2_LAUNCH("kv_compact", st, e = launch(kv_compact_kernel, dim3(c), dim3(kThreads), 0, c, st, a, w, bl, (int)own));
+    return e != cudaSuccess || own ? e : launch_copy(w, w.high, w.pages, nullptr, bl, most, st);
 }
 
 }  // namespace gdr2

@@ -510,25 +510,24 @@ def _token_rows(name, x, dtype):
     (a view of a fused projection may have a larger one): (tokens, heads, channels, stride in elements)."""
     if x.dtype is not dtype:
         raise TypeError(f"gdr2: {name} is {x.dtype}, not {dtype}")
-    shape = x.shape
+    shape, strides = x.shape, x.stride()
     if len(shape) == 3:
         T, H, d = shape
+        step, hs, ds = strides
     elif len(shape) == 4:
-        T, H, d = shape[0] * shape[1], shape[2], shape[3]
+        B, n, H, d = shape
+        T = B * n
+        bs, step, hs, ds = strides
+        if n == 1:
+            step = bs
+        elif B > 1 and bs != n * step:
+            raise ValueError(f"gdr2: the tokens of {name} must have one stride across the batch")
     else:
         raise ValueError(f"gdr2: {name} must be [T, H, d] or [B, T, H, d]")
     if T * H * d == 0:
         raise ValueError(f"gdr2: {name} is empty")
-    if x.is_contiguous():
-        return T, H, d, H * d
-    strides = x.stride()
-    if (d > 1 and strides[-1] != 1) or (H > 1 and strides[-2] != d):
+    if (ds != 1 and d > 1) or (hs != d and H > 1):
         raise ValueError(f"gdr2: heads and channels of {name} must be contiguous")
-    step = strides[0]
-    if len(shape) == 4 and shape[1] > 1:
-        step = strides[1]
-        if shape[0] > 1 and strides[0] != shape[1] * step:
-            raise ValueError(f"gdr2: the tokens of {name} must have one stride across the batch")
     return T, H, d, step if T > 1 else H * d
 
 
@@ -606,17 +605,19 @@ def _prologue_checks(xq, xk, gq, gk, pos, freqs, norm):
     Tk, Hk, dk, sk = _token_rows("xk", xk, dtype)
     if Tk != T or dk != d:
         raise ValueError("gdr2: xq and xk must have the same tokens and channels")
-    for name, g in (("gq", gq), ("gk", gk)):
-        if g is not None and not (g.shape == (d,) and g.dtype is _F32 and g.is_contiguous() and norm):
-            _shaped(name, g, (d,), _F32)
-            raise ValueError("gdr2: gq and gk are gains of the norm; pass None without it")
+    if gq is not None and (gq.dtype is not _F32 or gq.shape != (d,) or not gq.is_contiguous()):
+        _shaped("gq", gq, (d,), _F32)
+    if gk is not None and (gk.dtype is not _F32 or gk.shape != (d,) or not gk.is_contiguous()):
+        _shaped("gk", gk, (d,), _F32)
+    if not norm and (gq is not None or gk is not None):
+        raise ValueError("gdr2: gq and gk are gains of the norm; pass None without it")
     if freqs is None:
         return T, Hq, Hk, d, sq, sk, dt, 0
     if freqs.dtype is not _F64 or freqs.dim() != 1 or not freqs.is_contiguous():
         raise TypeError("gdr2: freqs must be a contiguous 1-D float64 tensor")
     if pos is None or pos.dtype is not _I32 or pos.numel() != T or not pos.is_contiguous():
         raise ValueError("gdr2: pos must hold one int32 position for each token")
-    return T, Hq, Hk, d, sq, sk, dt, 2 * freqs.shape[0]
+    return T, Hq, Hk, d, sq, sk, dt, 2 * freqs.numel()
 
 
 def attn_prologue_fwd(xq, xk, gq=None, gk=None, pos=None, freqs=None, *, norm=True, eps=1e-6, mag=1.0,
@@ -627,7 +628,7 @@ def attn_prologue_fwd(xq, xk, gq=None, gk=None, pos=None, freqs=None, *, norm=Tr
     T, Hq, Hk, d, sq, sk, dt, rot = _prologue_checks(xq, xk, gq, gk, pos, freqs, norm)
     if out is None:
         index = _device(xq, xk, gq, gk, pos, freqs)
-        q, k = xq.new_empty(xq.shape), xk.new_empty(xk.shape)
+        q, k = torch.empty_like(xq), torch.empty_like(xk)  # contiguous, whatever the token stride of the inputs
         out = {"q": q, "k": k}
         if stream is not None:
             _keep(stream, q, k)
@@ -659,7 +660,8 @@ def attn_prologue_bwd(xq, xk, gq, gk, pos, freqs, dq, dk, *, norm=True, eps=1e-6
         out = {"dxq": dxq, "dxk": dxk}
         dgq = dgk = None
         if norm:
-            dgq, dgk = xq.new_empty(d, dtype=_F32), xq.new_empty(d, dtype=_F32)
+            dgq = xq.new_empty(d, dtype=_F32)
+            dgk = torch.empty_like(dgq)
             out["dgq"], out["dgk"] = dgq, dgk
         if stream is not None:
             _keep(stream, dxq, dxk, dgq, dgk)
@@ -704,11 +706,10 @@ def _table(table):
     return shape
 
 
-def _ints(n, **arrays):
-    """int32 arrays of n values each."""
-    for name, t in arrays.items():
-        if not (t.shape == (n,) and t.dtype is _I32 and t.is_contiguous()):
-            _shaped(name, t, (n,), _I32)
+def _ints(n, name, t):
+    """An int32 array of n values."""
+    if t.dtype is not _I32 or t.shape != (n,) or not t.is_contiguous():
+        _shaped(name, t, (n,), _I32)
 
 
 def attn_prologue_cache(xq, xk, xv, gq, gk, seq, pos, freqs, k_pages, v_pages, table, *, norm=True, eps=1e-6,
@@ -726,10 +727,10 @@ def attn_prologue_cache(xq, xk, xv, gq, gk, seq, pos, freqs, k_pages, v_pages, t
         raise ValueError("gdr2: pos is needed to find a token's page")
     if freqs is None and (pos.dtype is not _I32 or pos.numel() != T or not pos.is_contiguous()):
         raise ValueError("gdr2: pos must hold one int32 position for each token")
-    _ints(T, seq=seq)
+    _ints(T, "seq", seq)
     if q is None:
         index = _device(xq, xk, xv, gq, gk, seq, pos, freqs, k_pages, v_pages, table)
-        q = xq.new_empty(xq.shape)
+        q = torch.empty_like(xq)
         if stream is not None:
             _keep(stream, q)
     else:
@@ -758,9 +759,9 @@ def attn_decode(q, k_pages, v_pages, table, lens, seq=None, *, scale=None, windo
     R, P = _table(table)
     if dp != d or k_pages.dtype is not dtype:
         raise ValueError("gdr2: q and the pools must agree in channels and dtype")
-    _ints(R, lens=lens)
+    _ints(R, "lens", lens)
     if seq is not None:
-        _ints(N, seq=seq)
+        _ints(N, "seq", seq)
     index = _device(q, k_pages, v_pages, table, lens, seq, o, lse)
     if o is None:
         o = torch.empty_like(q)
@@ -771,7 +772,7 @@ def attn_decode(q, k_pages, v_pages, table, lens, seq=None, *, scale=None, windo
     if lse is not None:
         _shaped("lse", lse, (N, Hq), _F32)
     elif want_lse:
-        lse = q.new_empty((N, Hq), dtype=_F32)
+        lse = q.new_empty(N, Hq, dtype=_F32)
         if stream is not None:
             _keep(stream, lse)
     workspace, nbytes = _scratch(q, workspace, stream, "gdr2_attn_decode_workspace_bytes", N, Hq, Hk, d, P, ps, window, dt)
@@ -798,9 +799,9 @@ def kv_reserve(table, lens, want, ref, *, page_size, window=0, out=None, workspa
     """gdr2_kv_reserve: pages for tokens [lens[r], want[r]) of every sequence (pages behind the window released
     first). Returns (table, ref, missing int32 [1]) after the call; `out` may name them (also the inputs)."""
     R, P = _table(table)
-    _ints(R, lens=lens, want=want)
+    _ints(R, "lens", lens), _ints(R, "want", want)
     num = ref.numel()
-    _ints(num, ref=ref)
+    _ints(num, "ref", ref)
     index = _device(table, lens, want, ref)
     t = r = m = None
     if out is not None:
@@ -824,8 +825,8 @@ def kv_fork(table, lens, ref, parent, k_pages, v_pages, *, out=None, workspace=N
     released). Partly filled last pages are copied in the pools. Returns (table, lens, ref, missing int32 [1])."""
     R, P = _table(table)
     num, Hk, ps, d = _pools(k_pages, v_pages)
-    _ints(R, lens=lens, parent=parent)
-    _ints(num, ref=ref)
+    _ints(R, "lens", lens), _ints(R, "parent", parent)
+    _ints(num, "ref", ref)
     dt = _dtype_code(k_pages)
     index = _device(table, lens, ref, parent, k_pages, v_pages)
     t = n = r = m = None
@@ -852,7 +853,7 @@ def kv_compact(table, ref, k_pages, v_pages, *, out=None, workspace=None, stream
     """gdr2_kv_compact: the live pages moved to [0, live). Returns (table, ref, live int32 [1])."""
     R, P = _table(table)
     num, Hk, ps, d = _pools(k_pages, v_pages)
-    _ints(num, ref=ref)
+    _ints(num, "ref", ref)
     dt = _dtype_code(k_pages)
     index = _device(table, ref, k_pages, v_pages)
     t = r = m = None

@@ -436,7 +436,8 @@ GDR2_API int gdr2_attn_prologue_bwd(const void *xq, const void *xk, const float 
  * row xv[t] go to the cache. Token t is token pos[t] of sequence seq[t].
  *   seq, pos int32 [T]     xv [T, Hk, d] dtype, xv_stride elements from token to token
  * A token whose seq is outside [0, R) is padding: nothing of it is written, its q row included. A token whose page is
- * not there (or whose pos is outside the table) gets its q row only. Two tokens for one place leave either's row.
+ * not there (or whose pos is outside the table) gets its q row only. Two tokens for one place leave
+ * it undefined.
  */
 GDR2_API int gdr2_attn_prologue_cache(const void *xq, const void *xk, const void *xv, const float *gq, const float *gk,
                                       int norm, float eps, const int *seq, const int *pos, const double *freqs,

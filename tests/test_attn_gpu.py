@@ -3,6 +3,9 @@ bounds): query / key prologue with its gradients, the prologue that writes the c
 from __future__ import annotations
 
 import math
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -170,6 +173,56 @@ def test_prologue_on_another_stream_and_in_a_graph():
             assert torch.equal(gout[n], grads[n])
 
 
+def test_prologue_without_gradients_of_the_gains():
+    """out without dgq and dgk: no workspace, the same dxq, dxk; out with one of them: only that one."""
+    x, kw, g = prologue_case(PROLOGUE[3])
+    a = (x["xq"], x["xk"], x["gq"], x["gk"], x["pos"], x["freqs"])
+    dq, dk = torch.randn_like(x["xq"]), torch.randn_like(x["xk"])
+    want = gdr2.attn_prologue_bwd(*a, dq, dk, **kw)
+    for only in ((), ("dgk",)):
+        out = {n: torch.empty_like(want[n]) for n in ("dxq", "dxk", *only)}
+        assert gdr2.attn_prologue_bwd(*a, dq, dk, **kw, out=out) is out
+        for n in out:
+            assert torch.equal(out[n], want[n]), n
+
+
+CAPTURE = """
+import torch
+from gated_delta_rule_65_b200 import gdr2
+i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+q = torch.randn(2, 8, 128, device="cuda").bfloat16()
+kv = torch.randn(2, 4, 128, device="cuda").bfloat16()
+k, v = torch.randn(2, 90, 2, 16, 128, device="cuda").bfloat16()
+table = torch.arange(90, dtype=torch.int32, device="cuda").view(2, 45)
+lens, seq, pos, ref, parent = i32([700, 33]), i32([0, 1]), i32([699, 32]), i32([1] * 90), i32([0, 1])
+freqs, _ = gdr2.rope_freqs(128)
+def step():
+    t, r, _ = gdr2.kv_reserve(table, lens, lens, ref, page_size=16)
+    y = gdr2.attn_prologue_cache(q, kv[:, :2], kv[:, 2:], None, None, seq, pos, freqs, k, v, t)
+    o = gdr2.attn_decode(y, k, v, t, lens)
+    g = gdr2.attn_prologue_bwd(q, kv, None, None, pos, freqs, q, kv)
+    f = gdr2.attn_prologue_fwd(q, kv, None, None, pos, freqs)
+    t, n, r, _ = gdr2.kv_fork(t, lens, r, parent, k, v)
+    return (o, *g.values(), *f.values(), t, n, *gdr2.kv_compact(t, r, k, v))
+graph = torch.cuda.CUDAGraph()
+torch.cuda.synchronize()
+with torch.cuda.graph(graph):
+    got = step()
+graph.replay()
+torch.cuda.synchronize()
+got = [x.clone() for x in got]
+assert all(torch.equal(x, y) for x, y in zip(got, step()))
+print("captured first")
+"""
+
+
+def test_first_call_of_a_process_inside_a_capture():
+    """Nothing has to run before the first capture: a fresh process captures every kernel's first launch."""
+    r = subprocess.run([sys.executable, "-c", CAPTURE], capture_output=True, text=True, timeout=240,
+                       cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert r.returncode == 0 and "captured first" in r.stdout, r.stderr[-2000:]
+
+
 # ---- the cache -----------------------------------------------------------------------------------------------
 
 
@@ -250,6 +303,11 @@ DECODE = [
     ([37 * (i % 11) for i in range(300)], 4, 2, 64, 16, 100, "bf16"),
     ([20011], 8, 1, 128, 128, 0, "bf16"),
     ([30001, 2], 2, 1, 64, 16, 0, "f32"),
+    # more rows than CTAs, some cut by their borders
+    ([(i * 97) % 700 for i in range(150)], 8, 4, 64, 16, 0, "bf16"),
+    ([(i * 97) % 400 for i in range(170)], 3, 3, 128, 16, 0, "f32"),
+    # more sequences than a CTA has threads, most of them empty
+    ([(i * 7919) % 23 if i % 3 == 0 else 0 for i in range(3000)], 2, 1, 64, 8, 0, "bf16"),
 ]
 
 
@@ -348,6 +406,22 @@ def test_decode_replayed_as_sequences_grow_and_two_graphs():
             ref.check("o", o, ro, to)
             ref.check("lse", lse, rl, tl)
             assert torch.equal(o, gdr2.attn_decode(q, k, v, table, ln))
+
+
+def test_decode_on_another_stream():
+    """stream= with fresh outputs and workspaces, the inputs made on the current stream, which then goes on at once."""
+    g = gen(25)
+    k, v, table, lens, _ = cache(g, [3000, 20, 900], 16, 2, 64, torch.bfloat16)
+    q = randn(g, 3, 8, 64, dtype=torch.bfloat16)
+    want = gdr2.attn_decode(q, k, v, table, lens)
+    side = torch.cuda.Stream()
+    got = []
+    for _ in range(20):
+        side.wait_stream(torch.cuda.current_stream())
+        got.append(gdr2.attn_decode(q, k, v, table, lens, stream=side))
+        torch.full((1 << 21,), math.nan, device="cuda")  # would reuse a workspace that was let go too early
+    side.synchronize()
+    assert all(torch.equal(x, want) for x in got)
 
 
 def test_decode_offsets_past_32_bits():
