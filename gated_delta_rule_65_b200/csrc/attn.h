@@ -4,6 +4,7 @@
 
 #include <cuda_runtime.h>
 #include <stddef.h>
+#include <stdint.h>
 
 #include <atomic>
 
@@ -11,6 +12,21 @@ namespace gdr2 {
 
 // SMs the persistent grids below are sized for. A constant, so that a workspace query and the launch agree.
 constexpr int kAttnSms = 148;
+
+// Division of numbers below 2^31 by d >= 1: x d' >> shift with d' = floor(2^(31 + s) / d) + 1, 2^s >= d, is exact.
+struct Divisor {
+    uint32_t magic, shift;
+    Divisor() : magic(0), shift(0) {}
+    explicit Divisor(uint32_t d) {
+        uint32_t s = 0;
+        while ((1ull << s) < d) ++s;
+        shift = 31 + s;
+        magic = (uint32_t)((1ull << shift) / d + 1);
+    }
+#ifdef __CUDACC__
+    __device__ __forceinline__ uint32_t divide(uint32_t x) const { return (uint32_t)((uint64_t)x * magic >> shift); }
+#endif
+};
 
 struct AttnPrologueArgs {
     const void *xq, *xk, *xv;             // [T, H, d], token strides sxq, sxk, sxv; xv only for the cache form
@@ -28,6 +44,7 @@ struct AttnPrologueArgs {
     const int *seq, *table;               // cache form
     void *k_pages, *v_pages;              // [num_pages, Hk, page_size, d]
     int R, P, page_size, num_pages;
+    Divisor by_page;                      // page_size, set by the launch
     int T, Hq, Hk, d, dtype;
     long long sxq, sxk, sxv, sdxq, sdxk;  // elements
     void *workspace;

@@ -92,14 +92,8 @@ __device__ __forceinline__ float pow2(float x) {
 struct Line {
     int G, nb, rows;        // query heads of a KV head, blocks of them, heads of a block
     int whole;              // no row is cut
-    uint32_t magic, shift;  // x / page_size = x * magic >> shift for x < 2^31
+    Divisor by_page;
 };
-__host__ inline void set_divisor(Line &ln, uint32_t d) {  // magic = floor(2^(31 + s) / d) + 1 with 2^s >= d
-    uint32_t s = 0;
-    while ((1ull << s) < d) ++s;
-    ln.shift = 31 + s;
-    ln.magic = (uint32_t)((1ull << ln.shift) / d + 1);
-}
 
 // The span of sequence n that is attended: tokens [start, len); false for a slot without a sequence.
 __device__ __forceinline__ bool span_of(const AttnDecodeArgs &p, int n, int &s, int &start, int &len) {
@@ -569,7 +563,7 @@ __global__ void __launch_bounds__(kThreads, M::kPerSm) attn_decode_kernel(AttnDe
         page = -1;
         const int tok = ahead.first + warp * M::kTok + lane;
         if (xa < end && lane < M::kTok && tok < ahead.len) {
-            const uint32_t j = (uint32_t)((uint64_t)(uint32_t)tok * ln.magic >> ln.shift);
+            const uint32_t j = ln.by_page.divide(tok);
             page = __ldg(ahead.pages + j);
             off = tok - (int)j * p.page_size;
         }
@@ -726,7 +720,7 @@ template <int D, typename M> Plan plan(const AttnDecodeArgs &a) {
     p.ln.G = a.Hq / a.Hk;
     p.ln.rows = M::kRows;
     p.ln.nb = (p.ln.G + M::kRows - 1) / M::kRows;
-    set_divisor(p.ln, a.page_size);
+    p.ln.by_page = Divisor(a.page_size);
     // no more CTAs than the largest possible line has tiles, or rows if they stay whole: short ones do, as there is
     // nothing to join then, and a few tiles more or less make no CTA late
     long long span = (long long)a.P * a.page_size;

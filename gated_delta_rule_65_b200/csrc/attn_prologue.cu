@@ -162,9 +162,11 @@ template <int D> __device__ __forceinline__ void stage_gain(const float *g, floa
 }
 
 // The work of a warp: units u = warp, warp + warps, ... of (token, part), token u / parts; part k of a token takes the
-// heads k kRows + (the lane's row), + parts kRows, ... of each tensor.
+// heads k kRows + (the lane's row), + parts kRows, ... of each tensor. parts = 2^log: no division in a unit's few rows.
 struct Units {
-    int parts, count, stride;
+    int log, count, stride;
+    __device__ __forceinline__ int token(int u) const { return u >> log; }
+    __device__ __forceinline__ int part(int u) const { return u & ((1 << log) - 1); }
 };
 
 __device__ __forceinline__ void cp16(void *dst, const void *src, bool on) {  // off: zeros, nothing is read
@@ -191,7 +193,7 @@ __global__ void __launch_bounds__(kThreads, kFwdCtas) attn_prologue_fwd_kernel(A
     FwdShared<D> &sh = *reinterpret_cast<FwdShared<D> *>(raw);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, grp = lane / Y::kLanes, l = lane % Y::kLanes;
     const Slot<D, T, kInter> w(l, p.rot);
-    const int step = un.parts * Y::kRows;
+    const int step = Y::kRows << un.log;
     const int tq = (p.Hq + step - 1) / step, tk = (p.Hk + step - 1) / step;
     int u = blockIdx.x * kWarps + warp;
     follow();
@@ -201,8 +203,8 @@ __global__ void __launch_bounds__(kThreads, kFwdCtas) attn_prologue_fwd_kernel(A
     int ua = u, seg = -1, left = 0, ha = 0, ea = 0;
     const T *src = nullptr;
     auto enter = [&]() {
-        const int tok = ua / un.parts;
-        ha = (ua - tok * un.parts) * Y::kRows + grp;
+        const int tok = un.token(ua);
+        ha = un.part(ua) * Y::kRows + grp;
         ++seg;
         const T *x = static_cast<const T *>(seg == 0 ? p.xq : seg == 1 ? p.xk : p.xv);
         src = x + (size_t)tok * (seg == 0 ? p.sxq : seg == 1 ? p.sxk : p.sxv) + (size_t)ha * D;
@@ -227,11 +229,11 @@ __global__ void __launch_bounds__(kThreads, kFwdCtas) attn_prologue_fwd_kernel(A
 #pragma unroll
     for (int i = 0; i < kFwdDepth; ++i) fetch(i);
     // the token of a unit, read one unit ahead (its sequence two)
-    auto token = [&](int v) { return v < un.count ? v / un.parts : 0; };
+    auto token = [&](int v) { return v < un.count ? un.token(v) : 0; };
     int pos = 0, seq = 0, page = -1, npos = 0, nseq = 0;
     auto find_page = [&](int q, int s) {
         if (s < 0 || s >= p.R || q < 0) return -1;
-        const int j = q / p.page_size;
+        const int j = (int)p.by_page.divide(q);
         return j < p.P ? __ldg(p.table + (size_t)s * p.P + j) : -1;
     };
     if (p.rot || kCache) {
@@ -251,7 +253,7 @@ __global__ void __launch_bounds__(kThreads, kFwdCtas) attn_prologue_fwd_kernel(A
     const bool all = p.rot == D;
     int slot = 0;
     for (; u < un.count; u += un.stride) {
-        const int tok = u / un.parts, h0 = (u - tok * un.parts) * Y::kRows + grp;
+        const int tok = un.token(u), h0 = un.part(u) * Y::kRows + grp;
         int fpos = 0, fseq = 0, npage = -1;
         if (p.rot || kCache) fpos = p.pos[token(u + 2 * un.stride)];
         if constexpr (kCache) {
@@ -262,7 +264,7 @@ __global__ void __launch_bounds__(kThreads, kFwdCtas) attn_prologue_fwd_kernel(A
         const bool live = !kCache || (seq >= 0 && seq < p.R);
         const bool put = !kCache || (live && page >= 0 && page < p.num_pages);
         const long long hs = kCache ? (long long)p.page_size * D : D;  // from head to head where keys go
-        const size_t at = kCache ? (put ? ((size_t)page * p.Hk * p.page_size + pos % p.page_size) * D : 0) : (size_t)tok * p.Hk * D;
+        const size_t at = kCache ? (put ? ((size_t)page * p.Hk * p.page_size + (pos - p.by_page.divide(pos) * p.page_size)) * D : 0) : (size_t)tok * p.Hk * D;
 #pragma unroll 1
         for (int which = 0; which < 2; ++which) {
             // u (.) g folded into the rotation: the partner's gain goes with its sine
@@ -357,14 +359,14 @@ __global__ void __launch_bounds__(kThreads, kBwdCtas) attn_prologue_bwd_kernel(A
     const int H = keys ? p.Hk : p.Hq;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, grp = lane / Y::kLanes, l = lane % Y::kLanes;
     const Slot<D, T, kInter> w(l, p.rot);
-    const int step = un.parts * Y::kRows, rows = (H + step - 1) / step;
+    const int step = Y::kRows << un.log, rows = (H + step - 1) / step;
     int u = (blockIdx.x - (keys ? cq : 0)) * kWarps + warp;
     follow();
     int ua = u, left = 0, ha = 0;  // as in the forward: the row this lane fetches next
     const T *sd = nullptr, *sr = nullptr;
     auto enter = [&]() {
-        const int tok = ua / un.parts;
-        ha = (ua - tok * un.parts) * Y::kRows + grp;
+        const int tok = un.token(ua);
+        ha = un.part(ua) * Y::kRows + grp;
         sd = dy + ((size_t)tok * H + ha) * D;
         sr = x + (size_t)tok * sx + (size_t)ha * D;
         left = rows;
@@ -388,7 +390,7 @@ __global__ void __launch_bounds__(kThreads, kBwdCtas) attn_prologue_bwd_kernel(A
     };
 #pragma unroll
     for (int i = 0; i < kBwdDepth; ++i) fetch(i);
-    auto position = [&](int v) { return p.rot ? p.pos[v < un.count ? v / un.parts : 0] : 0; };
+    auto position = [&](int v) { return p.rot ? p.pos[v < un.count ? un.token(v) : 0] : 0; };
     int pos = position(u);
     Freqs fr;
     fr.load(p, lane);
@@ -402,7 +404,7 @@ __global__ void __launch_bounds__(kThreads, kBwdCtas) attn_prologue_bwd_kernel(A
     const bool all = p.rot == D;
     int slot = 0;
     for (; u < un.count; u += un.stride) {
-        const int tok = u / un.parts, h0 = (u - tok * un.parts) * Y::kRows + grp;
+        const int tok = un.token(u), h0 = un.part(u) * Y::kRows + grp;
         const int npos = position(u + un.stride);
         fr.angles<D>(p, pos, sh.cs[warp], lane);
         Turn<T> t;
@@ -511,9 +513,9 @@ __global__ void __launch_bounds__(1024) attn_prologue_reduce_kernel(const float 
 // the token's angles, and with fewer units the last round leaves most warps idle), more below, up to one row a lane.
 Units split_units(int T, int most, int rows, int warps, int fill) {
     Units un;
-    un.parts = 1;
-    while (un.parts * rows < most && (long long)T * un.parts < (long long)fill * warps) un.parts *= 2;
-    un.count = T * un.parts;
+    un.log = 0;
+    while ((rows << un.log) < most && ((long long)T << un.log) < (long long)fill * warps) ++un.log;
+    un.count = T << un.log;
     un.stride = warps;
     return un;
 }
@@ -590,7 +592,11 @@ struct Bwd {
 size_t attn_prologue_workspace_bytes(int d) { return (size_t)kBwdGrid * d * sizeof(float); }
 
 cudaError_t launch_attn_prologue_fwd(const AttnPrologueArgs &a, cudaStream_t st) { return dispatch(a, Fwd{a, false, st}); }
-cudaError_t launch_attn_prologue_cache(const AttnPrologueArgs &a, cudaStream_t st) { return dispatch(a, Fwd{a, true, st}); }
+cudaError_t launch_attn_prologue_cache(const AttnPrologueArgs &a, cudaStream_t st) {
+    AttnPrologueArgs b = a;
+    b.by_page = Divisor(a.page_size);
+    return dispatch(b, Fwd{b, true, st});
+}
 cudaError_t launch_attn_prologue_bwd(const AttnPrologueArgs &a, cudaStream_t st) { return dispatch(a, Bwd{a, st}); }
 
 }  // namespace gdr2
