@@ -26,12 +26,13 @@ namespace cg = cooperative_groups;
 constexpr int kThreads = 1024;
 constexpr int kMaxCluster = 8;
 constexpr int kMaxWarps = kMaxCluster * kThreads / 32;
+constexpr int kOwners = 4096;
 
-// Workspace, ints: strip totals of two counts, the copies' count, then lists.
+// Workspace, ints: strip totals of three counts, numbers for the copies, then lists.
 struct Lists {
-    int *ta, *tb;    // [kMaxWarps] strip totals
-    int *ncopy;      // [4]
-    int *pages;      // [num_pages] free pages by rank (compact: the free ones below the live count)
+    int *ta, *tb, *tc;  // [kMaxWarps] strip totals
+    int *ncopy;      // [4] copies; compact: the live pages
+    int *pages;      // [num_pages] each strip's free pages from its start on (compact: those below the live count, by rank)
     int *high;       // [num_pages] compact: live pages at or above the live count, by rank
     int *rank;       // [num_pages] compact: rank of such a page
     int *owner;      // [R] fork: who keeps a sequence's partly filled page
@@ -46,7 +47,7 @@ Lists lists(void *ws, int R, int num_pages) {
         p += (n + 3) / 4 * 4;
         return x;
     };
-    w.ta = take(kMaxWarps), w.tb = take(kMaxWarps), w.ncopy = take(4);
+    w.ta = take(kMaxWarps), w.tb = take(kMaxWarps), w.tc = take(kMaxWarps), w.ncopy = take(4);
     w.pages = take(num_pages), w.high = take(num_pages), w.rank = take(num_pages);
     w.owner = take(R), w.src = take(R), w.dst = take(R), w.rows = take(R);
     return w;
@@ -97,7 +98,7 @@ __device__ __forceinline__ void before(const int *t, int warp, int warps, int la
 __device__ __forceinline__ int valid(int e, int num_pages) { return e >= 0 && e < num_pages ? e : -1; }
 __device__ __forceinline__ int entry(const int *table, int at, int num_pages) { return valid(__ldcg(table + at), num_pages); }
 
-// The number of free pages in a strip, and the free pages of rank < most listed by rank.
+// The number of free pages in a strip.
 __device__ __forceinline__ int count_free(const int *ref, Strip s, int lane) {
     int c = 0;
     for (int b = s.first; b < s.last; b += 32 * kAhead) {
@@ -109,19 +110,60 @@ __device__ __forceinline__ int count_free(const int *ref, Strip s, int lane) {
     }
     return __reduce_add_sync(0xffffffffu, c);
 }
-__device__ __forceinline__ void list_free(const int *ref, Strip s, int rank, int most, int *out, int lane) {
-    for (int b = s.first; b < s.last && rank < most; b += 32 * kAhead) {
+// The same, and the free pages listed at list[s.first ...]; the counts are copied to `copy` unless it is null.
+__device__ __forceinline__ int list_free(const int *ref, Strip s, int *list, int *copy, int lane) {
+    int c = 0;
+    for (int b = s.first; b < s.last; b += 32 * kAhead) {
         int n[kAhead];
 #pragma unroll
         for (int x = 0; x < kAhead; ++x) n[x] = b + 32 * x + lane < s.last ? __ldcg(ref + b + 32 * x + lane) : 1;
 #pragma unroll
         for (int x = 0; x < kAhead; ++x) {
+            const int i = b + 32 * x + lane;
             const unsigned m = __ballot_sync(0xffffffffu, n[x] <= 0);
-            const int at = rank + __popc(m & ((1u << lane) - 1));
-            if (n[x] <= 0 && at < most) out[at] = b + 32 * x + lane;
-            rank += __popc(m);
+            if (n[x] <= 0) list[s.first + c + __popc(m & ((1u << lane) - 1))] = i;
+            if (copy && i < s.last) copy[i] = n[x];
+            c += __popc(m);
         }
     }
+    return c;
+}
+
+// pre[i] = t[0] + ... + t[i - 1], i <= warps (a multiple of 32); by one warp.
+__device__ __forceinline__ void prefix(const int *t, int warps, int *pre, int lane) {
+    const int each = warps / 32;
+    int v[kMaxWarps / 32], sum = 0;
+#pragma unroll
+    for (int i = 0; i < kMaxWarps / 32; ++i) {
+        v[i] = i < each ? __ldcg(t + lane * each + i) : 0;
+        sum += v[i];
+    }
+    int at = sum;
+#pragma unroll
+    for (int x = 1; x < 32; x <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, at, x);
+        if (lane >= x) at += y;
+    }
+    at -= sum;
+#pragma unroll
+    for (int i = 0; i < kMaxWarps / 32; ++i)
+        if (i < each) {
+            pre[lane * each + i] = at;
+            at += v[i];
+        }
+    if (lane == 31) pre[warps] = at;
+}
+// The free page of a rank: the strip whose list holds it, and its place there.
+__device__ __forceinline__ int free_page(const int *pages, const int *pre, int rank, int warps, int length) {
+    int a = 0, e = warps;  // pre[a] <= rank < pre[e]
+    while (e - a > 1) {
+        const int mid = (a + e) / 2;
+        if (pre[mid] <= rank)
+            a = mid;
+        else
+            e = mid;
+    }
+    return __ldcg(pages + a * length + rank - pre[a]);
 }
 
 struct Place {
@@ -174,21 +216,10 @@ __global__ void __launch_bounds__(kThreads) kv_reserve_kernel(KvPagesArgs a, Lis
     const Place t = place();
     const int E = a.R * a.P, ps = a.page_size;
     follow();
+    __shared__ int need[kMaxWarps + 1], free[kMaxWarps + 1], past[kMaxWarps + 1];
     const Strip es = strip(E, t.warp, t.warps), pg = strip(a.num_pages, t.warp, t.warps);
-    // the counts are copied, and free pages counted on the way; a window's releases change them, so then count again
-    int nfree = 0;
-    for (int b = pg.first; b < pg.last; b += 32 * kAhead) {
-        int n[kAhead];
-#pragma unroll
-        for (int x = 0; x < kAhead; ++x) n[x] = b + 32 * x + t.lane < pg.last ? __ldcg(a.ref + b + 32 * x + t.lane) : 1;
-#pragma unroll
-        for (int x = 0; x < kAhead; ++x) {
-            nfree += n[x] <= 0;
-            if (b + 32 * x + t.lane < pg.last) a.ref_out[b + 32 * x + t.lane] = n[x];
-        }
-    }
-    nfree = __reduce_add_sync(0xffffffffu, nfree);
-    if (t.gid == 0) *a.count_out = 0;
+    // the counts are copied and free pages listed on the way; a window's releases change them, so then list later
+    int nfree = list_free(a.ref, pg, w.pages, a.ref_out, t.lane);
     if (a.window > 0) cl.sync();
     // entries: released, copied, and counted where a page is needed
     int c = 0;
@@ -221,26 +252,25 @@ __global__ void __launch_bounds__(kThreads) kv_reserve_kernel(KvPagesArgs a, Lis
         }
     }
     c = __reduce_add_sync(0xffffffffu, c);
-    if (t.lane == 0) w.ta[t.warp] = c, w.tb[t.warp] = nfree;
     int over = 0;  // pages past the table's end
     for (int r = t.gid; r < a.R; r += t.threads) {
         const int want = a.want[r];
         if (want > 0) over += max(0, (want - 1) / ps + 1 - a.P);
     }
-    cl.sync();
-    if (a.window > 0) {
-        nfree = count_free(a.ref_out, pg, t.lane);
-        if (t.lane == 0) w.tb[t.warp] = nfree;
-    }
     over = __reduce_add_sync(0xffffffffu, over);
-    if (t.lane == 0 && over) atomicAdd(a.count_out, over);
-    if (a.window > 0) cl.sync();
-    int need0, needed, free0;
-    before(w.ta, t.warp, t.warps, t.lane, need0, needed);
-    before(w.tb, t.warp, t.warps, t.lane, free0, nfree);
-    list_free(a.ref_out, pg, free0, needed, w.pages, t.lane);
-    if (t.gid == 0 && needed > nfree) atomicAdd(a.count_out, needed - nfree);
+    if (a.window > 0) {
+        cl.sync();
+        nfree = list_free(a.ref_out, pg, w.pages, nullptr, t.lane);
+    }
+    if (t.lane == 0) w.ta[t.warp] = c, w.tb[t.warp] = nfree, w.tc[t.warp] = over;
     cl.sync();
+    if (threadIdx.x < 32) prefix(w.ta, t.warps, need, t.lane);
+    if (threadIdx.x / 32 == 1) prefix(w.tb, t.warps, free, t.lane);
+    if (threadIdx.x / 32 == 2) prefix(w.tc, t.warps, past, t.lane);
+    __syncthreads();
+    const int all = free[t.warps], length = strip_length(a.num_pages, t.warps);
+    int rank0 = need[t.warp];
+    if (t.gid == 0) *a.count_out = past[t.warps] + max(0, need[t.warps] - all);
     if (c == 0) return;
     at = Cell(es.first + t.lane, a.P);
     for (int b = es.first; b < es.last; b += 32 * kAhead) {
@@ -257,15 +287,15 @@ __global__ void __launch_bounds__(kThreads) kv_reserve_kernel(KvPagesArgs a, Lis
         }
 #pragma unroll
         for (int x = 0; x < kAhead; ++x) {
-            const bool need = e[x] < 0 && tok[x] + ps > max(len[x], 0) && tok[x] < want[x];
-            const unsigned m = __ballot_sync(0xffffffffu, need);
-            const int rank = need0 + __popc(m & ((1u << t.lane) - 1));
-            if (need && rank < nfree) {
-                const int page = __ldcg(w.pages + rank);
+            const bool is = e[x] < 0 && tok[x] + ps > max(len[x], 0) && tok[x] < want[x];
+            const unsigned m = __ballot_sync(0xffffffffu, is);
+            const int rank = rank0 + __popc(m & ((1u << t.lane) - 1));
+            if (is && rank < all) {
+                const int page = free_page(w.pages, free, rank, t.warps, length);
                 a.table_out[b + 32 * x + t.lane] = page;
                 a.ref_out[page] = 1;
             }
-            need0 += __popc(m);
+            rank0 += __popc(m);
         }
     }
 }
@@ -279,7 +309,20 @@ __global__ void __launch_bounds__(kThreads) kv_fork_kernel(KvPagesArgs a, Lists 
     const int E = a.R * a.P, ps = a.page_size;
     follow();
     const Strip es = strip(E, t.warp, t.warps), pg = strip(a.num_pages, t.warp, t.warps), rs = strip(a.R, t.warp, t.warps);
-    for (int r = t.gid; r < a.R; r += t.threads) w.owner[r] = a.R;
+    // who keeps a sequence's last page: up to kOwners sequences each CTA finds it for itself
+    __shared__ int need[kMaxWarps + 1], free[kMaxWarps + 1], owner_here[kOwners];
+    const bool here = a.R <= kOwners;
+    int *owner = here ? owner_here : w.owner;
+    const int r0 = here ? threadIdx.x : t.gid, rn = here ? kThreads : t.threads;
+    for (int r = r0; r < a.R; r += rn) owner[r] = a.R;
+    if (here)
+        __syncthreads();
+    else
+        cl.sync();
+    for (int r = r0; r < a.R; r += rn) {
+        const int p = a.parent[r];
+        if (p >= 0 && p < a.R) atomicMin(owner + p, r == p ? -1 : r);
+    }
     for (int b = pg.first; b < pg.last; b += 32 * kAhead) {
         int n[kAhead];
 #pragma unroll
@@ -288,15 +331,9 @@ __global__ void __launch_bounds__(kThreads) kv_fork_kernel(KvPagesArgs a, Lists 
         for (int x = 0; x < kAhead; ++x)
             if (b + 32 * x + t.lane < pg.last) a.ref_out[b + 32 * x + t.lane] = n[x];
     }
-    if (t.gid == 0) *a.count_out = 0;
-    cl.sync();
-    for (int r = t.gid; r < a.R; r += t.threads) {
-        const int p = a.parent[r];
-        if (p >= 0 && p < a.R) atomicMin(w.owner + p, r == p ? -1 : r);
-    }
     cl.sync();
     auto length = [&](int p) { return (int)min((long long)max(__ldg(a.lens + p), 0), (long long)a.P * ps); };
-    auto owns = [&](int r, int p) { return __ldcg(w.owner + p) == (r == p ? -1 : r); };
+    auto owns = [&](int r, int p) { return (here ? owner_here[p] : __ldcg(w.owner + p)) == (r == p ? -1 : r); };
     constexpr int kFew = 4;
     Cell at(es.first + t.lane, a.P);
     for (int b = es.first; b < es.last; b += 32 * kFew) {
@@ -342,28 +379,27 @@ __global__ void __launch_bounds__(kThreads) kv_fork_kernel(KvPagesArgs a, Lists 
     };
     int c = 0;
     for (int b = rs.first; b < rs.last; b += 32) c += __popc(__ballot_sync(0xffffffffu, source(b + t.lane) >= 0));
-    if (t.lane == 0) w.ta[t.warp] = c;
     cl.sync();
-    c = count_free(a.ref_out, pg, t.lane);
-    if (t.lane == 0) w.tb[t.warp] = c;
+    const int nfree = list_free(a.ref_out, pg, w.pages, nullptr, t.lane);
+    if (t.lane == 0) w.ta[t.warp] = c, w.tb[t.warp] = nfree;
     cl.sync();
-    int need0, needed, free0, nfree;
-    before(w.ta, t.warp, t.warps, t.lane, need0, needed);
-    before(w.tb, t.warp, t.warps, t.lane, free0, nfree);
-    list_free(a.ref_out, pg, free0, needed, w.pages, t.lane);
+    if (threadIdx.x < 32) prefix(w.ta, t.warps, need, t.lane);
+    if (threadIdx.x / 32 == 1) prefix(w.tb, t.warps, free, t.lane);
+    __syncthreads();
+    const int all = free[t.warps], needed = need[t.warps], each = strip_length(a.num_pages, t.warps);
+    int rank0 = need[t.warp];
     if (t.gid == 0) {
-        w.ncopy[0] = min(needed, nfree);
-        if (needed > nfree) *a.count_out = needed - nfree;
+        w.ncopy[0] = min(needed, all);
+        *a.count_out = max(0, needed - all);
     }
-    cl.sync();
     for (int b = rs.first; b < rs.last; b += 32) {
         const int r = b + t.lane, src = source(r);
         const unsigned m = __ballot_sync(0xffffffffu, src >= 0);
-        const int rank = need0 + __popc(m & ((1u << t.lane) - 1));
+        const int rank = rank0 + __popc(m & ((1u << t.lane) - 1));
         if (src >= 0) {
             const int len = length(a.parent[r]), j = len / ps;
-            if (rank < nfree) {
-                const int page = __ldcg(w.pages + rank);
+            if (rank < all) {
+                const int page = free_page(w.pages, free, rank, t.warps, each);
                 a.table_out[r * a.P + j] = page;
                 a.ref_out[page] = 1;
                 w.src[rank] = src, w.dst[rank] = page, w.rows[rank] = len - j * ps;
@@ -371,19 +407,43 @@ __global__ void __launch_bounds__(kThreads) kv_fork_kernel(KvPagesArgs a, Lists 
                 a.lens_out[r] = j * ps;
             }
         }
-        need0 += __popc(m);
+        rank0 += __popc(m);
     }
     if (copy) {
         cl.sync();
-        copy_rows(min(needed, nfree), w.src, w.dst, w.rows, bl, t.warp, t.warps, t.lane);
+        copy_rows(min(needed, all), w.src, w.dst, w.rows, bl, t.warp, t.warps, t.lane);
     }
 }
 
-// Live pages numbered live or above move to the free numbers below, in order; table and counts follow.
+// The rest of a compaction, once the lists are there: counts and pages move, the table follows.
+__device__ __forceinline__ void move_pages(const KvPagesArgs &a, const Lists &w, const Blocks &bl, int moves, int live, const Place &t) {
+    for (int k = t.gid; k < moves; k += t.threads) {
+        const int src = __ldcg(w.high + k), dst = __ldcg(w.pages + k);
+        const int n = __ldcg(a.ref + src);
+        a.ref_out[dst] = n;
+        a.ref_out[src] = 0;
+    }
+    const int E = a.R * a.P;
+    for (int b = t.gid; b < E; b += 4 * t.threads) {
+        int e[4], k[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) e[x] = (long long)b + x * t.threads < E ? entry(a.table, b + x * t.threads, a.num_pages) : -1;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) k[x] = e[x] >= live ? __ldcg(w.rank + e[x]) : -1;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            if (k[x] >= 0) e[x] = __ldcg(w.pages + k[x]);
+            if ((long long)b + x * t.threads < E) a.table_out[b + x * t.threads] = e[x];
+        }
+    }
+    copy_rows(moves, w.high, w.pages, nullptr, bl, t.warp, t.warps, t.lane);
+}
+
+// Live pages numbered live or above move to the free numbers below, in order; table and counts follow (here if `copy`,
+// else in kv_move_kernel).
 __global__ void __launch_bounds__(kThreads) kv_compact_kernel(KvPagesArgs a, Lists w, Blocks bl, int copy) {
     cg::cluster_group cl = cg::this_cluster();
     const Place t = place();
-    const int E = a.R * a.P;
     follow();
     const Strip pg = strip(a.num_pages, t.warp, t.warps);
     const int nf = count_free(a.ref, pg, t.lane);
@@ -426,33 +486,25 @@ __global__ void __launch_bounds__(kThreads) kv_compact_kernel(KvPagesArgs a, Lis
         }
     }
     if (t.gid == 0) {
-        w.ncopy[0] = moves;
+        w.ncopy[0] = moves, w.ncopy[1] = live;
         *a.count_out = live;
     }
-    cl.sync();
-    for (int k = t.gid; k < moves; k += t.threads) {
-        const int src = __ldcg(w.high + k), dst = __ldcg(w.pages + k);
-        const int n = __ldcg(a.ref + src);
-        a.ref_out[dst] = n;
-        a.ref_out[src] = 0;
+    if (copy) {
+        cl.sync();
+        move_pages(a, w, bl, moves, live, t);
     }
-    const Strip es = strip(E, t.warp, t.warps);
-    for (int b = es.first; b < es.last; b += 32 * kAhead) {
-        int e[kAhead], k[kAhead];
-#pragma unroll
-        for (int x = 0; x < kAhead; ++x) e[x] = b + 32 * x + t.lane < es.last ? entry(a.table, b + 32 * x + t.lane, a.num_pages) : -1;
-#pragma unroll
-        for (int x = 0; x < kAhead; ++x) k[x] = e[x] >= live ? __ldcg(w.rank + e[x]) : -1;
-#pragma unroll
-        for (int x = 0; x < kAhead; ++x) {
-            if (k[x] >= 0) e[x] = __ldcg(w.pages + k[x]);
-            if (b + 32 * x + t.lane < es.last) a.table_out[b + 32 * x + t.lane] = e[x];
-        }
-    }
-    if (copy) copy_rows(moves, w.high, w.pages, nullptr, bl, t.warp, t.warps, t.lane);
 }
 
-// The same by a kernel of its own over the whole GPU.
+__global__ void __launch_bounds__(256) kv_move_kernel(KvPagesArgs a, Lists w, Blocks bl) {
+    follow();
+    Place t;
+    t.gid = blockIdx.x * 256 + threadIdx.x, t.threads = gridDim.x * 256;
+    t.warp = t.gid >> 5, t.warps = t.threads >> 5, t.lane = threadIdx.x & 31;
+    const int2 n = __ldcg(reinterpret_cast<const int2 *>(w.ncopy));
+    move_pages(a, w, bl, n.x, n.y, t);
+}
+
+// Copies by a kernel of its own over the whole GPU.
 __global__ void __launch_bounds__(256) kv_copy_kernel(const int *ncopy, const int *src, const int *dst, const int *rows, Blocks bl) {
     follow();
     copy_rows(__ldcg(ncopy), src, dst, rows, bl, blockIdx.x * 8 + (threadIdx.x >> 5), gridDim.x * 8, threadIdx.x & 31);
@@ -478,22 +530,18 @@ bool own_copy(const Blocks &bl, long long most) {
     return most * 2 * bl.Hk * bl.page_size * bl.row_bytes <= kOwnCopy;  // most < 2^31, the block's bytes < 2^32
 }
 
-cudaError_t launch_copy(const Lists &w, const int *src, const int *dst, const int *rows, const Blocks &bl, long long most,
-                        cudaStream_t st) {
+// CTAs of a copy over the whole GPU: a warp for each 4 KB that may move, eight CTAs an SM at most.
+int copy_grid(const Blocks &bl, long long most) {
     const long long pieces = ((long long)bl.page_size * bl.row_bytes + 4095) / 4096;
     const long long want = (most * bl.Hk * 2 * pieces + 7) / 8, full = 8LL * kAttnSms;
-    const int grid = (int)(want < full ? want : full);
-    cudaError_t e;
-    GDR2_LAUNCH("kv_copy", st,
-                e = launch(kv_copy_kernel, dim3(grid), dim3(256), 0, 0, st, (const int *)w.ncopy, src, dst, rows, bl));
-    return e;
+    return (int)(want < full ? want : full);
 }
 
 }  // namespace
 
 size_t kv_workspace_bytes(int R, int num_pages) {
     const size_t n = ((size_t)num_pages + 3) / 4 * 4, r = ((size_t)R + 3) / 4 * 4;
-    return (2 * (size_t)kMaxWarps + 4 + 3 * n + 4 * r) * sizeof(int);
+    return (3 * (size_t)kMaxWarps + 4 + 3 * n + 4 * r) * sizeof(int);
 }
 
 cudaError_t launch_kv_reserve(const KvPagesArgs &a, cudaStream_t st) {
@@ -511,7 +559,11 @@ cudaError_t launch_kv_fork(const KvPagesArgs &a, cudaStream_t st) {
     const int c = cluster_size(a, own);
     cudaError_t e;
     GDR2_LAUNCH("kv_fork", st, e = launch(kv_fork_kernel, dim3(c), dim3(kThreads), 0, c, st, a, w, bl, (int)own));
-    return e != cudaSuccess || own ? e : launch_copy(w, w.src, w.dst, w.rows, bl, a.R, st);
+    if (e != cudaSuccess || own) return e;
+    GDR2_LAUNCH("kv_copy", st,
+                e = launch(kv_copy_kernel, dim3(copy_grid(bl, a.R)), dim3(256), 0, 0, st, (const int *)w.ncopy,
+                           (const int *)w.src, (const int *)w.dst, (const int *)w.rows, bl));
+    return e;
 }
 
 cudaError_t launch_kv_compact(const KvPagesArgs &a, cudaStream_t st) {
@@ -522,7 +574,9 @@ cudaError_t launch_kv_compact(const KvPagesArgs &a, cudaStream_t st) {
     const int c = cluster_size(a, own);
     cudaError_t e;
     GDR2_LAUNCH("kv_compact", st, e = launch(kv_compact_kernel, dim3(c), dim3(kThreads), 0, c, st, a, w, bl, (int)own));
-    return e != cudaSuccess || own ? e : launch_copy(w, w.high, w.pages, nullptr, bl, most, st);
+    if (e != cudaSuccess || own) return e;
+    GDR2_LAUNCH("kv_move", st, e = launch(kv_move_kernel, dim3(copy_grid(bl, most)), dim3(256), 0, 0, st, a, w, bl));
+    return e;
 }
 
 }  // namespace gdr2
