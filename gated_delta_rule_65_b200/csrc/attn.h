@@ -79,6 +79,11 @@ cudaError_t launch_kv_reserve(const KvPagesArgs &a, cudaStream_t st);
 cudaError_t launch_kv_fork(const KvPagesArgs &a, cudaStream_t st);
 cudaError_t launch_kv_compact(const KvPagesArgs &a, cudaStream_t st);
 
+// As in kernels.h; only failed index checks of the debug build set a bit here.
+int status_take_attn_prologue();
+int status_take_attn_decode();
+int status_take_kv_pages();
+
 // The launch of every kernel here: its blocks may become resident while the kernel before it on the stream still runs.
 // So each kernel begins with follow(), which lets the next one do the same and waits until everything before it on
 // the stream has finished and can be read; nothing of global memory is touched before. (Two launches of a pair are

@@ -579,6 +579,8 @@ __global__ void __launch_bounds__(kThreads, M::kPerSm) attn_decode_kernel(AttnDe
             if (lane == 0) sh.on[warp][stage] = mask;
             const uint32_t row = on ? ((uint32_t)page * p.Hk + ahead.h) * p.page_size + off : 0u;  // below 2^32: checked
             const uint32_t dst = ring + stage * S::kStage;
+            GDR2_DCHECK(stage >= 0 && stage < S::kStages && ahead.n >= 0 && ahead.n < p.N && ahead.h >= 0 && ahead.h < p.Hk);
+            GDR2_DCHECK((uint64_t)row < (uint64_t)p.num_pages * p.Hk * p.page_size);
 #pragma unroll
             for (int i = 0; i < M::kTok * CH / 32; ++i) {
                 constexpr int kStep = 32 / CH;
@@ -621,6 +623,7 @@ __global__ void __launch_bounds__(kThreads, M::kPerSm) attn_decode_kernel(AttnDe
         if (++stage == S::kStages) stage = 0;
         if (cur.last() || x + 1 == end) {
             const bool whole = head_of_row && cur.last();
+            GDR2_DCHECK(cur.n < p.N && j0 >= 0 && j0 + heads <= p.Hq && heads > 0 && (whole || !ln.whole));
             const int slot = 2 * blockIdx.x + head_of_row;
             const int row = (cur.n * p.Hk + cur.h) * ln.nb + cur.blk;
             if (head_of_row && !whole && tid == 0) {
@@ -628,6 +631,7 @@ __global__ void __launch_bounds__(kThreads, M::kPerSm) attn_decode_kernel(AttnDe
                 const int done = (cur.first - cur.start) / TILE, nt = (cur.len - cur.start + TILE - 1) / TILE;
                 const long long e = (x - done + nt) * parts, k = (e + total - 1) / total - 1;
                 cut = make_int4(row, blockIdx.x, (int)(k - blockIdx.x) + 1, 0);
+                GDR2_DCHECK(k > blockIdx.x && k < gridDim.x);
             }
             if (head_of_row && w.by_row && tid == 0) w.cut[row] = whole ? make_int4(-1, 0, 0, 0) : cut;
             T *o = static_cast<T *>(p.o) + ((size_t)cur.n * p.Hq + j0) * D;
@@ -660,6 +664,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_decode_join_kernel(AttnDeco
     const int row = cut.x, c = cut.y, cnt = cut.z;
     if (row < 0) return;
     const int nh = row / ln.nb, blk = row - nh * ln.nb, n = nh / p.Hk, h = nh - n * p.Hk;
+    GDR2_DCHECK(n < p.N && c >= 0 && cnt > 1 && c + cnt <= kMaxCtas);
     const bool on = head < min(ln.rows, ln.G - blk * ln.rows);
     float m = -INFINITY, l = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -788,6 +793,8 @@ struct Bytes {
 size_t attn_decode_workspace_bytes(const AttnDecodeArgs &a) {
     return a.d == 128 ? dispatch<128>(a, Bytes{a}) : dispatch<64>(a, Bytes{a});
 }
+
+int status_take_attn_decode() { return take_status(); }
 
 cudaError_t launch_attn_decode(const AttnDecodeArgs &a, cudaStream_t st) {
     return a.d == 128 ? dispatch<128>(a, Run{a, st}) : dispatch<64>(a, Run{a, st});

@@ -213,6 +213,7 @@ __global__ void __launch_bounds__(kThreads, kFwdCtas) attn_prologue_fwd_kernel(A
     };
     if (ua < un.count) enter();
     auto fetch = [&](int slot) {
+        GDR2_DCHECK(slot >= 0 && slot < kFwdDepth);
         if (ua < un.count) {
             const bool on = ha < ea;
             const T *x = on ? src : static_cast<const T *>(p.xq);
@@ -254,6 +255,7 @@ __global__ void __launch_bounds__(kThreads, kFwdCtas) attn_prologue_fwd_kernel(A
     int slot = 0;
     for (; u < un.count; u += un.stride) {
         const int tok = un.token(u), h0 = un.part(u) * Y::kRows + grp;
+        GDR2_DCHECK(tok >= 0 && tok < p.T);
         int fpos = 0, fseq = 0, npage = -1;
         if (p.rot || kCache) fpos = p.pos[token(u + 2 * un.stride)];
         if constexpr (kCache) {
@@ -263,6 +265,7 @@ __global__ void __launch_bounds__(kThreads, kFwdCtas) attn_prologue_fwd_kernel(A
         fr.angles<D>(p, pos, sh.cs[warp], lane);
         const bool live = !kCache || (seq >= 0 && seq < p.R);
         const bool put = !kCache || (live && page >= 0 && page < p.num_pages);
+        GDR2_DCHECK(!kCache || !put || (pos >= 0 && pos - p.by_page.divide(pos) * p.page_size < (uint32_t)p.page_size));
         const long long hs = kCache ? (long long)p.page_size * D : D;  // from head to head where keys go
         const size_t at = kCache ? (put ? ((size_t)page * p.Hk * p.page_size + (pos - p.by_page.divide(pos) * p.page_size)) * D : 0) : (size_t)tok * p.Hk * D;
 #pragma unroll 1
@@ -373,6 +376,7 @@ __global__ void __launch_bounds__(kThreads, kBwdCtas) attn_prologue_bwd_kernel(A
     };
     if (ua < un.count) enter();
     auto fetch = [&](int slot) {
+        GDR2_DCHECK(slot >= 0 && slot < kBwdDepth);
         if (ua < un.count) {
             const bool on = ha < H, ox = on && p.norm;
             const T *g = on ? sd : dy, *r = on ? sr : x;
@@ -405,6 +409,7 @@ __global__ void __launch_bounds__(kThreads, kBwdCtas) attn_prologue_bwd_kernel(A
     int slot = 0;
     for (; u < un.count; u += un.stride) {
         const int tok = un.token(u), h0 = un.part(u) * Y::kRows + grp;
+        GDR2_DCHECK(tok >= 0 && tok < p.T && slot % kBwdBurst >= 0 && slot < kBwdDepth);
         const int npos = position(u + un.stride);
         fr.angles<D>(p, pos, sh.cs[warp], lane);
         Turn<T> t;
@@ -590,6 +595,8 @@ struct Bwd {
 }  // namespace
 
 size_t attn_prologue_workspace_bytes(int d) { return (size_t)kBwdGrid * d * sizeof(float); }
+
+int status_take_attn_prologue() { return take_status(); }
 
 cudaError_t launch_attn_prologue_fwd(const AttnPrologueArgs &a, cudaStream_t st) { return dispatch(a, Fwd{a, false, st}); }
 cudaError_t launch_attn_prologue_cache(const AttnPrologueArgs &a, cudaStream_t st) {

@@ -5,6 +5,7 @@
 // synchronises.
 #include <stdint.h>
 
+#include "attn.h"
 #include "gdr2.h"
 #include "kernels.h"
 #include "status.cuh"
@@ -103,7 +104,12 @@ int gdr2_check(void *stream) {
     const int a = gdr2::status_take_tc(), b = gdr2::status_take_simt(), c = gdr2::status_take_decode(),
               d = gdr2::status_take_chain();
     if (a < 0 || b < 0 || c < 0 || d < 0) return GDR2_ERR_CUDA;
-    const int bits = a | b | c | d;
+    int bits = a | b | c | d;
+#ifdef GDR2_DEBUG
+    const int e = gdr2::status_take_attn_prologue(), f = gdr2::status_take_attn_decode(), g = gdr2::status_take_kv_pages();
+    if (e < 0 || f < 0 || g < 0) return GDR2_ERR_CUDA;
+    bits |= e | f | g;
+#endif
     if (bits & gdr2::kStatusBounds) return GDR2_ERR_BOUNDS;
     if (bits & gdr2::kStatusTimeout) return GDR2_ERR_TIMEOUT;
     if (bits & gdr2::kStatusRange) return GDR2_ERR_RANGE;

@@ -163,6 +163,7 @@ __device__ __forceinline__ int free_page(const int *pages, const int *pre, int r
         else
             e = mid;
     }
+    GDR2_DCHECK(rank >= pre[a] && rank < pre[a + 1]);
     return __ldcg(pages + a * length + rank - pre[a]);
 }
 
@@ -195,6 +196,7 @@ __device__ __forceinline__ void copy_rows(int n, const int *src, const int *dst,
         const uint32_t y = x / pieces, piece = x - y * pieces, i = y / heads, hh = y - i * heads, h = hh >> 1;
         const long long bytes = rows ? (long long)__ldcg(rows + i) * bl.row_bytes : block;
         uint8_t *pool = hh & 1 ? bl.v : bl.k;
+        GDR2_DCHECK(i < (uint32_t)n && h < (uint32_t)bl.Hk && bytes <= block && __ldcg(src + i) != __ldcg(dst + i));
         const uint8_t *s = pool + ((long long)__ldcg(src + i) * bl.Hk + h) * block;
         uint8_t *d = pool + ((long long)__ldcg(dst + i) * bl.Hk + h) * block;
         const long long base = (long long)piece * kPiece + lane * 16;
@@ -292,6 +294,7 @@ __global__ void __launch_bounds__(kThreads) kv_reserve_kernel(KvPagesArgs a, Lis
             const int rank = rank0 + __popc(m & ((1u << t.lane) - 1));
             if (is && rank < all) {
                 const int page = free_page(w.pages, free, rank, t.warps, length);
+                GDR2_DCHECK(page >= 0 && page < a.num_pages);
                 a.table_out[b + 32 * x + t.lane] = page;
                 a.ref_out[page] = 1;
             }
@@ -400,6 +403,7 @@ __global__ void __launch_bounds__(kThreads) kv_fork_kernel(KvPagesArgs a, Lists 
             const int len = length(a.parent[r]), j = len / ps;
             if (rank < all) {
                 const int page = free_page(w.pages, free, rank, t.warps, each);
+                GDR2_DCHECK(page >= 0 && page < a.num_pages && j < a.P && rank < a.R);
                 a.table_out[r * a.P + j] = page;
                 a.ref_out[page] = 1;
                 w.src[rank] = src, w.dst[rank] = page, w.rows[rank] = len - j * ps;
@@ -470,12 +474,14 @@ __global__ void __launch_bounds__(kThreads) kv_compact_kernel(KvPagesArgs a, Lis
             const int lb = live0 + __popc(m & ((1u << t.lane) - 1));  // live pages before i
             if (i < pg.last) {
                 if (i < live) {
+                    GDR2_DCHECK(lb <= i);
                     if (is)
                         a.ref_out[i] = n[x];
                     else
                         w.pages[i - lb] = i;
                 } else {
                     w.rank[i] = is ? lb - below : -1;
+                    GDR2_DCHECK(!is || (lb >= below && lb - below < moves));
                     if (is)
                         w.high[lb - below] = i;
                     else
@@ -543,6 +549,8 @@ size_t kv_workspace_bytes(int R, int num_pages) {
     const size_t n = ((size_t)num_pages + 3) / 4 * 4, r = ((size_t)R + 3) / 4 * 4;
     return (3 * (size_t)kMaxWarps + 4 + 3 * n + 4 * r) * sizeof(int);
 }
+
+int status_take_kv_pages() { return take_status(); }
 
 cudaError_t launch_kv_reserve(const KvPagesArgs &a, cudaStream_t st) {
     const int c = cluster_size(a, false);
