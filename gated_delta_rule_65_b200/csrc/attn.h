@@ -74,7 +74,7 @@ struct KvPagesArgs {
     int R, P, num_pages, page_size, window, Hk, d, dtype;
     void *workspace;
 };
-size_t kv_workspace_bytes(int R, int num_pages);
+size_t kv_workspace_bytes(int R, int P, int num_pages);
 cudaError_t launch_kv_reserve(const KvPagesArgs &a, cudaStream_t st);
 cudaError_t launch_kv_fork(const KvPagesArgs &a, cudaStream_t st);
 cudaError_t launch_kv_compact(const KvPagesArgs &a, cudaStream_t st);

@@ -189,8 +189,8 @@ int gdr2_attn_decode(const void *q, const void *k_pages, const void *v_pages, co
     return done(gdr2::launch_attn_decode(a, (cudaStream_t)stream));
 }
 
-size_t gdr2_kv_workspace_bytes(int R, int num_pages) {
-    return R > 0 && num_pages > 0 ? gdr2::kv_workspace_bytes(R, num_pages) : 0;
+size_t gdr2_kv_workspace_bytes(int R, int P, int num_pages) {
+    return check_pages(R, P, 1, num_pages) == GDR2_OK ? gdr2::kv_workspace_bytes(R, P, num_pages) : 0;
 }
 
 int gdr2_kv_reserve(const int *table, const int *lens, const int *want, const int *ref, int *table_out, int *ref_out,
@@ -201,7 +201,7 @@ int gdr2_kv_reserve(const int *table, const int *lens, const int *want, const in
     if (window < 0 || !ok_num(table) || !ok_num(lens) || !ok_num(want) || !ok_num(ref) || !ok_num(table_out) ||
         !ok_num(ref_out) || !ok_num(missing))
         return GDR2_ERR_INVALID_ARG;
-    if (!ok_ptr(workspace) || workspace_bytes < gdr2::kv_workspace_bytes(R, num_pages)) return GDR2_ERR_WORKSPACE;
+    if (!ok_ptr(workspace) || workspace_bytes < gdr2::kv_workspace_bytes(R, P, num_pages)) return GDR2_ERR_WORKSPACE;
     gdr2::KvPagesArgs a{};
     a.table = table; a.lens = lens; a.want = want; a.ref = ref;
     a.table_out = table_out; a.ref_out = ref_out; a.count_out = missing;
@@ -220,7 +220,7 @@ int gdr2_kv_fork(const int *table, const int *lens, const int *ref, const int *p
         !ok_num(ref_out) || !ok_num(missing) || !ok_ptr(k_pages) || !ok_ptr(v_pages) || table_out == table ||
         lens_out == lens)
         return GDR2_ERR_INVALID_ARG;
-    if (!ok_ptr(workspace) || workspace_bytes < gdr2::kv_workspace_bytes(R, num_pages)) return GDR2_ERR_WORKSPACE;
+    if (!ok_ptr(workspace) || workspace_bytes < gdr2::kv_workspace_bytes(R, P, num_pages)) return GDR2_ERR_WORKSPACE;
     gdr2::KvPagesArgs a{};
     a.table = table; a.lens = lens; a.ref = ref; a.parent = parent;
     a.table_out = table_out; a.lens_out = lens_out; a.ref_out = ref_out; a.count_out = missing;
@@ -240,7 +240,7 @@ int gdr2_kv_compact(const int *table, const int *ref, int *table_out, int *ref_o
     if (!ok_num(table) || !ok_num(ref) || !ok_num(table_out) || !ok_num(ref_out) || !ok_num(live) || !ok_ptr(k_pages) ||
         !ok_ptr(v_pages))
         return GDR2_ERR_INVALID_ARG;
-    if (!ok_ptr(workspace) || workspace_bytes < gdr2::kv_workspace_bytes(R, num_pages)) return GDR2_ERR_WORKSPACE;
+    if (!ok_ptr(workspace) || workspace_bytes < gdr2::kv_workspace_bytes(R, P, num_pages)) return GDR2_ERR_WORKSPACE;
     gdr2::KvPagesArgs a{};
     a.table = table; a.ref = ref; a.table_out = table_out; a.ref_out = ref_out; a.count_out = live;
     a.k_pages = k_pages; a.v_pages = v_pages;

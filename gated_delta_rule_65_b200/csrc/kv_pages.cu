@@ -35,11 +35,14 @@ struct Lists {
     int *pages;      // [num_pages] each strip's free pages from its start on (compact: those below the live count, by rank)
     int *high;       // [num_pages] compact: live pages at or above the live count, by rank
     int *rank;       // [num_pages] compact: rank of such a page
+    int *needs;      // [R P / 32] reserve: which of 32 entries need a page, a bit each
     int *owner;      // [R] fork: who keeps a sequence's partly filled page
     int *src, *dst, *rows;  // [R] fork: copies
 };
 
-Lists lists(void *ws, int R, int num_pages) {
+size_t need_words(int R, int P) { return ((size_t)R * P + 31) / 32; }
+
+Lists lists(void *ws, int R, int P, int num_pages) {
     Lists w;
     int *p = static_cast<int *>(ws);
     auto take = [&](size_t n) {
@@ -49,6 +52,7 @@ Lists lists(void *ws, int R, int num_pages) {
     };
     w.ta = take(kMaxWarps), w.tb = take(kMaxWarps), w.tc = take(kMaxWarps), w.ncopy = take(4);
     w.pages = take(num_pages), w.high = take(num_pages), w.rank = take(num_pages);
+    w.needs = take(need_words(R, P));
     w.owner = take(R), w.src = take(R), w.dst = take(R), w.rows = take(R);
     return w;
 }
@@ -129,13 +133,14 @@ __device__ __forceinline__ int list_free(const int *ref, Strip s, int *list, int
     return c;
 }
 
-// pre[i] = t[0] + ... + t[i - 1], i <= warps (a multiple of 32); by one warp.
+// pre[i] = t[0] + ... + t[i - 1], i <= warps (a multiple of 32); by one warp. t: global memory, or shared memory where
+// the cluster is one CTA.
 __device__ __forceinline__ void prefix(const int *t, int warps, int *pre, int lane) {
     const int each = warps / 32;
     int v[kMaxWarps / 32], sum = 0;
 #pragma unroll
     for (int i = 0; i < kMaxWarps / 32; ++i) {
-        v[i] = i < each ? __ldcg(t + lane * each + i) : 0;
+        v[i] = i < each ? *static_cast<const volatile int *>(t + lane * each + i) : 0;
         sum += v[i];
     }
     int at = sum;
@@ -218,8 +223,16 @@ __global__ void __launch_bounds__(kThreads) kv_reserve_kernel(KvPagesArgs a, Lis
     const Place t = place();
     const int E = a.R * a.P, ps = a.page_size;
     follow();
-    __shared__ int need[kMaxWarps + 1], free[kMaxWarps + 1], past[kMaxWarps + 1];
+    __shared__ int need[kMaxWarps + 1], free[kMaxWarps + 1], past[kMaxWarps + 1], sums[3][kThreads / 32];
+    const bool one = gridDim.x == 1;
+    int *ta = one ? sums[0] : w.ta, *tb = one ? sums[1] : w.tb, *tc = one ? sums[2] : w.tc;
     const Strip es = strip(E, t.warp, t.warps), pg = strip(a.num_pages, t.warp, t.warps);
+    if (es.first + t.lane * 32 < es.last) {  // the entries' way to L2 overlaps that of the counts
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(a.table + es.first + t.lane * 32));
+        const int r = (es.first + t.lane * 32) / a.P;
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(a.lens + r));
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(a.want + r));
+    }
     // the counts are copied and free pages listed on the way; a window's releases change them, so then list later
     int nfree = list_free(a.ref, pg, w.pages, a.ref_out, t.lane);
     if (a.window > 0) cl.sync();
@@ -238,9 +251,11 @@ __global__ void __launch_bounds__(kThreads) kv_reserve_kernel(KvPagesArgs a, Lis
             want[x] = in ? __ldg(a.want + at.r) : 0;
             at.next(a.P);
         }
+        int words = 0;
 #pragma unroll
         for (int x = 0; x < kAhead; ++x) {
             const int i = b + 32 * x + t.lane;
+            bool is = false;
             if (i < es.last) {
                 e[x] = valid(e[x], a.num_pages);
                 len[x] = max(len[x], 0);
@@ -249,11 +264,14 @@ __global__ void __launch_bounds__(kThreads) kv_reserve_kernel(KvPagesArgs a, Lis
                     e[x] = -1;
                 }
                 a.table_out[i] = e[x];
-                c += e[x] < 0 && tok[x] + ps > len[x] && tok[x] < want[x];
+                is = e[x] < 0 && tok[x] + ps > len[x] && tok[x] < want[x];
             }
+            const int m = (int)__ballot_sync(0xffffffffu, is);
+            c += __popc(m);
+            words = t.lane == x ? m : words;
         }
+        if (t.lane < kAhead && b + 32 * t.lane < es.last) w.needs[b / 32 + t.lane] = words;  // strips start at whole words
     }
-    c = __reduce_add_sync(0xffffffffu, c);
     int over = 0;  // pages past the table's end
     for (int r = t.gid; r < a.R; r += t.threads) {
         const int want = a.want[r];
@@ -264,38 +282,26 @@ __global__ void __launch_bounds__(kThreads) kv_reserve_kernel(KvPagesArgs a, Lis
         cl.sync();
         nfree = list_free(a.ref_out, pg, w.pages, nullptr, t.lane);
     }
-    if (t.lane == 0) w.ta[t.warp] = c, w.tb[t.warp] = nfree, w.tc[t.warp] = over;
+    if (t.lane == 0) ta[t.warp] = c, tb[t.warp] = nfree, tc[t.warp] = over;
     cl.sync();
-    if (threadIdx.x < 32) prefix(w.ta, t.warps, need, t.lane);
-    if (threadIdx.x / 32 == 1) prefix(w.tb, t.warps, free, t.lane);
-    if (threadIdx.x / 32 == 2) prefix(w.tc, t.warps, past, t.lane);
+    if (threadIdx.x < 32) prefix(ta, t.warps, need, t.lane);
+    if (threadIdx.x / 32 == 1) prefix(tb, t.warps, free, t.lane);
+    if (threadIdx.x / 32 == 2) prefix(tc, t.warps, past, t.lane);
     __syncthreads();
     const int all = free[t.warps], length = strip_length(a.num_pages, t.warps);
     int rank0 = need[t.warp];
     if (t.gid == 0) *a.count_out = past[t.warps] + max(0, need[t.warps] - all);
     if (c == 0) return;
-    at = Cell(es.first + t.lane, a.P);
-    for (int b = es.first; b < es.last; b += 32 * kAhead) {
-        int e[kAhead], len[kAhead], want[kAhead], tok[kAhead];  // tok: the first token of the entry's page
-#pragma unroll
-        for (int x = 0; x < kAhead; ++x) {
-            const int i = b + 32 * x + t.lane;
-            const bool in = i < es.last;
-            tok[x] = at.j * ps;
-            e[x] = in ? __ldcg(a.table_out + i) : 0;
-            len[x] = in ? __ldg(a.lens + at.r) : 0;
-            want[x] = in ? __ldg(a.want + at.r) : 0;
-            at.next(a.P);
-        }
-#pragma unroll
-        for (int x = 0; x < kAhead; ++x) {
-            const bool is = e[x] < 0 && tok[x] + ps > max(len[x], 0) && tok[x] < want[x];
-            const unsigned m = __ballot_sync(0xffffffffu, is);
+    for (int g = es.first / 32; g * 32 < es.last; g += 32) {
+        const int mine = (g + t.lane) * 32 < es.last ? __ldcg(w.needs + g + t.lane) : 0;
+        for (unsigned some = __ballot_sync(0xffffffffu, mine != 0); some; some &= some - 1) {
+            const int x = __ffs(some) - 1;
+            const unsigned m = (unsigned)__shfl_sync(0xffffffffu, mine, x);
             const int rank = rank0 + __popc(m & ((1u << t.lane) - 1));
-            if (is && rank < all) {
+            if ((m >> t.lane & 1) && rank < all) {
                 const int page = free_page(w.pages, free, rank, t.warps, length);
-                GDR2_DCHECK(page >= 0 && page < a.num_pages);
-                a.table_out[b + 32 * x + t.lane] = page;
+                GDR2_DCHECK(page >= 0 && page < a.num_pages && (g + x) * 32 + t.lane < es.last);
+                a.table_out[(g + x) * 32 + t.lane] = page;
                 a.ref_out[page] = 1;
             }
             rank0 += __popc(m);
@@ -313,7 +319,9 @@ __global__ void __launch_bounds__(kThreads) kv_fork_kernel(KvPagesArgs a, Lists 
     follow();
     const Strip es = strip(E, t.warp, t.warps), pg = strip(a.num_pages, t.warp, t.warps), rs = strip(a.R, t.warp, t.warps);
     // who keeps a sequence's last page: up to kOwners sequences each CTA finds it for itself
-    __shared__ int need[kMaxWarps + 1], free[kMaxWarps + 1], owner_here[kOwners];
+    __shared__ int need[kMaxWarps + 1], free[kMaxWarps + 1], owner_here[kOwners], sums[2][kThreads / 32];
+    const bool one = gridDim.x == 1;
+    int *ta = one ? sums[0] : w.ta, *tb = one ? sums[1] : w.tb;
     const bool here = a.R <= kOwners;
     int *owner = here ? owner_here : w.owner;
     const int r0 = here ? threadIdx.x : t.gid, rn = here ? kThreads : t.threads;
@@ -384,10 +392,10 @@ __global__ void __launch_bounds__(kThreads) kv_fork_kernel(KvPagesArgs a, Lists 
     for (int b = rs.first; b < rs.last; b += 32) c += __popc(__ballot_sync(0xffffffffu, source(b + t.lane) >= 0));
     cl.sync();
     const int nfree = list_free(a.ref_out, pg, w.pages, nullptr, t.lane);
-    if (t.lane == 0) w.ta[t.warp] = c, w.tb[t.warp] = nfree;
+    if (t.lane == 0) ta[t.warp] = c, tb[t.warp] = nfree;
     cl.sync();
-    if (threadIdx.x < 32) prefix(w.ta, t.warps, need, t.lane);
-    if (threadIdx.x / 32 == 1) prefix(w.tb, t.warps, free, t.lane);
+    if (threadIdx.x < 32) prefix(ta, t.warps, need, t.lane);
+    if (threadIdx.x / 32 == 1) prefix(tb, t.warps, free, t.lane);
     __syncthreads();
     const int all = free[t.warps], needed = need[t.warps], each = strip_length(a.num_pages, t.warps);
     int rank0 = need[t.warp];
@@ -545,9 +553,9 @@ int copy_grid(const Blocks &bl, long long most) {
 
 }  // namespace
 
-size_t kv_workspace_bytes(int R, int num_pages) {
-    const size_t n = ((size_t)num_pages + 3) / 4 * 4, r = ((size_t)R + 3) / 4 * 4;
-    return (3 * (size_t)kMaxWarps + 4 + 3 * n + 4 * r) * sizeof(int);
+size_t kv_workspace_bytes(int R, int P, int num_pages) {
+    auto whole = [](size_t n) { return (n + 3) / 4 * 4; };
+    return (3 * (size_t)kMaxWarps + 4 + 3 * whole(num_pages) + whole(need_words(R, P)) + 4 * whole(R)) * sizeof(int);
 }
 
 int status_take_kv_pages() { return take_status(); }
@@ -556,12 +564,12 @@ cudaError_t launch_kv_reserve(const KvPagesArgs &a, cudaStream_t st) {
     const int c = cluster_size(a, false);
     cudaError_t e;
     GDR2_LAUNCH("kv_reserve", st,
-                e = launch(kv_reserve_kernel, dim3(c), dim3(kThreads), 0, c, st, a, lists(a.workspace, a.R, a.num_pages)));
+                e = launch(kv_reserve_kernel, dim3(c), dim3(kThreads), 0, c, st, a, lists(a.workspace, a.R, a.P, a.num_pages)));
     return e;
 }
 
 cudaError_t launch_kv_fork(const KvPagesArgs &a, cudaStream_t st) {
-    const Lists w = lists(a.workspace, a.R, a.num_pages);
+    const Lists w = lists(a.workspace, a.R, a.P, a.num_pages);
     const Blocks bl = blocks(a);
     const bool own = own_copy(bl, a.R);
     const int c = cluster_size(a, own);
@@ -575,7 +583,7 @@ cudaError_t launch_kv_fork(const KvPagesArgs &a, cudaStream_t st) {
 }
 
 cudaError_t launch_kv_compact(const KvPagesArgs &a, cudaStream_t st) {
-    const Lists w = lists(a.workspace, a.R, a.num_pages);
+    const Lists w = lists(a.workspace, a.R, a.P, a.num_pages);
     const Blocks bl = blocks(a);
     const long long most = a.num_pages / 2;  // a live page above for each free one below
     const bool own = own_copy(bl, most);

@@ -132,7 +132,7 @@ def lib(build_if_missing: bool = True) -> ctypes.CDLL:
             L.gdr2_attn_decode.restype = _I
             L.gdr2_attn_decode.argtypes = ([_VP] * 6 + [_F, _I, _VP, _VP] + [_I] * 9 + [_VP, ctypes.c_size_t, _VP])
             L.gdr2_kv_workspace_bytes.restype = ctypes.c_size_t
-            L.gdr2_kv_workspace_bytes.argtypes = [_I] * 2
+            L.gdr2_kv_workspace_bytes.argtypes = [_I] * 3
             L.gdr2_kv_reserve.restype = _I
             L.gdr2_kv_reserve.argtypes = [_VP] * 7 + [_I] * 5 + [_VP, ctypes.c_size_t, _VP]
             L.gdr2_kv_fork.restype = _I
@@ -811,7 +811,7 @@ def kv_reserve(table, lens, want, ref, *, page_size, window=0, out=None, workspa
     m = ref.new_empty(1) if m is None else m
     if stream is not None:
         _keep(stream, t, r, m)
-    workspace, nbytes = _scratch(ref, workspace, stream, "gdr2_kv_workspace_bytes", R, num)
+    workspace, nbytes = _scratch(ref, workspace, stream, "gdr2_kv_workspace_bytes", R, P, num)
     st = (_lib or lib()).gdr2_kv_reserve(
         table.data_ptr(), lens.data_ptr(), want.data_ptr(), ref.data_ptr(), t.data_ptr(), r.data_ptr(), m.data_ptr(),
         R, P, page_size, num, window, _p(workspace), nbytes, _raw_stream(stream, index))
@@ -839,7 +839,7 @@ def kv_fork(table, lens, ref, parent, k_pages, v_pages, *, out=None, workspace=N
     m = ref.new_empty(1) if m is None else m
     if stream is not None:
         _keep(stream, t, n, r, m)
-    workspace, nbytes = _scratch(ref, workspace, stream, "gdr2_kv_workspace_bytes", R, num)
+    workspace, nbytes = _scratch(ref, workspace, stream, "gdr2_kv_workspace_bytes", R, P, num)
     st = (_lib or lib()).gdr2_kv_fork(
         table.data_ptr(), lens.data_ptr(), ref.data_ptr(), parent.data_ptr(), t.data_ptr(), n.data_ptr(), r.data_ptr(),
         m.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), R, P, Hk, ps, d, num, dt, _p(workspace), nbytes,
@@ -864,7 +864,7 @@ def kv_compact(table, ref, k_pages, v_pages, *, out=None, workspace=None, stream
     m = ref.new_empty(1) if m is None else m
     if stream is not None:
         _keep(stream, t, r, m)
-    workspace, nbytes = _scratch(ref, workspace, stream, "gdr2_kv_workspace_bytes", R, num)
+    workspace, nbytes = _scratch(ref, workspace, stream, "gdr2_kv_workspace_bytes", R, P, num)
     st = (_lib or lib()).gdr2_kv_compact(
         table.data_ptr(), ref.data_ptr(), t.data_ptr(), r.data_ptr(), m.data_ptr(), k_pages.data_ptr(),
         v_pages.data_ptr(), R, P, Hk, ps, d, num, dt, _p(workspace), nbytes, _raw_stream(stream, index))

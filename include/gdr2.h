@@ -471,7 +471,7 @@ GDR2_API int gdr2_attn_decode(const void *q, const void *k_pages, const void *v_
  * table entries that name a page (a caller may add to it to pin one); a page with ref <= 0 is free. Free pages are
  * handed out lowest number first to entries in (r, j) order, so each call has exactly one result. Each call reads
  * table, lens and ref and writes the state after it to table_out, lens_out, ref_out; the workspace is
- * gdr2_kv_workspace_bytes(R, num_pages) bytes.
+ * gdr2_kv_workspace_bytes(R, P, num_pages) bytes.
  *
  * gdr2_kv_reserve: pages for tokens [lens[r], want[r]) of every sequence: the entries from the one of token lens[r]
  * to the one of token want[r] - 1 that have no page get one (want[r] <= lens[r] asks for none). With window > 0 the
@@ -490,7 +490,7 @@ GDR2_API int gdr2_attn_decode(const void *q, const void *k_pages, const void *v_
  * below. table_out and ref_out follow, live (int32 [1]) is written. table_out may be table and ref_out may be ref.
  * An entry that names a free page keeps its number.
  */
-GDR2_API size_t gdr2_kv_workspace_bytes(int R, int num_pages);
+GDR2_API size_t gdr2_kv_workspace_bytes(int R, int P, int num_pages);
 
 GDR2_API int gdr2_kv_reserve(const int *table, const int *lens, const int *want, const int *ref, int *table_out,
                              int *ref_out, int *missing, int R, int P, int page_size, int num_pages, int window,

@@ -114,9 +114,10 @@ def test_workspace_sizes():
     assert f(3, 8, 2, 64, 4, 16, 0, 1) == 0 and f(3, 8, 2, 64, 1000, 16, 64, 1) == 0  # short rows stay whole
     assert f(0, 8, 2, 64, 1000, 16, 0, 1) == 0 and f(3, 7, 2, 64, 1000, 16, 0, 1) == 0
     assert f(3, 8, 2, 96, 1000, 16, 0, 1) == 0 and f(3, 8, 2, 64, 1000, 16, -1, 1) == 0
-    assert L.gdr2_kv_workspace_bytes(3, 100) > 0
-    assert L.gdr2_kv_workspace_bytes(0, 100) == 0 and L.gdr2_kv_workspace_bytes(3, -1) == 0
-    assert L.gdr2_kv_workspace_bytes(1 << 20, 1 << 30) > 1 << 33  # more than 32 bits of bytes
+    f = L.gdr2_kv_workspace_bytes  # R, P, num_pages
+    assert 0 < f(3, 5, 100) < f(3, 500, 100)
+    assert f(0, 5, 100) == 0 and f(3, 5, -1) == 0 and f(3, 0, 100) == 0 and f(1 << 20, 1 << 12, 100) == 0
+    assert f(1 << 20, 5, 1 << 30) > 1 << 33  # more than 32 bits of bytes
 
 
 # ---- the binding ---------------------------------------------------------------------------------------------
