@@ -494,8 +494,12 @@ __global__ void __launch_bounds__(kThreads, M::kPerSm) attn_decode_kernel(AttnDe
     // (with fewer tiles than CTAs the first ones take one each: the join expects no empty CTA between two parts)
     const long long parts = min((long long)gridDim.x, total);
     long long edge[2];
-    edge[0] = blockIdx.x < parts ? total * blockIdx.x / parts : total;
-    edge[1] = blockIdx.x < parts ? total * (blockIdx.x + 1) / parts : total;
+    const bool small = total < (1 << 22);  // then a product with a CTA's number fits 32 bits, whose divisions are short
+    edge[0] = edge[1] = total;
+    if (blockIdx.x < parts) {
+        edge[0] = small ? (uint32_t)total * blockIdx.x / (uint32_t)parts : total * blockIdx.x / parts;
+        edge[1] = small ? (uint32_t)total * (blockIdx.x + 1) / (uint32_t)parts : total * (blockIdx.x + 1) / parts;
+    }
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
         if (edge[x] < total && edge[x] < pre && edge[x] >= pre - mine) {
@@ -527,7 +531,12 @@ __global__ void __launch_bounds__(kThreads, M::kPerSm) attn_decode_kernel(AttnDe
             for (int x = tid; x < p.Hq; x += kThreads) p.lse[(size_t)n * p.Hq + x] = -INFINITY;
     }
     __syncthreads();
-    int head_start = edge[0] < total ? (int)(sh.at[0] % sh.nt0[0]) : 0;  // tiles of its row before the run
+    // the row that the run begins in, and its tiles before the run
+    int first_row = 0, head_start = 0;
+    if (edge[0] < total) {
+        first_row = small ? (int)((uint32_t)sh.at[0] / (uint32_t)sh.nt0[0]) : (int)(sh.at[0] / sh.nt0[0]);
+        head_start = (int)(sh.at[0] - (long long)first_row * sh.nt0[0]);
+    }
     if (ln.whole) {  // a row belongs to the run that its first tile lies in
 #pragma unroll
         for (int x = 0; x < 2; ++x)
@@ -546,9 +555,8 @@ __global__ void __launch_bounds__(kThreads, M::kPerSm) attn_decode_kernel(AttnDe
     cur.n = sh.n0[0];
     cur.enter(p);
     {
-        const int hg = (int)(sh.at[0] / sh.nt0[0]);
-        cur.h = hg / ln.nb;
-        cur.blk = hg - cur.h * ln.nb;
+        cur.h = first_row / ln.nb;
+        cur.blk = first_row - cur.h * ln.nb;
         cur.first = cur.start + head_start * TILE;
         if (ln.whole && head_start) {
             cur.first = cur.len - 1;  // past the row that belongs to the run before
