@@ -48,8 +48,6 @@ __device__ __forceinline__ float sum2(F2 x) {
 template <typename T> struct Chunk {
     static constexpr int kElems = 16 / sizeof(T), kPairs = kElems / 2;
     uint4 v;
-    __device__ __forceinline__ void zero() { v = make_uint4(0, 0, 0, 0); }
-    __device__ __forceinline__ void load_stream(const T *p) { v = __ldcs(reinterpret_cast<const uint4 *>(p)); }
     __device__ __forceinline__ void put(T *p) const { *reinterpret_cast<uint4 *>(p) = v; }
     __device__ __forceinline__ void get(F2 (&x)[kPairs]) const {
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};

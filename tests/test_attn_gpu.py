@@ -358,6 +358,52 @@ def test_decode_slots_missing_pages_and_lengths_off_the_table(dt):
     assert (o[[4, 7]] == 0).all() and (lse[[4, 7]] == -math.inf).all()
 
 
+@pytest.mark.parametrize("dt,G", [("bf16", 4), ("bf16", 12), ("f32", 2), ("f32", 8)])
+@pytest.mark.parametrize("scale", [-0.3, 0.0, 1.7])
+def test_decode_scales(dt, G, scale):
+    """A negative scale turns the order of the scores, a scale of zero weighs all tokens alike."""
+    g = gen(26)
+    k, v, table, lens, _ = cache(g, [700, 1, 90], 16, 2, 64, DT[dt])
+    q = randn(g, 3, 2 * G, 64, dtype=DT[dt])
+    o, lse = gdr2.attn_decode(q, k, v, table, lens, scale=scale, want_lse=True)
+    ro, rl, to, tl, _ = ref.attention(q, k, v, table, lens, scale=scale)
+    ref.check("o", o, ro, to)
+    ref.check("lse", lse, rl, tl)
+
+
+def test_captured_behind_memsets_and_other_streams():
+    """Launches that follow a memset, a copy, and work of another stream inside one capture wait for all of them."""
+    g = gen(27)
+    k0, v0, table, lens, ref_ = cache(g, [600, 40], 16, 2, 64, torch.bfloat16)
+    q0 = randn(g, 2, 8, 64, dtype=torch.bfloat16)
+    k, v, q, n = torch.empty_like(k0), torch.empty_like(v0), torch.empty_like(q0), torch.empty_like(lens)
+    want = gdr2.attn_decode(q0, k0, v0, table, lens)
+    side = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        main = torch.cuda.current_stream()
+        k.zero_(), n.zero_()
+        k.copy_(k0)
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            for _ in range(20):
+                v.copy_(v0)
+            q.zero_()
+            q.copy_(q0)
+        n.copy_(lens)
+        main.wait_stream(side)
+        o = gdr2.attn_decode(q, k, v, table, n)
+        t, r, _ = gdr2.kv_reserve(table, n, n + 1, ref_, page_size=16)
+        o2 = gdr2.attn_decode(q, k, v, t, n)
+    for _ in range(3):
+        for x in (k, v, q):
+            x.fill_(math.nan)
+        n.fill_(-1)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(o, want) and torch.equal(o2, want)
+
+
 def test_decode_extreme_scores():
     """Scores of +-10^4 (one token takes all) and scores that are all equal."""
     g = gen(22)
