@@ -687,29 +687,30 @@ def attn_prologue_bwd(xq, xk, gq, gk, pos, freqs, dq, dk, *, norm=True, eps=1e-6
     return out
 
 
-def _pools(k_pages, v_pages):
-    shape = k_pages.shape
-    if len(shape) != 4:
-        raise ValueError("gdr2: k_pages must be [num_pages, Hk, page_size, d]")
-    if not (v_pages.shape == shape and v_pages.dtype is k_pages.dtype and k_pages.is_contiguous() and
-            v_pages.is_contiguous()):
-        _shaped("k_pages", k_pages, shape, k_pages.dtype), _shaped("v_pages", v_pages, shape, k_pages.dtype)
-    return shape
+def _fine(index, dtype, *tensors):
+    """Contiguous tensors of one dtype on device `index`."""
+    for t in tensors:
+        if t.dtype is not dtype or not t.is_contiguous() or t.get_device() != index:
+            return False
+    return True
 
 
-def _table(table):
-    shape = table.shape
-    if len(shape) != 2:
+def _refuse(dtype, pools, table, **ints):
+    """Names what is wrong with a cache's tensors: the pools (of this dtype, None: their own), the table, int32 arrays
+    name=(tensor, shape)."""
+    if pools is not None:
+        k_pages, v_pages = pools
+        if k_pages.dim() != 4:
+            raise ValueError("gdr2: k_pages must be [num_pages, Hk, page_size, d]")
+        _shaped("k_pages", k_pages, k_pages.shape, dtype or k_pages.dtype)
+        _shaped("v_pages", v_pages, k_pages.shape, k_pages.dtype)
+    if table.dim() != 2:
         raise ValueError("gdr2: table must be [R, P]")
-    if table.dtype is not _I32 or not table.is_contiguous():
-        _shaped("table", table, shape, _I32)
-    return shape
-
-
-def _ints(n, name, t):
-    """An int32 array of n values."""
-    if t.dtype is not _I32 or t.shape != (n,) or not t.is_contiguous():
-        _shaped(name, t, (n,), _I32)
+    _shaped("table", table, table.shape, _I32)
+    for name, (t, shape) in ints.items():
+        if t is not None:
+            _shaped(name, t, shape, _I32)
+    _device(table, *(pools or ()), *(t for t, _ in ints.values()))
 
 
 def attn_prologue_cache(xq, xk, xv, gq, gk, seq, pos, freqs, k_pages, v_pages, table, *, norm=True, eps=1e-6,
@@ -719,23 +720,26 @@ def attn_prologue_cache(xq, xk, xv, gq, gk, seq, pos, freqs, k_pages, v_pages, t
     [num_pages, Hk, page_size, d] by table int32 [R, P]; q is returned (padding rows as they were)."""
     T, Hq, Hk, d, sq, sk, dt, rot = _prologue_checks(xq, xk, gq, gk, pos, freqs, norm)
     Tv, Hv, dv, sv = _token_rows("xv", xv, xq.dtype)
-    num, Hp, ps, dp = _pools(k_pages, v_pages)
-    R, P = _table(table)
-    if Tv != T or Hv != Hk or dv != d or Hp != Hk or dp != d or k_pages.dtype is not xq.dtype:
-        raise ValueError("gdr2: xk, xv and the pools must agree in tokens, heads, channels and dtype")
     if pos is None:
         raise ValueError("gdr2: pos is needed to find a token's page")
     if freqs is None and (pos.dtype is not _I32 or pos.numel() != T or not pos.is_contiguous()):
         raise ValueError("gdr2: pos must hold one int32 position for each token")
-    _ints(T, "seq", seq)
+    shape, tshape, index = k_pages.shape, table.shape, xq.get_device()
+    if not (len(shape) == 4 and v_pages.shape == shape and len(tshape) == 2 and seq.shape == (T,) and
+            _fine(index, xq.dtype, k_pages, v_pages) and _fine(index, _I32, table, seq)):
+        _refuse(xq.dtype, (k_pages, v_pages), table, seq=(seq, (T,)))
+    num, Hp, ps, dp = shape
+    R, P = tshape
+    if Tv != T or Hv != Hk or dv != d or Hp != Hk or dp != d:
+        raise ValueError("gdr2: xk, xv and the pools must agree in tokens, heads and channels")
     if q is None:
-        index = _device(xq, xk, xv, gq, gk, seq, pos, freqs, k_pages, v_pages, table)
+        _device(xq, xk, xv, gq, gk, pos, freqs)
         q = torch.empty_like(xq)
         if stream is not None:
             _keep(stream, q)
     else:
         _shaped("q", q, xq.shape, xq.dtype)
-        index = _device(xq, xk, xv, gq, gk, seq, pos, freqs, k_pages, v_pages, table, q)
+        _device(xq, xk, xv, gq, gk, pos, freqs, q)
     st = (_lib or lib()).gdr2_attn_prologue_cache(
         xq.data_ptr(), xk.data_ptr(), xv.data_ptr(), _p(gq), _p(gk), 1 if norm else 0, eps, seq.data_ptr(),
         pos.data_ptr(), _p(freqs), mag, rot, 1 if interleaved else 0, q.data_ptr(), k_pages.data_ptr(),
@@ -750,25 +754,26 @@ def attn_decode(q, k_pages, v_pages, table, lens, seq=None, *, scale=None, windo
     """gdr2_attn_decode: attention of one new token for each row of q [N, Hq, d] over sequence seq[n] (int32 [N];
     None: n) of the cache, its last `window` tokens (0: all), lens int32 [R] with the new token counted. scale: by
     default d^-1/2. Returns o [N, Hq, d], or (o, lse fp32 [N, Hq]) with want_lse or a given lse."""
-    shape, dtype = q.shape, q.dtype
-    dt = _dtype_code(q)
-    if len(shape) != 3 or not q.is_contiguous():
+    dtype, dt = q.dtype, _dtype_code(q)
+    qshape, shape, tshape, index = q.shape, k_pages.shape, table.shape, q.get_device()
+    if len(qshape) != 3 or not q.is_contiguous():
         raise ValueError("gdr2: q must be a contiguous [N, Hq, d]")
-    N, Hq, d = shape
-    num, Hk, ps, dp = _pools(k_pages, v_pages)
-    R, P = _table(table)
-    if dp != d or k_pages.dtype is not dtype:
-        raise ValueError("gdr2: q and the pools must agree in channels and dtype")
-    _ints(R, "lens", lens)
-    if seq is not None:
-        _ints(N, "seq", seq)
-    index = _device(q, k_pages, v_pages, table, lens, seq, o, lse)
+    N, Hq, d = qshape
+    if not (len(shape) == 4 and v_pages.shape == shape and len(tshape) == 2 and lens.shape == tshape[:1] and
+            (seq is None or (seq.shape == qshape[:1] and _fine(index, _I32, seq))) and
+            _fine(index, dtype, k_pages, v_pages) and _fine(index, _I32, table, lens)):
+        _refuse(dtype, (k_pages, v_pages), table, lens=(lens, tshape[:1]), seq=(seq, qshape[:1]))
+    num, Hk, ps, dp = shape
+    R, P = tshape
+    if dp != d:
+        raise ValueError("gdr2: q and the pools must agree in channels")
+    _device(q, o, lse)
     if o is None:
         o = torch.empty_like(q)
         if stream is not None:
             _keep(stream, o)
     else:
-        _shaped("o", o, shape, dtype)
+        _shaped("o", o, qshape, dtype)
     if lse is not None:
         _shaped("lse", lse, (N, Hq), _F32)
     elif want_lse:
@@ -798,11 +803,12 @@ def _given(out, name, like, shape):
 def kv_reserve(table, lens, want, ref, *, page_size, window=0, out=None, workspace=None, stream=None):
     """gdr2_kv_reserve: pages for tokens [lens[r], want[r]) of every sequence (pages behind the window released
     first). Returns (table, ref, missing int32 [1]) after the call; `out` may name them (also the inputs)."""
-    R, P = _table(table)
-    _ints(R, "lens", lens), _ints(R, "want", want)
-    num = ref.numel()
-    _ints(num, "ref", ref)
-    index = _device(table, lens, want, ref)
+    shape, rows, index, num = table.shape, table.shape[:1], table.get_device(), ref.numel()
+    if not (len(shape) == 2 and lens.shape == rows and want.shape == rows and ref.dim() == 1 and
+            _fine(index, _I32, table, lens, want, ref)):
+        _refuse(None, None, table, lens=(lens, rows), want=(want, rows), ref=(ref, (num,)))
+    R, P = shape
+    _device(table)
     t = r = m = None
     if out is not None:
         t, r, m = _given(out, "table", ref, (R, P)), _given(out, "ref", ref, (num,)), _given(out, "missing", ref, (1,))
@@ -823,12 +829,13 @@ def kv_reserve(table, lens, want, ref, *, page_size, window=0, out=None, workspa
 def kv_fork(table, lens, ref, parent, k_pages, v_pages, *, out=None, workspace=None, stream=None):
     """gdr2_kv_fork: sequence r takes over the content of sequence parent[r] (int32 [R]; r: stays, outside [0, R):
     released). Partly filled last pages are copied in the pools. Returns (table, lens, ref, missing int32 [1])."""
-    R, P = _table(table)
-    num, Hk, ps, d = _pools(k_pages, v_pages)
-    _ints(R, "lens", lens), _ints(R, "parent", parent)
-    _ints(num, "ref", ref)
-    dt = _dtype_code(k_pages)
-    index = _device(table, lens, ref, parent, k_pages, v_pages)
+    shape, rows, pool, index, dt = table.shape, table.shape[:1], k_pages.shape, table.get_device(), _dtype_code(k_pages)
+    if not (len(shape) == 2 and len(pool) == 4 and v_pages.shape == pool and lens.shape == rows and
+            parent.shape == rows and ref.shape == pool[:1] and _fine(index, _I32, table, lens, parent, ref) and
+            _fine(index, k_pages.dtype, k_pages, v_pages)):
+        _refuse(None, (k_pages, v_pages), table, lens=(lens, rows), parent=(parent, rows), ref=(ref, pool[:1]))
+    (R, P), (num, Hk, ps, d) = shape, pool
+    _device(table)
     t = n = r = m = None
     if out is not None:
         t, n = _given(out, "table", ref, (R, P)), _given(out, "lens", ref, (R,))
@@ -851,11 +858,12 @@ def kv_fork(table, lens, ref, parent, k_pages, v_pages, *, out=None, workspace=N
 
 def kv_compact(table, ref, k_pages, v_pages, *, out=None, workspace=None, stream=None):
     """gdr2_kv_compact: the live pages moved to [0, live). Returns (table, ref, live int32 [1])."""
-    R, P = _table(table)
-    num, Hk, ps, d = _pools(k_pages, v_pages)
-    _ints(num, "ref", ref)
-    dt = _dtype_code(k_pages)
-    index = _device(table, ref, k_pages, v_pages)
+    shape, pool, index, dt = table.shape, k_pages.shape, table.get_device(), _dtype_code(k_pages)
+    if not (len(shape) == 2 and len(pool) == 4 and v_pages.shape == pool and ref.shape == pool[:1] and
+            _fine(index, _I32, table, ref) and _fine(index, k_pages.dtype, k_pages, v_pages)):
+        _refuse(None, (k_pages, v_pages), table, ref=(ref, pool[:1]))
+    (R, P), (num, Hk, ps, d) = shape, pool
+    _device(table)
     t = r = m = None
     if out is not None:
         t, r, m = _given(out, "table", ref, (R, P)), _given(out, "ref", ref, (num,)), _given(out, "live", ref, (1,))

@@ -128,7 +128,7 @@ def bf(*shape):
 
 
 def i32(*shape):
-    return torch.zeros(*shape, dtype=torch.int32)
+    return torch.zeros(shape, dtype=torch.int32)
 
 
 def test_binding_refuses_wrong_shapes_before_it_looks_at_devices():
@@ -156,6 +156,14 @@ def test_binding_refuses_wrong_shapes_before_it_looks_at_devices():
         lambda: gdr2.attn_decode(bf(3, 4, 64), bf(9, 2, 16, 128), bf(9, 2, 16, 128), i32(3, 5), i32(3)),
         lambda: gdr2.attn_decode(bf(3, 4, 64), bf(9, 2, 16, 64), bf(9, 2, 16, 64), i32(3, 5), i32(2)),
         lambda: gdr2.attn_decode(bf(3, 4, 64), bf(9, 2, 16, 64), bf(9, 2, 16, 64), i32(15), i32(3)),
+        lambda: gdr2.attn_decode(bf(3, 4, 64), bf(9, 2, 16, 64), bf(9, 2, 16, 64), i32(), i32(3)),
+        lambda: gdr2.attn_decode(bf(3, 256), bf(9, 2, 16, 64), bf(9, 2, 16, 64), i32(3, 5), i32(3)),
+        lambda: gdr2.attn_decode(bf(3, 4, 64), bf(9, 32, 64), bf(9, 32, 64), i32(3, 5), i32(3)),
+        lambda: gdr2.attn_decode(bf(3, 4, 64), bf(9, 2, 16, 64), bf(9, 2, 16, 64), i32(3, 5), i32(3), i32(4)),
+        lambda: gdr2.attn_decode(bf(3, 4, 64), bf(9, 2, 32, 64)[:, :, ::2], bf(9, 2, 16, 64), i32(3, 5), i32(3)),
+        lambda: gdr2.kv_reserve(i32(15), i32(3), i32(3), i32(9), page_size=16),
+        lambda: gdr2.kv_compact(i32(), i32(9), bf(9, 2, 16, 64), bf(9, 2, 16, 64)),
+        lambda: gdr2.kv_fork(i32(3, 5), i32(3), i32(9), i32(3), bf(9, 2, 1024), bf(9, 2, 1024)),
         lambda: gdr2.attn_decode(bf(3, 4, 64), bf(9, 2, 16, 64), bf(9, 2, 16, 64), i32(5, 3).t(), i32(3)),
         lambda: gdr2.kv_reserve(i32(3, 5), i32(3), i32(4), i32(9), page_size=16),
         lambda: gdr2.kv_fork(i32(3, 5), i32(3), i32(9), i32(2), bf(9, 2, 16, 64), bf(9, 2, 16, 64)),
@@ -177,6 +185,9 @@ def test_binding_refuses_wrong_shapes_before_it_looks_at_devices():
         lambda: gdr2.attn_prologue_fwd(x, y, torch.ones(64).double(), None, pos, fr),
         lambda: gdr2.attn_decode(bf(3, 4, 64), bf(9, 2, 16, 64), bf(9, 2, 16, 64), i32(3, 5).long(), i32(3)),
         lambda: gdr2.kv_reserve(i32(3, 5), i32(3).long(), i32(3), i32(9), page_size=16),
+        lambda: gdr2.attn_decode(bf(3, 4, 64), bf(9, 2, 16, 64).float(), bf(9, 2, 16, 64).float(), i32(3, 5), i32(3)),
+        lambda: gdr2.kv_compact(i32(3, 5), i32(9), bf(9, 2, 16, 64).half(), bf(9, 2, 16, 64).half()),
+        lambda: gdr2.kv_fork(i32(3, 5), i32(3), i32(9), i32(3).long(), bf(9, 2, 16, 64), bf(9, 2, 16, 64)),
     ]
     for f in wrong_type:
         with pytest.raises(TypeError):
