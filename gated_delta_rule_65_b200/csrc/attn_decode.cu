@@ -143,6 +143,7 @@ template <int TILE> struct Place {
 template <int D, bool kPacked> struct Bf16Math {
     using T = __nv_bfloat16;
     static constexpr int kTok = 16, kRows = kPacked ? 8 : 16, kRowBytes = 2 * D, kStats = kPacked ? 1 : 2, kPerSm = 2;
+    static constexpr int kCols = D;  // columns merged at a time
     uint32_t a[D / 16][4];
     float o[D / 8][4], m[kStats], ms[kStats], l[kStats];
     static __device__ __forceinline__ int swizzle(int row) { return row & 7; }
@@ -241,7 +242,7 @@ template <int D, bool kPacked> struct Bf16Math {
             }
         }
     }
-    // The warp's statistics (m in units of log2), and half of its output's columns, for the merge: wo [kRows][D / 2].
+    // The warp's statistics (m in units of log2), and columns [C0, C0 + kCols) of its output, for the merge: wo [kRows][kCols].
     __device__ __forceinline__ void stats(float *wm, float *wl, int lane) {
         const int g = lane >> 2, t = lane & 3;
 #pragma unroll
@@ -252,16 +253,16 @@ template <int D, bool kPacked> struct Bf16Math {
             if (t == 0) wm[g + 8 * h] = m[h] == -INFINITY ? -INFINITY : ms[h], wl[g + 8 * h] = x;
         }
     }
-    template <int HALF> __device__ __forceinline__ void put(float *wo, int lane) {
+    template <int C0> __device__ __forceinline__ void put(float *wo, int lane) {
         const int g = lane >> 2, t = lane & 3;
 #pragma unroll
-        for (int j = 0; j < D / 16; ++j) {
-            const float(&c)[4] = o[HALF * (D / 16) + j];
+        for (int j = 0; j < kCols / 8; ++j) {
+            const float(&c)[4] = o[C0 / 8 + j];
             if constexpr (kPacked) {
-                *reinterpret_cast<float2 *>(wo + g * (D / 2) + 8 * j + 2 * t) = make_float2(c[0] + c[2], c[1] + c[3]);
+                *reinterpret_cast<float2 *>(wo + g * kCols + 8 * j + 2 * t) = make_float2(c[0] + c[2], c[1] + c[3]);
             } else {
-                *reinterpret_cast<float2 *>(wo + g * (D / 2) + 8 * j + 2 * t) = make_float2(c[0], c[1]);
-                *reinterpret_cast<float2 *>(wo + (g + 8) * (D / 2) + 8 * j + 2 * t) = make_float2(c[2], c[3]);
+                *reinterpret_cast<float2 *>(wo + g * kCols + 8 * j + 2 * t) = make_float2(c[0], c[1]);
+                *reinterpret_cast<float2 *>(wo + (g + 8) * kCols + 8 * j + 2 * t) = make_float2(c[2], c[3]);
             }
         }
     }
@@ -273,6 +274,7 @@ template <int D, bool kPacked> struct Bf16Math {
 template <int D, int GB> struct F32Math {
     using T = float;
     static constexpr int kTok = 1024 / D, kRows = GB, kRowBytes = 4 * D, kPer = kTok / 8, kPerSm = GB <= 4 ? 3 : 2;
+    static constexpr int kCols = D / 2;  // columns merged at a time: all of them leave no room for a third CTA
     static constexpr int kHeads = (GB + 3) / 4;  // heads whose statistics a lane keeps: t, t + 4
     static constexpr int kLanes = D / 4;         // lanes of an output row
     float4 o[GB];
@@ -402,18 +404,18 @@ template <int D, int GB> struct F32Math {
             }
         }
     }
-    template <int HALF> __device__ __forceinline__ void put(float *wo, int lane) {
-        const int c = lane - HALF * (D / 8);
-        if (c < 0 || c >= D / 8) return;
+    template <int C0> __device__ __forceinline__ void put(float *wo, int lane) {
+        const int c = lane - C0 / 4;
+        if (c < 0 || c >= kCols / 4) return;
 #pragma unroll
-        for (int h = 0; h < GB; ++h) *reinterpret_cast<float4 *>(wo + h * (D / 2) + 4 * c) = o[h];
+        for (int h = 0; h < GB; ++h) *reinterpret_cast<float4 *>(wo + h * kCols + 4 * c) = o[h];
     }
 };
 
 template <int D, typename M> struct Shared {
     static constexpr int kStage = 2 * M::kTok * M::kRowBytes, kStages = kRing / kStage;
     alignas(1024) uint8_t ring[kWarps][kStages][kStage];
-    alignas(16) float merge[kWarps][M::kRows][D / 2];
+    alignas(16) float merge[kWarps][M::kRows][M::kCols];
     float wm[kWarps][M::kRows], wl[kWarps][M::kRows];
     uint32_t on[kWarps][kStages];
     alignas(16) float q[sizeof(typename M::T) == 4 ? M::kRows * D : 4];
@@ -426,14 +428,14 @@ template <int D, typename M> struct Shared {
 template <typename T> __device__ __forceinline__ void store_out(T *p, float4 v) { store4(p, v); }
 
 // One row's result in this CTA from its warps' parts: finished (whole) or left in the workspace (slot).
-template <int D, typename M, int HALF>
-__device__ __forceinline__ void merge_half(Shared<D, M> &sh, M &math, typename M::T *o, float *lse, int heads,
+template <int D, typename M, int C0>
+__device__ __forceinline__ void merge_columns(Shared<D, M> &sh, M &math, typename M::T *o, float *lse, int heads,
                                            bool whole, float *part, float *ml, int warp, int lane) {
-    if (HALF == 0) math.stats(sh.wm[warp], sh.wl[warp], lane);
-    math.template put<HALF>(&sh.merge[warp][0][0], lane);
+    if (C0 == 0) math.stats(sh.wm[warp], sh.wl[warp], lane);
+    math.template put<C0>(&sh.merge[warp][0][0], lane);
     __syncthreads();
-    for (int x = threadIdx.x; x < M::kRows * (D / 8); x += kThreads) {
-        const int row = x / (D / 8), c = 4 * (x % (D / 8));
+    for (int x = threadIdx.x; x < M::kRows * (M::kCols / 4); x += kThreads) {
+        const int row = x / (M::kCols / 4), c = 4 * (x % (M::kCols / 4));
         if (row >= heads) break;
         float mx = sh.wm[0][row];
 #pragma unroll
@@ -447,14 +449,14 @@ __device__ __forceinline__ void merge_half(Shared<D, M> &sh, M &math, typename M
             s.x = fmaf(f, y.x, s.x), s.y = fmaf(f, y.y, s.y), s.z = fmaf(f, y.z, s.z), s.w = fmaf(f, y.w, s.w);
             l = fmaf(f, sh.wl[w][row], l);
         }
-        const int col = HALF * (D / 2) + c;
+        const int col = C0 + c;
         if (whole) {
             const float i = l == 0.f ? 0.f : 1.f / l;  // no token left: zeros
             store_out(o + (size_t)row * D + col, make_float4(s.x * i, s.y * i, s.z * i, s.w * i));
-            if (HALF == 0 && c == 0 && lse) lse[row] = (mx + log2f(l)) * kLn2;
+            if (C0 == 0 && c == 0 && lse) lse[row] = (mx + log2f(l)) * kLn2;
         } else {
             *reinterpret_cast<float4 *>(part + (size_t)row * D + col) = s;
-            if (HALF == 0 && c == 0) ml[2 * row] = mx, ml[2 * row + 1] = l;
+            if (C0 == 0 && c == 0) ml[2 * row] = mx, ml[2 * row + 1] = l;
         }
     }
     __syncthreads();
@@ -652,8 +654,8 @@ __global__ void __launch_bounds__(kThreads, M::kPerSm) attn_decode_kernel(AttnDe
             T *o = static_cast<T *>(p.o) + ((size_t)cur.n * p.Hq + j0) * D;
             float *lse = p.lse ? p.lse + (size_t)cur.n * p.Hq + j0 : nullptr;
             float *part = w.o + (size_t)slot * kMaxRows * D, *ml = w.ml + (size_t)slot * kMaxRows * 2;
-            merge_half<D, M, 0>(sh, math, o, lse, heads, whole, part, ml, warp, lane);
-            merge_half<D, M, 1>(sh, math, o, lse, heads, whole, part, ml, warp, lane);
+            merge_columns<D, M, 0>(sh, math, o, lse, heads, whole, part, ml, warp, lane);
+            if constexpr (M::kCols < D) merge_columns<D, M, D / 2>(sh, math, o, lse, heads, whole, part, ml, warp, lane);
             fresh = true;
         }
         if (x + 1 < end) cur.next(p, ln);
