@@ -34,11 +34,12 @@ namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 // CTAs on an SM and rows of a lane in flight, measured on the training batch (B = 8, T = 4096, 16 + 16 heads of 128
-// channels, bf16), kernel times with their events (about 3 us). Forward, 2 CTAs: 90 us with 8 rows, 91 with 5; 3 CTAs:
-// 118 to 130 us with 4 to 8 rows (spills, and more warps on more tokens scatter the requests). Backward, 2 CTAs: 173 us
+// channels, bf16), kernel times with their events (about 3 us). Forward, 2 CTAs: 92 us with 4 to 8 rows (and 16 packed
+// prompts into the cache 49.1 us with 4, 49.9 with 8); 3 CTAs: 118 to 130 us with 4 to 8 rows (spills, and more warps on
+// more tokens scatter the requests). Backward, 2 CTAs: 173 us
 // fetching row by row (4 rows ahead), 141 in bursts of 2 and 145 of 3; 1 CTA: 149 row by row, 143 and 146 in bursts of
 // 2 and 4.
-constexpr int kFwdCtas = 2, kFwdDepth = 8;
+constexpr int kFwdCtas = 2, kFwdDepth = 4;
 constexpr int kBwdCtas = 2, kBwdBurst = 2, kBwdDepth = 2 * kBwdBurst;
 constexpr int kBwdGrid = kBwdCtas * kAttnSms;  // CTAs of the backward (a partial sum of dgq or dgk each)
 

@@ -87,18 +87,6 @@ struct Cell {
     }
 };
 
-// Sum of t[0 .. warp) and of all t; every warp on its own. t was written before the cluster's last barrier.
-__device__ __forceinline__ void before(const int *t, int warp, int warps, int lane, int &pre, int &total) {
-    int a = 0, b = 0;
-    for (int i = lane; i < warps; i += 32) {
-        const int v = __ldcg(t + i);
-        b += v;
-        if (i < warp) a += v;
-    }
-    pre = __reduce_add_sync(0xffffffffu, a);
-    total = __reduce_add_sync(0xffffffffu, b);
-}
-
 __device__ __forceinline__ int valid(int e, int num_pages) { return e >= 0 && e < num_pages ? e : -1; }
 __device__ __forceinline__ int entry(const int *table, int at, int num_pages) { return valid(__ldcg(table + at), num_pages); }
 
@@ -458,17 +446,19 @@ __global__ void __launch_bounds__(kThreads) kv_compact_kernel(KvPagesArgs a, Lis
     const Place t = place();
     follow();
     const Strip pg = strip(a.num_pages, t.warp, t.warps);
+    __shared__ int pre[kMaxWarps + 1], sums[kThreads / 32];
+    int *ta = gridDim.x == 1 ? sums : w.ta;
     const int nf = count_free(a.ref, pg, t.lane);
-    if (t.lane == 0) w.ta[t.warp] = pg.last - pg.first - nf;
+    if (t.lane == 0) ta[t.warp] = pg.last - pg.first - nf;
     cl.sync();
-    int live0, live;  // live pages before this strip, and in all
-    before(w.ta, t.warp, t.warps, t.lane, live0, live);
+    if (threadIdx.x < 32) prefix(ta, t.warps, pre, t.lane);
+    __syncthreads();
+    int live0 = pre[t.warp];          // live pages before this strip
+    const int live = pre[t.warps];
     // live pages below number `live`: those of the strips before the one that holds it, and of its first part
     const int len = strip_length(a.num_pages, t.warps), mid = live / len;
-    int below, all;
-    before(w.ta, mid, t.warps, t.lane, below, all);
     const Strip part{mid * len, live};
-    below += live - part.first - count_free(a.ref, part, t.lane);
+    const int below = pre[mid] + live - part.first - count_free(a.ref, part, t.lane);
     const int moves = live - below;  // as many live above as free below
     for (int b = pg.first; b < pg.last; b += 32 * kAhead) {
         int n[kAhead];
