@@ -31,6 +31,7 @@
 #include <math.h>
 
 #include "attn.h"
+#include "attn_vec.cuh"
 #include "common.cuh"
 #include "kernels.h"
 
@@ -268,59 +269,63 @@ template <int D, bool kPacked> struct Bf16Math {
     }
 };
 
-// The products of one warp's tile, fp32: GB query heads against kTok tokens (4 KB of K). Scores: four lanes of a token
-// take 16-byte chunks t, t + 4, ... of its row, each lane one token of every eight. Output: a lane owns four channels
-// (d = 64: of every other token).
+// The products of one warp's tile, fp32: GB query heads against kTok tokens (4 KB of K), on pairs of floats. Scores: four
+// lanes of a token take 16-byte chunks t, t + 4, ... of its row, each lane one token of every eight, and the exchange
+// that adds their parts leaves lane t with heads t, t + 4, ... Output: a lane owns four channels (d = 64: of every other
+// token).
 template <int D, int GB> struct F32Math {
     using T = float;
     static constexpr int kTok = 1024 / D, kRows = GB, kRowBytes = 4 * D, kPer = kTok / 8, kPerSm = GB <= 4 ? 3 : 2;
     static constexpr int kCols = D / 2;  // columns merged at a time: all of them leave no room for a third CTA
-    static constexpr int kHeads = (GB + 3) / 4;  // heads whose statistics a lane keeps: t, t + 4
+    static constexpr int kHeads = (GB + 3) / 4;  // heads whose statistics a lane keeps
     static constexpr int kLanes = D / 4;         // lanes of an output row
-    float4 o[GB];
+    F2 o[GB][2];
     float m[kHeads], ms[kHeads], l[kHeads];
     // rows 2 i and 2 i + 1 share a quarter-warp's access to four neighbouring chunks: bit 2 keeps them apart
     static __device__ __forceinline__ int swizzle(int row) { return ((row & 1) << 2) | ((row >> 1) & 3); }
+    static __device__ __forceinline__ void load(const void *p, F2 (&x)[2]) {
+        const ulonglong2 v = *reinterpret_cast<const ulonglong2 *>(p);
+        x[0].v = v.x, x[1].v = v.y;
+    }
     __device__ __forceinline__ void begin(const T *q, int heads, float scale, float *sq, int) {
         const float sign = scale < 0.f ? -1.f : scale == 0.f ? 0.f : 1.f;
         for (int x = threadIdx.x; x < GB * D; x += kThreads) sq[x] = x / D < heads && scale != 0.f ? sign * q[x] : 0.f;
 #pragma unroll
-        for (int h = 0; h < GB; ++h) o[h] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int h = 0; h < GB; ++h) o[h][0] = o[h][1] = f2(0.f, 0.f);
 #pragma unroll
         for (int i = 0; i < kHeads; ++i) m[i] = -INFINITY, ms[i] = 0.f, l[i] = 0.f;
         __syncthreads();
     }
-    // sp: the warp's probabilities [kTok][GB] and factors [GB]
+    // Sums over the four lanes of a token of four heads' parts; lane t gets head t's.
+    static __device__ __forceinline__ float spread(float a0, float a1, float a2, float a3, int t) {
+        const bool b0 = t & 1, b1 = t & 2;
+        float x = b0 ? a1 : a0, y = b0 ? a3 : a2;
+        x += __shfl_xor_sync(0xffffffffu, b0 ? a0 : a1, 1);
+        y += __shfl_xor_sync(0xffffffffu, b0 ? a2 : a3, 1);
+        const float z = b1 ? y : x;
+        return z + __shfl_xor_sync(0xffffffffu, b1 ? x : y, 2);
+    }
+    // sp: the warp's probabilities [kTok][GB] and factors [GB], each twice side by side
     __device__ __forceinline__ void step(uint32_t stage, uint32_t on, float sc, const float *sq, float *sp, int lane) {
         const int g = lane >> 2, t = lane & 3;
         const char *k = reinterpret_cast<const char *>(__cvta_shared_to_generic(stage)) + g * kRowBytes;
         const char *v = reinterpret_cast<const char *>(__cvta_shared_to_generic(stage)) + kTok * kRowBytes;
-        float s[kPer][GB];
-#pragma unroll
-        for (int y = 0; y < kPer; ++y)
-#pragma unroll
-            for (int h = 0; h < GB; ++h) s[y][h] = 0.f;
+        float2 *pp = reinterpret_cast<float2 *>(sp);
+        F2 s[kPer][GB];
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) {
-            float4 kk[kPer];
+            F2 kk[kPer][2];
 #pragma unroll
-            for (int y = 0; y < kPer; ++y)
-                kk[y] = *reinterpret_cast<const float4 *>(k + y * 8 * kRowBytes + (((t + 4 * i) ^ swizzle(g)) << 4));
+            for (int y = 0; y < kPer; ++y) load(k + y * 8 * kRowBytes + (((t + 4 * i) ^ swizzle(g)) << 4), kk[y]);
 #pragma unroll
             for (int h = 0; h < GB; ++h) {
-                const float4 qq = *reinterpret_cast<const float4 *>(sq + h * D + 4 * (t + 4 * i));
+                F2 qq[2];
+                load(sq + h * D + 4 * (t + 4 * i), qq);
 #pragma unroll
                 for (int y = 0; y < kPer; ++y)
-                    s[y][h] = fmaf(qq.x, kk[y].x, fmaf(qq.y, kk[y].y, fmaf(qq.z, kk[y].z, fmaf(qq.w, kk[y].w, s[y][h]))));
+                    s[y][h] = fma(qq[1], kk[y][1], i ? fma(qq[0], kk[y][0], s[y][h]) : mul(qq[0], kk[y][0]));
             }
         }
-#pragma unroll
-        for (int y = 0; y < kPer; ++y)
-#pragma unroll
-            for (int h = 0; h < GB; ++h) {
-                s[y][h] += __shfl_xor_sync(0xffffffffu, s[y][h], 1);
-                s[y][h] += __shfl_xor_sync(0xffffffffu, s[y][h], 2);
-            }
         bool moved = false;
 #pragma unroll
         for (int i = 0; i < kHeads; ++i) {
@@ -328,11 +333,11 @@ template <int D, int GB> struct F32Math {
             float mx = m[i];
 #pragma unroll
             for (int y = 0; y < kPer; ++y) {
-                x[y] = -INFINITY;
+                float a[4];
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
-                    if (4 * i + c < GB && t == c) x[y] = s[y][4 * i + c < GB ? 4 * i + c : 0];
-                if (!(on >> (8 * y + g) & 1)) x[y] = -INFINITY;
+                for (int c = 0; c < 4; ++c) a[c] = 4 * i + c < GB ? sum2(s[y][4 * i + c < GB ? 4 * i + c : 0]) : 0.f;
+                x[y] = spread(a[0], a[1], a[2], a[3], t);
+                if (4 * i + t >= GB || !(on >> (8 * y + g) & 1)) x[y] = -INFINITY;
                 mx = fmaxf(mx, x[y]);
             }
 #pragma unroll
@@ -347,41 +352,37 @@ template <int D, int GB> struct F32Math {
             for (int y = 0; y < kPer; ++y) {
                 const float pr = pow2(fmaf(x[y], sc, -ms[i]));
                 l[i] += pr;
-                if (4 * i + t < GB) sp[(8 * y + g) * GB + 4 * i + t] = pr;
+                if (4 * i + t < GB) pp[(8 * y + g) * GB + 4 * i + t] = make_float2(pr, pr);
             }
-            if (4 * i + t < GB && g == 0) sp[kTok * GB + 4 * i + t] = al;
+            if (4 * i + t < GB && g == 0) pp[kTok * GB + 4 * i + t] = make_float2(al, al);
         }
         __syncwarp();
         if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
             for (int h = 0; h < GB; ++h) {
-                const float al = sp[kTok * GB + h];
-                o[h].x *= al, o[h].y *= al, o[h].z *= al, o[h].w *= al;
+                F2 al;
+                al.v = *reinterpret_cast<const unsigned long long *>(pp + kTok * GB + h);
+                o[h][0] = mul(o[h][0], al), o[h][1] = mul(o[h][1], al);
             }
         }
         const int c = lane % kLanes, sub = lane / kLanes;
 #pragma unroll
         for (int i = 0; i < kTok; i += 32 / kLanes) {
             const int tok = i + sub;
-            const float4 vv = *reinterpret_cast<const float4 *>(v + tok * kRowBytes + ((c ^ swizzle(tok & 7)) << 4));
-            float pr[GB];
+            F2 vv[2], pr[GB < 2 ? 2 : GB];
+            load(v + tok * kRowBytes + ((c ^ swizzle(tok & 7)) << 4), vv);
             if constexpr (GB == 1) {
-                pr[0] = sp[tok];
-            } else if constexpr (GB == 2) {
-                const float2 f = *reinterpret_cast<const float2 *>(sp + tok * 2);
-                pr[0] = f.x, pr[1] = f.y;
+                pr[0].v = *reinterpret_cast<const unsigned long long *>(pp + tok);
             } else {
 #pragma unroll
-                for (int h = 0; h < GB; h += 4) {
-                    const float4 f = *reinterpret_cast<const float4 *>(sp + tok * GB + h);
-                    pr[h] = f.x, pr[h + 1] = f.y, pr[h + 2] = f.z, pr[h + 3] = f.w;
+                for (int h = 0; h < GB; h += 2) {
+                    F2 two[2];
+                    load(pp + tok * GB + h, two);
+                    pr[h] = two[0], pr[h + 1] = two[1];
                 }
             }
 #pragma unroll
-            for (int h = 0; h < GB; ++h) {
-                o[h].x = fmaf(pr[h], vv.x, o[h].x), o[h].y = fmaf(pr[h], vv.y, o[h].y);
-                o[h].z = fmaf(pr[h], vv.z, o[h].z), o[h].w = fmaf(pr[h], vv.w, o[h].w);
-            }
+            for (int h = 0; h < GB; ++h) o[h][0] = fma(pr[h], vv[0], o[h][0]), o[h][1] = fma(pr[h], vv[1], o[h][1]);
         }
         __syncwarp();
     }
@@ -396,19 +397,21 @@ template <int D, int GB> struct F32Math {
         }
         if constexpr (D == 64) {
 #pragma unroll
-            for (int h = 0; h < GB; ++h) {
-                o[h].x += __shfl_xor_sync(0xffffffffu, o[h].x, 16);
-                o[h].y += __shfl_xor_sync(0xffffffffu, o[h].y, 16);
-                o[h].z += __shfl_xor_sync(0xffffffffu, o[h].z, 16);
-                o[h].w += __shfl_xor_sync(0xffffffffu, o[h].w, 16);
-            }
+            for (int h = 0; h < GB; ++h)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    F2 y;
+                    y.v = __shfl_xor_sync(0xffffffffu, o[h][x].v, 16);
+                    o[h][x] = add(o[h][x], y);
+                }
         }
     }
     template <int C0> __device__ __forceinline__ void put(float *wo, int lane) {
         const int c = lane - C0 / 4;
         if (c < 0 || c >= kCols / 4) return;
 #pragma unroll
-        for (int h = 0; h < GB; ++h) *reinterpret_cast<float4 *>(wo + h * kCols + 4 * c) = o[h];
+        for (int h = 0; h < GB; ++h)
+            *reinterpret_cast<ulonglong2 *>(wo + h * kCols + 4 * c) = make_ulonglong2(o[h][0].v, o[h][1].v);
     }
 };
 
@@ -419,7 +422,7 @@ template <int D, typename M> struct Shared {
     float wm[kWarps][M::kRows], wl[kWarps][M::kRows];
     uint32_t on[kWarps][kStages];
     alignas(16) float q[sizeof(typename M::T) == 4 ? M::kRows * D : 4];
-    alignas(16) float p[sizeof(typename M::T) == 4 ? kWarps : 1][sizeof(typename M::T) == 4 ? M::kRows * (M::kTok + 4) : 4];
+    alignas(16) float p[sizeof(typename M::T) == 4 ? kWarps : 1][sizeof(typename M::T) == 4 ? 2 * M::kRows * (M::kTok + 2) : 4];
     long long scan[kWarps];
     long long at[2];
     int n0[2], nt0[2];
@@ -788,7 +791,8 @@ template <int D, typename F> auto dispatch(const AttnDecodeArgs &a, F f) {
     if (G == 1) return f.template operator()<D, F32Math<D, 1>>();
     if (G == 2) return f.template operator()<D, F32Math<D, 2>>();
     if (G <= 4) return f.template operator()<D, F32Math<D, 4>>();
-    return f.template operator()<D, F32Math<D, 8>>();
+    if (G <= 8) return f.template operator()<D, F32Math<D, 8>>();
+    return f.template operator()<D, F32Math<D, 16>>();
 }
 
 struct Run {

@@ -1,6 +1,5 @@
-// attn_vec.cuh -- rows of the query / key prologue as lanes hold them: two 16-byte chunks of a row per lane, kept as
-// loaded (bf16 packed two to a register) until they are converted, and arithmetic on pairs of floats (one instruction
-// for two on sm_100).
+// attn_vec.cuh -- arithmetic on pairs of floats (one instruction for two on sm_100), and the 16-byte chunks of rows that
+// lanes of the query / key prologue hold, kept as loaded (bf16 packed two to a register) until they are converted.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -21,6 +20,11 @@ __device__ __forceinline__ void split(F2 x, float &a, float &b) { asm("mov.b64 {
 __device__ __forceinline__ F2 mul(F2 a, F2 b) {
     F2 r;
     asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 add(F2 a, F2 b) {
+    F2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
     return r;
 }
 __device__ __forceinline__ F2 fma(F2 a, F2 b, F2 c) {
