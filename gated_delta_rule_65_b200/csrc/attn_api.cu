@@ -53,6 +53,7 @@ int check_decode(const gdr2::AttnDecodeArgs &a, int R) {
     if (st == GDR2_OK) st = check_pages(R, a.P, a.page_size, a.num_pages);
     if (st != GDR2_OK) return st;
     if (a.N <= 0 || a.Hq % a.Hk != 0 || a.window < 0) return GDR2_ERR_INVALID_ARG;
+    if (a.Hq / a.Hk > 1024) return GDR2_ERR_UNSUPPORTED;  // a CTA for each block of a KV head's query heads
     // rows of the work and token rows of the pool are counted in 32 bits
     if ((long long)a.N * a.Hq > 0x7fffffffLL || (long long)a.Hk * a.page_size > 0x7fffffffLL ||
         (long long)a.Hk * a.page_size * a.num_pages > 0xffffffffLL)

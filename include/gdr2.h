@@ -375,8 +375,8 @@ GDR2_API int gdr2_decode_step(const void *q, const void *k, const void *v, const
  * cache's bookkeeping. The conventions at the top of this file hold, except that arrays of ints, the gains gq
  * and gk, dgq, dgk and lse need the alignment of their own type only.
  *
- * Sizes: d in {64, 128}; any Hq, Hk >= 1 (attention: Hq a multiple of Hk, query head j reads KV head
- * j / (Hq / Hk)); any page_size >= 1 with P * page_size below 2^31 - 65536.
+ * Sizes: d in {64, 128}; any Hq, Hk >= 1 (attention: Hq a multiple of Hk, at most 1,024 times as
+ * many; query head j reads KV head j / (Hq / Hk)); any page_size >= 1 with P * page_size below 2^31 - 65536.
  */
 
 /*

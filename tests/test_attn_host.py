@@ -72,7 +72,7 @@ DECODE = dict(q=FAKE, kp=FAKE, vp=FAKE, table=FAKE, lens=FAKE, seq=None, scale=0
     (dict(seq=ODD), ARG), (dict(o=None), ARG), (dict(lse=ODD), ARG), (dict(window=-1), ARG), (dict(N=0), ARG),
     (dict(N=4), ARG), (dict(Hq=5), ARG), (dict(Hq=1), ARG), (dict(d=32), UNS), (dict(dtype=-1), ARG), (dict(R=0), ARG),
     (dict(ps=-4), ARG), (dict(P=1 << 30), UNS), (dict(N=1 << 30, seq=FAKE), UNS), (dict(ws=None), WS),
-    (dict(wsb=1000), WS), (dict(num=1 << 30, ps=16, P=200), UNS)], ids=str)
+    (dict(wsb=1000), WS), (dict(num=1 << 30, ps=16, P=200), UNS), (dict(Hq=2050), UNS)], ids=str)
 def test_decode_refusals(over, status):
     assert call("gdr2_attn_decode", DECODE, **over) == status
 
