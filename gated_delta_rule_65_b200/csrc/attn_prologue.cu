@@ -16,8 +16,9 @@
 // Bound: HBM moves 2 (forward) or 3 (backward) rows of d elements per (token, head); next to it stands the issue of
 // instructions. So a lane holds two 16-byte chunks of a row, in the half layout the two that are rotated into one
 // another: the rotation needs no exchange between lanes, a warp takes four bf16 rows of 128 channels at once, and all
-// arithmetic runs on pairs of floats. A warp keeps ONE token and walks its heads, so the coefficients (gain, cosine and
-// sine folded together) stay in registers for all of them and the token's angles are formed once, two a lane. Every
+// arithmetic runs on pairs of floats. A lane keeps ONE token and walks its heads, so the coefficients (gain, cosine and
+// sine folded together) stay in registers for all of them and the token's angles are formed once, by the whole warp. All
+// lane groups of a warp share a token where its heads fill them, else several tokens share the warp. Every
 // lane feeds itself: cp.async into shared memory that only it reads, several rows deep and running on into the next
 // token, so that nothing but a warp's own exchange of angles ever waits.
 //
@@ -47,6 +48,8 @@ constexpr int kBwdGrid = kBwdCtas * kAttnSms;  // CTAs of the backward (a partia
 template <int D, typename T> struct Layout {
     static constexpr int kElems = Chunk<T>::kElems, kPairs = Chunk<T>::kPairs;
     static constexpr int kLanes = D / (2 * kElems), kRows = 32 / kLanes;
+    static constexpr int kRowsLog = kRows == 8 ? 3 : kRows == 4 ? 2 : 1;
+    static_assert(1 << kRowsLog == kRows, "2, 4 or 8 rows");
 };
 
 // The two channels at which lane l's chunks start, and which of them are rotated. Half layout: lanes below
@@ -77,18 +80,25 @@ struct Freqs {
         for (int i = 0; i < 2; ++i)
             f[i] = lane + 32 * i < p.rot / 2 ? p.freqs[lane + 32 * i] * 0.15915494309189533577 : 0.0;
     }
-    // cos and sin of the warp's token, scaled by mag: cs[0 .. D / 2) and cs[D / 2 .. D)
-    template <int D> __device__ __forceinline__ void angles(const AttnPrologueArgs &p, int pos, float *cs, int lane) const {
-        __syncwarp();  // the token before has been read
+    // cos and sin of the warp's `tokens` tokens, scaled by mag: cs[k][0 .. D / 2) and cs[k][D / 2 .. D). pos: the position
+    // of the lane's token; token k's first lane is k 32 / tokens.
+    template <int D>
+    __device__ __forceinline__ void angles(const AttnPrologueArgs &p, int pos, int tokens, float (*cs)[D], int lane) const {
+        __syncwarp();  // the tokens before have been read
+        int at = pos;
+#pragma unroll 1
+        for (int k = 0; k < tokens; ++k) {
+            if (tokens > 1) at = __shfl_sync(0xffffffffu, pos, k * (32 / tokens));
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int x = lane + 32 * i;
-            if (x < p.rot / 2) {
-                const double turns = (double)pos * f[i];
-                float s, c;
-                sincospif(2.f * (float)(turns - rint(turns)), &s, &c);
-                cs[x] = p.mag * c;
-                cs[D / 2 + x] = p.mag * s;
+            for (int i = 0; i < D / 64; ++i) {
+                const int x = lane + 32 * i;
+                if (x < p.rot / 2) {
+                    const double turns = (double)at * f[i];
+                    float s, c;
+                    sincospif(2.f * (float)(turns - rint(turns)), &s, &c);
+                    cs[k][x] = p.mag * c;
+                    cs[k][D / 2 + x] = p.mag * s;
+                }
             }
         }
         __syncwarp();
@@ -167,12 +177,23 @@ template <int D> __device__ __forceinline__ void stage_gain(const float *g, floa
     for (int i = threadIdx.x; i < D; i += kThreads) sg[i] = g ? g[i] : 1.f;
 }
 
-// The work of a warp: units u = warp, warp + warps, ... of (token, part), token u / parts; part k of a token takes the
-// heads k kRows + (the lane's row), + parts kRows, ... of each tensor. parts = 2^log: no division in a unit's few rows.
+// The work of a warp: units u = warp, warp + warps, ... of (block of tokens, part). groups = 2^gl lane groups share a
+// token, so that a block has kRows / groups tokens and lane group grp works on token grp / groups of it; there are
+// parts = 2^log parts, and part k of a token takes the heads k groups + grp % groups, + parts groups, ... of each
+// tensor. All powers of two: no division in a unit's few rows. kOne: all groups on one token, known to the compiler.
 struct Units {
-    int log, count, stride;
-    __device__ __forceinline__ int token(int u) const { return u >> log; }
-    __device__ __forceinline__ int part(int u) const { return u & ((1 << log) - 1); }
+    int log, gl, count, stride;
+};
+template <typename Y, bool kOne> struct Walk : Units {
+    __device__ __forceinline__ explicit Walk(const Units &u) : Units(u) {}
+    __device__ __forceinline__ int groups_log() const { return kOne ? Y::kRowsLog : gl; }
+    __device__ __forceinline__ int tokens() const { return kOne ? 1 : Y::kRows >> gl; }
+    __device__ __forceinline__ int slot(int grp) const { return kOne ? 0 : grp >> gl; }  // which token of the block
+    __device__ __forceinline__ int token(int u, int grp) const { return (u >> log) * tokens() + slot(grp); }
+    __device__ __forceinline__ int head(int u, int grp) const {
+        return ((u & ((1 << log) - 1)) << groups_log()) + (kOne ? grp : grp & ((1 << gl) - 1));
+    }
+    __device__ __forceinline__ int step() const { return 1 << (log + groups_log()); }
 };
 
 __device__ __forceinline__ void cp16(void *dst, const void *src, bool on) {  // off: zeros, nothing is read
@@ -185,21 +206,23 @@ template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.as
 
 // ---- forward and cache form ----------------------------------------------------------------------------------
 
-template <int D> struct FwdShared {
+template <int D, typename T> struct FwdShared {
     uint4 ring[kFwdDepth][2][kThreads];
     alignas(16) float gain[2][D];
-    alignas(16) float cs[kWarps][D];
+    alignas(16) float cs[kWarps][Layout<D, T>::kRows][D];
 };
 
-template <int D, typename T, bool kInter, bool kAll, bool kCache>
-__global__ void __launch_bounds__(kThreads, kFwdCtas) attn_prologue_fwd_kernel(AttnPrologueArgs p, Units un) {
+template <int D, typename T, bool kInter, bool kAll, bool kCache, bool kOne>
+__global__ void __launch_bounds__(kThreads, kFwdCtas) attn_prologue_fwd_kernel(AttnPrologueArgs p, Units units) {
     using Y = Layout<D, T>;
+    const Walk<Y, kOne> un(units);
     constexpr int N = Y::kPairs;
     extern __shared__ __align__(16) uint8_t raw[];
-    FwdShared<D> &sh = *reinterpret_cast<FwdShared<D> *>(raw);
+    FwdShared<D, T> &sh = *reinterpret_cast<FwdShared<D, T> *>(raw);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, grp = lane / Y::kLanes, l = lane % Y::kLanes;
     const Slot<D, T, kInter> w(l, p.rot);
-    const int step = Y::kRows << un.log;
+    const int step = un.step(), tokens = un.tokens();
+    const float *cs = sh.cs[warp][un.slot(grp)];
     const int tq = (p.Hq + step - 1) / step, tk = (p.Hk + step - 1) / step;
     int u = blockIdx.x * kWarps + warp;
     follow();
@@ -209,12 +232,12 @@ __global__ void __launch_bounds__(kThreads, kFwdCtas) attn_prologue_fwd_kernel(A
     int ua = u, seg = -1, left = 0, ha = 0, ea = 0;
     const T *src = nullptr;
     auto enter = [&]() {
-        const int tok = un.token(ua);
-        ha = un.part(ua) * Y::kRows + grp;
+        const int tok = un.token(ua, grp);
+        ha = un.head(ua, grp);
         ++seg;
         const T *x = static_cast<const T *>(seg == 0 ? p.xq : seg == 1 ? p.xk : p.xv);
         src = x + (size_t)tok * (seg == 0 ? p.sxq : seg == 1 ? p.sxk : p.sxv) + (size_t)ha * D;
-        ea = seg == 0 ? p.Hq : p.Hk;
+        ea = !kOne && tok >= p.T ? 0 : seg == 0 ? p.Hq : p.Hk;
         left = seg == 0 ? tq : tk;
     };
     if (ua < un.count) enter();
@@ -235,8 +258,11 @@ __global__ void __launch_bounds__(kThreads, kFwdCtas) attn_prologue_fwd_kernel(A
     };
 #pragma unroll
     for (int i = 0; i < kFwdDepth; ++i) fetch(i);
-    // the token of a unit, read one unit ahead (its sequence two)
-    auto token = [&](int v) { return v < un.count ? un.token(v) : 0; };
+    // the lane's token of a unit (0 behind the last), its position and its sequence read two units ahead
+    auto token = [&](int v) {
+        const int tok = v < un.count ? un.token(v, grp) : 0;
+        return kOne || tok < p.T ? tok : 0;
+    };
     int pos = 0, seq = 0, page = -1, npos = 0, nseq = 0;
     auto find_page = [&](int q, int s) {
         if (s < 0 || s >= p.R || q < 0) return -1;
@@ -259,17 +285,18 @@ __global__ void __launch_bounds__(kThreads, kFwdCtas) attn_prologue_fwd_kernel(A
     __syncthreads();
     int slot = 0;
     for (; u < un.count; u += un.stride) {
-        const int tok = un.token(u), h0 = un.part(u) * Y::kRows + grp;
-        GDR2_DCHECK(tok >= 0 && tok < p.T);
+        const int tok = un.token(u, grp), h0 = un.head(u, grp);
+        const bool real = kOne || tok < p.T;
+        GDR2_DCHECK(tok >= 0 && tok < p.T + tokens - 1);
         int fpos = 0, fseq = 0, npage = -1;
         if (p.rot || kCache) fpos = p.pos[token(u + 2 * un.stride)];
         if constexpr (kCache) {
             fseq = p.seq[token(u + 2 * un.stride)];
             npage = find_page(npos, nseq);
         }
-        fr.angles<D>(p, pos, sh.cs[warp], lane);
-        const bool live = !kCache || (seq >= 0 && seq < p.R);
-        const bool put = !kCache || (live && page >= 0 && page < p.num_pages);
+        fr.angles<D>(p, pos, tokens, sh.cs[warp], lane);
+        const bool live = real && (!kCache || (seq >= 0 && seq < p.R));
+        const bool put = live && (!kCache || (page >= 0 && page < p.num_pages));
         GDR2_DCHECK(!kCache || !put || (pos >= 0 && pos - p.by_page.divide(pos) * p.page_size < (uint32_t)p.page_size));
         const long long hs = kCache ? (long long)p.page_size * D : D;  // from head to head where keys go
         const size_t at = kCache ? (put ? ((size_t)page * p.Hk * p.page_size + (pos - p.by_page.divide(pos) * p.page_size)) * D : 0) : (size_t)tok * p.Hk * D;
@@ -277,7 +304,7 @@ __global__ void __launch_bounds__(kThreads, kFwdCtas) attn_prologue_fwd_kernel(A
         for (int which = 0; which < 2; ++which) {
             // u (.) g folded into the rotation: the partner's gain goes with its sine
             Turn<T> t;
-            load_turn<D, T, kInter>(w, sh.cs[warp], sh.cs[warp] + D / 2, t);
+            load_turn<D, T, kInter>(w, cs, cs + D / 2, t);
             F2 g0[N], g1[N];
             load_pairs(sh.gain[which] + w.at0, g0);
             load_pairs(sh.gain[which] + w.at1, g1);
@@ -344,37 +371,38 @@ __global__ void __launch_bounds__(kThreads, kFwdCtas) attn_prologue_fwd_kernel(A
 
 // ---- backward --------------------------------------------------------------------------------------------------
 
-template <int D> struct BwdShared {
+template <int D, typename T> struct BwdShared {
     uint4 ring[kBwdDepth][4][kThreads];
     alignas(16) float gain[D];
-    alignas(16) float cs[kWarps][D];
+    alignas(16) float cs[kWarps][Layout<D, T>::kRows][D];
 };
 
 // The first `cq` CTAs take the queries, the others the keys (one set of sums in a lane's registers), each warp a fixed
 // set of units: the sums over tokens have a fixed order.
-template <int D, typename T, bool kInter, bool kAll>
+template <int D, typename T, bool kInter, bool kAll, bool kOne>
 __global__ void __launch_bounds__(kThreads, kBwdCtas) attn_prologue_bwd_kernel(AttnPrologueArgs p, Units uq, Units uk, int cq,
                                                                                float *__restrict__ partial) {
     using Y = Layout<D, T>;
     constexpr int N = Y::kPairs;
     extern __shared__ __align__(16) uint8_t raw[];
-    BwdShared<D> &sh = *reinterpret_cast<BwdShared<D> *>(raw);
+    BwdShared<D, T> &sh = *reinterpret_cast<BwdShared<D, T> *>(raw);
     const bool keys = blockIdx.x >= cq;
-    const Units un = keys ? uk : uq;
+    const Walk<Y, kOne> un(keys ? uk : uq);
     const T *x = static_cast<const T *>(keys ? p.xk : p.xq), *dy = static_cast<const T *>(keys ? p.dk : p.dq);
     T *dx = static_cast<T *>(keys ? p.dxk : p.dxq);
     const long long sx = keys ? p.sxk : p.sxq, sdx = keys ? p.sdxk : p.sdxq;
     const int H = keys ? p.Hk : p.Hq;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, grp = lane / Y::kLanes, l = lane % Y::kLanes;
     const Slot<D, T, kInter> w(l, p.rot);
-    const int step = Y::kRows << un.log, rows = (H + step - 1) / step;
+    const int step = un.step(), tokens = un.tokens(), rows = (H + step - 1) / step;
+    const float *cs = sh.cs[warp][un.slot(grp)];
     int u = (blockIdx.x - (keys ? cq : 0)) * kWarps + warp;
     follow();
     int ua = u, left = 0, ha = 0;  // as in the forward: the row this lane fetches next
     const T *sd = nullptr, *sr = nullptr;
     auto enter = [&]() {
-        const int tok = un.token(ua);
-        ha = un.part(ua) * Y::kRows + grp;
+        const int tok = un.token(ua, grp);
+        ha = kOne || tok < p.T ? un.head(ua, grp) : H;
         sd = dy + ((size_t)tok * H + ha) * D;
         sr = x + (size_t)tok * sx + (size_t)ha * D;
         left = rows;
@@ -399,7 +427,10 @@ __global__ void __launch_bounds__(kThreads, kBwdCtas) attn_prologue_bwd_kernel(A
     };
 #pragma unroll
     for (int i = 0; i < kBwdDepth; ++i) fetch(i);
-    auto position = [&](int v) { return p.rot ? p.pos[v < un.count ? un.token(v) : 0] : 0; };
+    auto position = [&](int v) {
+        const int tok = v < un.count ? un.token(v, grp) : 0;
+        return p.rot ? p.pos[kOne || tok < p.T ? tok : 0] : 0;
+    };
     int pos = position(u);
     Freqs fr;
     fr.load(p, lane);
@@ -412,12 +443,12 @@ __global__ void __launch_bounds__(kThreads, kBwdCtas) attn_prologue_bwd_kernel(A
     for (int i = 0; i < N; ++i) a0[i] = a1[i] = f2(0.f, 0.f);
     int slot = 0;
     for (; u < un.count; u += un.stride) {
-        const int tok = un.token(u), h0 = un.part(u) * Y::kRows + grp;
-        GDR2_DCHECK(tok >= 0 && tok < p.T && slot % kBwdBurst >= 0 && slot < kBwdDepth);
+        const int tok = un.token(u, grp), h0 = kOne || tok < p.T ? un.head(u, grp) : H;
+        GDR2_DCHECK(tok >= 0 && tok < p.T + tokens - 1 && slot % kBwdBurst >= 0 && slot < kBwdDepth);
         const int npos = position(u + un.stride);
-        fr.angles<D>(p, pos, sh.cs[warp], lane);
+        fr.angles<D>(p, pos, tokens, sh.cs[warp], lane);
         Turn<T> t;
-        load_turn<D, T, kInter>(w, sh.cs[warp], sh.cs[warp] + D / 2, t);
+        load_turn<D, T, kInter>(w, cs, cs + D / 2, t);
 #pragma unroll
         for (int i = 0; i < N; ++i) t.s0[i] = neg(t.s0[i]), t.s1[i] = neg(t.s1[i]);  // the transposed rotation
         T *out = dx + (size_t)tok * sdx + (size_t)h0 * D;
@@ -518,52 +549,64 @@ __global__ void __launch_bounds__(1024) attn_prologue_reduce_kernel(const float 
     }
 }
 
+// Lane groups of a token: as many as leave no lane idle (bf16, 2 + 1 heads of 64 with all eight groups on one token: 309
+// us forward and 455 backward for 150 MB of rows; with one group a token 77 and 148), more while that leaves fewer than
+// two units for each warp of the grid.
 // Parts of a token: one warp for all its heads while there are two units for each warp of the grid (a part repeats the
 // token's angles; with fewer units the last round leaves most warps idle: 16 packed prompts took 69 us with eight units
 // asked for, 51 with two), more below, up to one row a lane.
-Units split_units(int T, int most, int rows, int warps) {
-    Units un;
-    un.log = 0;
-    while ((rows << un.log) < most && ((long long)T << un.log) < 2LL * warps) ++un.log;
-    un.count = T << un.log;
+Units split_units(int T, int Hq, int Hk, int rows, int warps) {
+    Units un{};
+    const int most = Hq > Hk ? Hq : Hk;
+    auto even = [&](int groups) { return Hq % groups == 0 && Hk % groups == 0; };
+    auto blocks = [&] { return (((long long)T << un.gl) + rows - 1) / rows; };
+    while ((2 << un.gl) <= rows && even(2 << un.gl)) ++un.gl;
+    while ((2 << un.gl) <= rows && blocks() < 2LL * warps) ++un.gl;
+    while ((1 << (un.log + un.gl)) < most && (blocks() << un.log) < 2LL * warps) ++un.log;
+    un.count = (int)(blocks() << un.log);
     un.stride = warps;
     return un;
 }
 
 template <int D, typename T, bool kInter, bool kAll, bool kCache>
 cudaError_t run_fwd(const AttnPrologueArgs &a, cudaStream_t st) {
-    constexpr int smem = sizeof(FwdShared<D>), full = kFwdCtas * kAttnSms;
-    const auto kernel = attn_prologue_fwd_kernel<D, T, kInter, kAll, kCache>;
-    static Allowed allowed;
-    cudaError_t e = allowed(kernel, smem);
-    if (e != cudaSuccess) return e;
-    Units un = split_units(a.T, a.Hq > a.Hk ? a.Hq : a.Hk, Layout<D, T>::kRows, full * kWarps);
+    constexpr int smem = sizeof(FwdShared<D, T>), full = kFwdCtas * kAttnSms;
+    Units un = split_units(a.T, a.Hq, a.Hk, Layout<D, T>::kRows, full * kWarps);
     const int need = (int)(((long long)un.count + kWarps - 1) / kWarps), grid = need < full ? need : full;
     un.stride = grid * kWarps;
+    const bool whole = un.gl == Layout<D, T>::kRowsLog;
+    const auto kernel = whole ? attn_prologue_fwd_kernel<D, T, kInter, kAll, kCache, true>
+                              : attn_prologue_fwd_kernel<D, T, kInter, kAll, kCache, false>;
+    static Allowed allowed[2];
+    cudaError_t e = allowed[whole](kernel, smem);
+    if (e != cudaSuccess) return e;
     GDR2_LAUNCH(kCache ? "attn_prologue_cache" : "attn_prologue_fwd", st, e = launch(kernel, dim3(grid), dim3(kThreads), smem, 0, st, a, un));
     return e;
 }
 
 template <int D, typename T, bool kInter, bool kAll>
 cudaError_t run_bwd(const AttnPrologueArgs &a, cudaStream_t st) {
-    constexpr int smem = sizeof(BwdShared<D>);
-    const auto kernel = attn_prologue_bwd_kernel<D, T, kInter, kAll>;
-    static Allowed allowed;
-    cudaError_t e = allowed(kernel, smem);
-    if (e != cudaSuccess) return e;
-    // CTAs in proportion to the heads, at least one each
-    const long long heads = (long long)a.Hq + a.Hk;
-    int cq = (int)((kBwdGrid * (long long)a.Hq + heads / 2) / heads);
+    constexpr int smem = sizeof(BwdShared<D, T>);
+    // CTAs in proportion to the heads and a token's angles, which take about the time of kAngles rows; at least one each
+    // (7 + 1 bf16 heads of 128, 150 MB of rows: 93 us with 2, 99 with 4, 180 by the heads alone)
+    constexpr int kAngles = 2;
+    const long long heads = (long long)a.Hq + a.Hk + 2 * kAngles;
+    int cq = (int)((kBwdGrid * (long long)(a.Hq + kAngles) + heads / 2) / heads);
     cq = cq < 1 ? 1 : cq > kBwdGrid - 1 ? kBwdGrid - 1 : cq;
     int ck = kBwdGrid - cq;
     auto part = [&](int H, int &ctas) {
-        Units un = split_units(a.T, H, Layout<D, T>::kRows, ctas * kWarps);
+        Units un = split_units(a.T, H, 0, Layout<D, T>::kRows, ctas * kWarps);
         const int need = (int)(((long long)un.count + kWarps - 1) / kWarps);
         ctas = need < ctas ? need : ctas;
         un.stride = ctas * kWarps;
         return un;
     };
     const Units uq = part(a.Hq, cq), uk = part(a.Hk, ck);
+    const bool whole = uq.gl == Layout<D, T>::kRowsLog && uk.gl == uq.gl;
+    const auto kernel = whole ? attn_prologue_bwd_kernel<D, T, kInter, kAll, true> : attn_prologue_bwd_kernel<D, T, kInter, kAll, false>;
+    static Allowed allowed[2];
+    cudaError_t e = allowed[whole](kernel, smem);
+    if (e != cudaSuccess) return e;
     float *partial = a.dgq || a.dgk ? static_cast<float *>(a.workspace) : nullptr;
     GDR2_LAUNCH("attn_prologue_bwd", st, e = launch(kernel, dim3(cq + ck), dim3(kThreads), smem, 0, st, a, uq, uk, cq, partial));
     if (e != cudaSuccess || partial == nullptr) return e;

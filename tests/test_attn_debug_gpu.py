@@ -27,6 +27,7 @@ for c in A.PROLOGUE:
     ok("prologue")
 A.test_cache_prologue("bf16", 64, 3, 3, 7, True)
 A.test_cache_prologue("f32", 128, 5, 1, 1, True)
+A.test_cache_prologue_tokens_share_a_warp(64, 1, 1, "bf16")
 ok("cache")
 for c in A.DECODE:
     A.test_decode(c)

@@ -48,6 +48,13 @@ PROLOGUE = [
     (50, 2, 2, 128, 0, False, True, "bf16", 0, 0),
     (1500, 1, 1, 128, 64, True, True, "f32", 0, 0),
     (2500, 16, 8, 128, 128, False, True, "bf16", 8, 500000),
+    # heads that do not fill a warp's rows, tokens enough that several share it, the last block not full
+    (38003, 1, 1, 64, 64, False, True, "bf16", 0, 90000),
+    (20003, 6, 2, 64, 48, True, True, "bf16", 1, 0),
+    (19011, 3, 1, 128, 128, True, True, "bf16", 0, 17),
+    (12001, 2, 2, 128, 32, False, False, "bf16", 0, 0),
+    (19015, 1, 3, 64, 64, False, True, "f32", 0, 5),
+    (9503, 5, 1, 128, 128, True, True, "f32", 2, 1 << 20),
 ]
 
 
@@ -280,6 +287,45 @@ def test_cache_prologue(dt, d, Hq, Hk, ps, inter):
     assert torch.equal(v, vr)
     err = (k.double() - kr).abs()
     assert (err <= tk).all() and int((tk > 0).sum()) > 0  # a bound of 0 where nothing was written
+
+
+@pytest.mark.parametrize("d,Hq,Hk,dt", [(64, 1, 1, "bf16"), (128, 3, 1, "bf16"), (64, 2, 2, "f32")])
+def test_cache_prologue_tokens_share_a_warp(d, Hq, Hk, dt):
+    """Few heads and many tokens: several tokens of a warp, each with its own sequence, page, and none at times."""
+    g = gen(5 + d + Hq)
+    R, n, ps, num = 4, 10001, 16, 2600
+    P = -(-n // ps)
+    T = R * n + 3
+    table = torch.randperm(num, generator=g, device="cuda")[:R * P].view(R, P).int()
+    table[1, 5], table[2, 7] = -1, num
+    seq = torch.cat([torch.arange(R, device="cuda").repeat_interleave(n), torch.tensor([0, -1, R], device="cuda")]).int()
+    pos = torch.cat([torch.arange(n, device="cuda").repeat(R), torch.tensor([P * ps, 0, 0], device="cuda")]).int()
+    seq[::97] = -1
+    order = torch.randperm(T, generator=g, device="cuda")
+    seq, pos = seq[order], pos[order]
+    xq, xk, xv = (randn(g, T, h, d, dtype=DT[dt]) for h in (Hq, Hk, Hk))
+    gq, gk = 1 + 0.2 * randn(g, d), 1 + 0.2 * randn(g, d)
+    fr, _ = gdr2.rope_freqs(d)
+    k0, v0 = randn(g, num, Hk, ps, d, dtype=DT[dt]), randn(g, num, Hk, ps, d, dtype=DT[dt])
+    k, v = k0.clone(), v0.clone()
+    q = torch.full((T, Hq, d), 5.0, dtype=DT[dt], device="cuda")
+    gdr2.attn_prologue_cache(xq, xk, xv, gq, gk, seq, pos, fr, k, v, table, q=q)
+    live = (seq >= 0) & (seq < R)
+    y, tol = ref.prologue(xq, gq, pos, fr)
+    ref.check("q", q[live], y[live], tol[live])
+    assert (q[~live] == 5).all()
+    put = live & (pos < P * ps)
+    page = table[seq[put].long(), pos[put].long() // ps].long()
+    ok = (page >= 0) & (page < num)
+    page, at = page[ok], pos[put][ok].long() % ps
+    z, tolk = ref.prologue(xk, gk, pos, fr)
+    z, tolk = z[put][ok], tolk[put][ok]
+    ref.check("k", k[page, :, at], z, tolk)
+    vr = v0.clone()
+    vr[page, :, at] = xv[put][ok]
+    assert torch.equal(v, vr)
+    k[page, :, at] = k0[page, :, at]
+    assert torch.equal(k, k0)
 
 
 DECODE = [
