@@ -46,7 +46,7 @@ constexpr int kBwdGrid = kBwdCtas * kAttnSms;  // CTAs of the backward (a partia
 
 // How lanes hold a row: kLanes lanes of two chunks each, kRows rows in a warp.
 template <int D, typename T> struct Layout {
-    static constexpr int kElems = Chunk<T>::kElems, kPairs = Chunk<T>::kPairs;
+    static constexpr int kElems = 16 / sizeof(T), kPairs = kElems / 2;
     static constexpr int kLanes = D / (2 * kElems), kRows = 32 / kLanes;
     static constexpr int kRowsLog = kRows == 8 ? 3 : kRows == 4 ? 2 : 1;
     static_assert(1 << kRowsLog == kRows, "2, 4 or 8 rows");
@@ -59,6 +59,7 @@ template <int D, typename T, bool kInter> struct Slot {
     using Y = Layout<D, T>;
     int at0, at1;
     bool on0, on1;
+    __device__ __forceinline__ bool on(int i) const { return kInter && i >= Y::kPairs / 2 ? on1 : on0; }  // u[i], v[i] rotated
     __device__ __forceinline__ Slot(int l, int rot) {
         if constexpr (kInter) {
             at0 = l * Y::kElems, at1 = (l + Y::kLanes) * Y::kElems;
@@ -105,65 +106,35 @@ struct Freqs {
     }
 };
 
-// 2 N consecutive floats of shared memory, 16-byte aligned.
-template <int N> __device__ __forceinline__ void load_pairs(const float *p, F2 (&w)[N]) {
-#pragma unroll
-    for (int i = 0; i < N; i += 2) {
-        const float4 v = *reinterpret_cast<const float4 *>(p + 2 * i);
-        w[i] = f2(v.x, v.y), w[i + 1] = f2(v.z, v.w);
-    }
-}
-
-// A token's rotation as lane l applies it, y = c0 (.) x0 + s0 (.) partner(x0), likewise for chunk 1: the partner of
-// chunk 0 is chunk 1 (half layout) or chunk 0 with its pairs swapped (interleaved). Unrotated chunks have c = 1, s = 0.
-template <typename T> struct Turn {
-    F2 c0[Chunk<T>::kPairs], s0[Chunk<T>::kPairs], c1[Chunk<T>::kPairs], s1[Chunk<T>::kPairs];
-};
-
+// A token's rotation as a lane applies it to u and v (partners, Chunks): cosines and sines, 1 and 0 where nothing is
+// rotated.
 template <int D, typename T, bool kInter>
-__device__ __forceinline__ void load_turn(const Slot<D, T, kInter> &w, const float *sc, const float *ss, Turn<T> &t) {
-    constexpr int N = Chunk<T>::kPairs;
-    const F2 one = f2(1.f, 1.f), zero = f2(0.f, 0.f);
+__device__ __forceinline__ void load_turn(const Slot<D, T, kInter> &w, const float *sc, const float *ss, F2 (&c)[Chunks<T, kInter>::kPairs],
+                                          F2 (&s)[Chunks<T, kInter>::kPairs]) {
+    using C = Chunks<T, kInter>;
     if constexpr (kInter) {
-        auto both = [&](int at, bool on, F2(&c)[N], F2(&s)[N]) {
-#pragma unroll
-            for (int i = 0; i < N; i += 2) {
-                const float2 cc = *reinterpret_cast<const float2 *>(sc + at / 2 + i);
-                const float2 si = *reinterpret_cast<const float2 *>(ss + at / 2 + i);
-                c[i] = on ? f2(cc.x, cc.x) : one, c[i + 1] = on ? f2(cc.y, cc.y) : one;
-                s[i] = on ? f2(-si.x, si.x) : zero, s[i + 1] = on ? f2(-si.y, si.y) : zero;
-            }
-        };
-        both(w.at0, w.on0, t.c0, t.s0);
-        both(w.at1, w.on1, t.c1, t.s1);
+        C::template load<C::kHalf>(sc + w.at0 / 2, c), C::template load<C::kHalf>(sc + w.at1 / 2, c + C::kHalf);
+        C::template load<C::kHalf>(ss + w.at0 / 2, s), C::template load<C::kHalf>(ss + w.at1 / 2, s + C::kHalf);
     } else {
-        const int a = w.on0 ? w.at0 : 0;
-        load_pairs(sc + a, t.c0);
-        load_pairs(ss + a, t.s1);
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            if (!w.on0) t.c0[i] = one, t.s1[i] = zero;
-            t.c1[i] = t.c0[i];
-            t.s0[i] = neg(t.s1[i]);
-        }
+        const int at = w.on0 ? w.at0 : 0;
+        C::template load<C::kPairs>(sc + at, c), C::template load<C::kPairs>(ss + at, s);
     }
+#pragma unroll
+    for (int i = 0; i < C::kPairs; ++i)
+        if (!w.on(i)) c[i] = f2(1.f, 1.f), s[i] = f2(0.f, 0.f);
 }
 
-// y = c (.) x + s (.) partner(x) for both chunks. An infinity in an unrotated channel must not reach another one as
-// 0 * inf: without a rotation the partner's place is taken by a zero (kAll: the whole row is rotated).
-template <typename T, bool kInter, bool kAll, int N>
-__device__ __forceinline__ void turn(const Turn<T> &t, bool on0, bool on1, const F2 (&x0)[N], const F2 (&x1)[N], F2 (&y0)[N],
-                                     F2 (&y1)[N]) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-        F2 p0 = kInter ? swap(x0[i]) : x1[i], p1 = kInter ? swap(x1[i]) : x0[i];
-        if (!kAll) {
-            p0.v = on0 ? p0.v : 0;
-            p1.v = on1 ? p1.v : 0;
-        }
-        y0[i] = fma(t.c0[i], x0[i], mul(t.s0[i], p0));
-        y1[i] = fma(t.c1[i], x1[i], mul(t.s1[i], p1));
+// y = cu u + sv v, z = cv v + su u. An infinity in an unrotated channel must not reach another one as 0 * inf: without a
+// rotation the partner's place is taken by a zero (kAll: the whole row is rotated).
+template <bool kAll>
+__device__ __forceinline__ void turn(bool on, F2 cu, F2 sv, F2 cv, F2 su, F2 u, F2 v, F2 &y, F2 &z) {
+    F2 pu = u, pv = v;
+    if (!kAll) {
+        pu.v = on ? pu.v : 0;
+        pv.v = on ? pv.v : 0;
     }
+    y = fma(cu, u, mul(sv, pv));
+    z = fma(cv, v, mul(su, pu));
 }
 
 template <int L> __device__ __forceinline__ float sum_row(float v) {
@@ -172,9 +143,9 @@ template <int L> __device__ __forceinline__ float sum_row(float v) {
     return v;
 }
 
-// A row's gain in shared memory (ones where there is none).
-template <int D> __device__ __forceinline__ void stage_gain(const float *g, float *sg) {
-    for (int i = threadIdx.x; i < D; i += kThreads) sg[i] = g ? g[i] : 1.f;
+// A row's gain in shared memory, in the lanes' order (ones where there is none).
+template <int D, typename C> __device__ __forceinline__ void stage_gain(const float *g, float *sg) {
+    for (int i = threadIdx.x; i < D; i += kThreads) sg[C::place(i)] = g ? g[i] : 1.f;
 }
 
 // The work of a warp: units u = warp, warp + warps, ... of (block of tokens, part). groups = 2^gl lane groups share a
@@ -216,6 +187,7 @@ template <int D, typename T, bool kInter, bool kAll, bool kCache, bool kOne>
 __global__ void __launch_bounds__(kThreads, kFwdCtas) attn_prologue_fwd_kernel(AttnPrologueArgs p, Units units) {
     using Y = Layout<D, T>;
     const Walk<Y, kOne> un(units);
+    using C = Chunks<T, kInter>;
     constexpr int N = Y::kPairs;
     extern __shared__ __align__(16) uint8_t raw[];
     FwdShared<D, T> &sh = *reinterpret_cast<FwdShared<D, T> *>(raw);
@@ -280,8 +252,8 @@ __global__ void __launch_bounds__(kThreads, kFwdCtas) attn_prologue_fwd_kernel(A
     }
     Freqs fr;
     fr.load(p, lane);
-    stage_gain<D>(p.gq, sh.gain[0]);
-    stage_gain<D>(p.gk, sh.gain[1]);
+    stage_gain<D, C>(p.gq, sh.gain[0]);
+    stage_gain<D, C>(p.gk, sh.gain[1]);
     __syncthreads();
     int slot = 0;
     for (; u < un.count; u += un.stride) {
@@ -302,16 +274,17 @@ __global__ void __launch_bounds__(kThreads, kFwdCtas) attn_prologue_fwd_kernel(A
         const size_t at = kCache ? (put ? ((size_t)page * p.Hk * p.page_size + (pos - p.by_page.divide(pos) * p.page_size)) * D : 0) : (size_t)tok * p.Hk * D;
 #pragma unroll 1
         for (int which = 0; which < 2; ++which) {
-            // u (.) g folded into the rotation: the partner's gain goes with its sine
-            Turn<T> t;
-            load_turn<D, T, kInter>(w, cs, cs + D / 2, t);
-            F2 g0[N], g1[N];
-            load_pairs(sh.gain[which] + w.at0, g0);
-            load_pairs(sh.gain[which] + w.at1, g1);
+            // the gain folded into the rotation: the partner's goes with its sine
+            F2 cu[N], sv[N], cv[N], su[N];
+            {
+                F2 c[N], s[N], gu[N], gv[N];
+                load_turn<D, T, kInter>(w, cs, cs + D / 2, c, s);
+                C::pairs(sh.gain[which] + w.at0, sh.gain[which] + w.at1, gu, gv);
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-                t.c0[i] = mul(t.c0[i], g0[i]), t.c1[i] = mul(t.c1[i], g1[i]);
-                t.s0[i] = mul(t.s0[i], kInter ? swap(g0[i]) : g1[i]), t.s1[i] = mul(t.s1[i], kInter ? swap(g1[i]) : g0[i]);
+                for (int i = 0; i < N; ++i) {
+                    cu[i] = mul(c[i], gu[i]), sv[i] = mul(neg(s[i]), gv[i]);
+                    cv[i] = mul(c[i], gv[i]), su[i] = mul(s[i], gu[i]);
+                }
             }
             const int H = (which ? put : live) ? (which ? p.Hk : p.Hq) : 0, trips = which ? tk : tq;  // H: heads to store
             const long long os = which ? hs : D, inc = os * step;
@@ -320,30 +293,24 @@ __global__ void __launch_bounds__(kThreads, kFwdCtas) attn_prologue_fwd_kernel(A
 #pragma unroll 1
             for (int i = 0, h = h0; i < trips; ++i, h += step, out += inc) {
                 cp_wait<kFwdDepth - 1>();
-                Chunk<T> a, b;
-                a.v = sh.ring[slot][0][threadIdx.x];
-                b.v = sh.ring[slot][1][threadIdx.x];
-                F2 x0[N], x1[N], y0[N], y1[N];
-                a.get(x0);
-                b.get(x1);
-                turn<T, kInter, kAll>(t, w.on0, w.on1, x0, x1, y0, y1);
+                F2 u[N], v[N], y[N], z[N];
+                C::get(sh.ring[slot][0][threadIdx.x], sh.ring[slot][1][threadIdx.x], u, v);
+#pragma unroll
+                for (int i = 0; i < N; ++i) turn<kAll>(w.on(i), cu[i], sv[i], cv[i], su[i], u[i], v[i], y[i], z[i]);
                 if (p.norm) {
-                    F2 q = mul(x0[0], x0[0]);
+                    F2 q = mul(u[0], u[0]);
 #pragma unroll
-                    for (int i = 1; i < N; ++i) q = fma(x0[i], x0[i], q);
+                    for (int i = 1; i < N; ++i) q = fma(u[i], u[i], q);
 #pragma unroll
-                    for (int i = 0; i < N; ++i) q = fma(x1[i], x1[i], q);
+                    for (int i = 0; i < N; ++i) q = fma(v[i], v[i], q);
                     const float n = rsqrtf(sum_row<Y::kLanes>(sum2(q)) * (1.f / D) + p.eps);
                     const F2 nn = f2(n, n);
 #pragma unroll
-                    for (int i = 0; i < N; ++i) y0[i] = mul(y0[i], nn), y1[i] = mul(y1[i], nn);
+                    for (int i = 0; i < N; ++i) y[i] = mul(y[i], nn), z[i] = mul(z[i], nn);
                 }
                 fetch(slot);
                 if (++slot == kFwdDepth) slot = 0;
-                if (h < H) {
-                    Chunk<T>::store(out + w.at0, y0);
-                    Chunk<T>::store(out + w.at1, y1);
-                }
+                if (h < H) C::put(out + w.at0, out + w.at1, y, z);
             }
         }
         if constexpr (kCache) {
@@ -351,12 +318,9 @@ __global__ void __launch_bounds__(kThreads, kFwdCtas) attn_prologue_fwd_kernel(A
 #pragma unroll 1
             for (int i = 0, h = h0; i < tk; ++i, h += step) {
                 cp_wait<kFwdDepth - 1>();
-                Chunk<T> a, b;
-                a.v = sh.ring[slot][0][threadIdx.x];
-                b.v = sh.ring[slot][1][threadIdx.x];
                 if (put && h < p.Hk) {
-                    a.put(v + h * hs + w.at0);
-                    b.put(v + h * hs + w.at1);
+                    *reinterpret_cast<uint4 *>(v + h * hs + w.at0) = sh.ring[slot][0][threadIdx.x];
+                    *reinterpret_cast<uint4 *>(v + h * hs + w.at1) = sh.ring[slot][1][threadIdx.x];
                 }
                 fetch(slot);
                 if (++slot == kFwdDepth) slot = 0;
@@ -383,6 +347,7 @@ template <int D, typename T, bool kInter, bool kAll, bool kOne>
 __global__ void __launch_bounds__(kThreads, kBwdCtas) attn_prologue_bwd_kernel(AttnPrologueArgs p, Units uq, Units uk, int cq,
                                                                                float *__restrict__ partial) {
     using Y = Layout<D, T>;
+    using C = Chunks<T, kInter>;
     constexpr int N = Y::kPairs;
     extern __shared__ __align__(16) uint8_t raw[];
     BwdShared<D, T> &sh = *reinterpret_cast<BwdShared<D, T> *>(raw);
@@ -434,49 +399,41 @@ __global__ void __launch_bounds__(kThreads, kBwdCtas) attn_prologue_bwd_kernel(A
     int pos = position(u);
     Freqs fr;
     fr.load(p, lane);
-    stage_gain<D>(keys ? p.gk : p.gq, sh.gain);
+    stage_gain<D, C>(keys ? p.gk : p.gq, sh.gain);
     __syncthreads();
-    F2 g0[N], g1[N], a0[N], a1[N];
-    load_pairs(sh.gain + w.at0, g0);
-    load_pairs(sh.gain + w.at1, g1);
+    F2 gu[N], gv[N], au[N], av[N];
+    C::pairs(sh.gain + w.at0, sh.gain + w.at1, gu, gv);
 #pragma unroll
-    for (int i = 0; i < N; ++i) a0[i] = a1[i] = f2(0.f, 0.f);
+    for (int i = 0; i < N; ++i) au[i] = av[i] = f2(0.f, 0.f);
     int slot = 0;
     for (; u < un.count; u += un.stride) {
         const int tok = un.token(u, grp), h0 = kOne || tok < p.T ? un.head(u, grp) : H;
         GDR2_DCHECK(tok >= 0 && tok < p.T + tokens - 1 && slot % kBwdBurst >= 0 && slot < kBwdDepth);
         const int npos = position(u + un.stride);
         fr.angles<D>(p, pos, tokens, sh.cs[warp], lane);
-        Turn<T> t;
-        load_turn<D, T, kInter>(w, cs, cs + D / 2, t);
-#pragma unroll
-        for (int i = 0; i < N; ++i) t.s0[i] = neg(t.s0[i]), t.s1[i] = neg(t.s1[i]);  // the transposed rotation
+        F2 tc[N], ts[N];
+        load_turn<D, T, kInter>(w, cs, cs + D / 2, tc, ts);
         T *out = dx + (size_t)tok * sdx + (size_t)h0 * D;
 #pragma unroll 1
         for (int i = 0, h = h0; i < rows; ++i, h += step, out += step * D) {
             if (slot % kBwdBurst == 0) cp_wait<kBwdBurst>();
-            Chunk<T> a, b;
-            a.v = sh.ring[slot][0][threadIdx.x];
-            b.v = sh.ring[slot][1][threadIdx.x];
-            F2 d0[N], d1[N], z0[N], z1[N];
-            a.get(d0);
-            b.get(d1);
-            turn<T, kInter, kAll>(t, w.on0, w.on1, d0, d1, z0, z1);
+            F2 u[N], v[N], y[N], z[N];
+            C::get(sh.ring[slot][0][threadIdx.x], sh.ring[slot][1][threadIdx.x], u, v);
+#pragma unroll
+            for (int i = 0; i < N; ++i)  // the transposed rotation
+                turn<kAll>(w.on(i), tc[i], ts[i], tc[i], neg(ts[i]), u[i], v[i], y[i], z[i]);
             if (p.norm) {
-                F2 x0[N], x1[N];
-                a.v = sh.ring[slot][2][threadIdx.x];
-                b.v = sh.ring[slot][3][threadIdx.x];
-                a.get(x0);
-                b.get(x1);
+                F2 xu[N], xv[N];
+                C::get(sh.ring[slot][2][threadIdx.x], sh.ring[slot][3][threadIdx.x], xu, xv);
                 F2 q = f2(0.f, 0.f), m = q;
 #pragma unroll
                 for (int i = 0; i < N; ++i) {
-                    q = fma(x0[i], x0[i], q);
-                    q = fma(x1[i], x1[i], q);
-                    d0[i] = mul(x0[i], z0[i]);
-                    d1[i] = mul(x1[i], z1[i]);
-                    m = fma(g0[i], d0[i], m);
-                    m = fma(g1[i], d1[i], m);
+                    q = fma(xu[i], xu[i], q);
+                    q = fma(xv[i], xv[i], q);
+                    u[i] = mul(xu[i], y[i]);
+                    v[i] = mul(xv[i], z[i]);
+                    m = fma(gu[i], u[i], m);
+                    m = fma(gv[i], v[i], m);
                 }
                 const float qs = sum_row<Y::kLanes>(sum2(q)), ms = sum_row<Y::kLanes>(sum2(m));
                 const float n = rsqrtf(qs * (1.f / D) + p.eps), c = -ms * (1.f / D) * n * n;
@@ -484,14 +441,14 @@ __global__ void __launch_bounds__(kThreads, kBwdCtas) attn_prologue_bwd_kernel(A
                 if (h < H) {  // a lane without a row has n = eps^-1/2, infinite for eps = 0
 #pragma unroll
                     for (int i = 0; i < N; ++i) {
-                        a0[i] = fma(d0[i], nn, a0[i]);
-                        a1[i] = fma(d1[i], nn, a1[i]);
+                        au[i] = fma(u[i], nn, au[i]);
+                        av[i] = fma(v[i], nn, av[i]);
                     }
                 }
 #pragma unroll
                 for (int i = 0; i < N; ++i) {
-                    z0[i] = mul(fma(cc, x0[i], mul(g0[i], z0[i])), nn);
-                    z1[i] = mul(fma(cc, x1[i], mul(g1[i], z1[i])), nn);
+                    y[i] = mul(fma(cc, xu[i], mul(gu[i], y[i])), nn);
+                    z[i] = mul(fma(cc, xv[i], mul(gv[i], z[i])), nn);
                 }
             }
             if (++slot % kBwdBurst == 0) {
@@ -499,10 +456,7 @@ __global__ void __launch_bounds__(kThreads, kBwdCtas) attn_prologue_bwd_kernel(A
                 for (int x = kBwdBurst; x > 0; --x) fetch(slot - x);
                 if (slot == kBwdDepth) slot = 0;
             }
-            if (h < H) {
-                Chunk<T>::store(out + w.at0, z0);
-                Chunk<T>::store(out + w.at1, z1);
-            }
+            if (h < H) C::put(out + w.at0, out + w.at1, y, z);
         }
         pos = npos;
     }
@@ -514,8 +468,8 @@ __global__ void __launch_bounds__(kThreads, kBwdCtas) attn_prologue_bwd_kernel(A
     float *red = reinterpret_cast<float *>(&sh.ring[0][0][0]), *mine = red + (warp * Y::kRows + grp) * D;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        split(a0[i], mine[w.at0 + 2 * i], mine[w.at0 + 2 * i + 1]);
-        split(a1[i], mine[w.at1 + 2 * i], mine[w.at1 + 2 * i + 1]);
+        split(au[i], mine[C::element(i, 0, false, w.at0, w.at1)], mine[C::element(i, 1, false, w.at0, w.at1)]);
+        split(av[i], mine[C::element(i, 0, true, w.at0, w.at1)], mine[C::element(i, 1, true, w.at0, w.at1)]);
     }
     __syncthreads();
     if (threadIdx.x < D) {
