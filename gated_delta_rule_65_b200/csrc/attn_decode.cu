@@ -8,16 +8,17 @@
 // Bound: each K and V element is read once and used 2 G times (G = Hq / Hk query heads of a KV head), G operations a
 // byte of bf16 against the 250 of the GPU's balance, so HBM bounds the step for every head layout and the M = 128
 // tiles of tcgen05 would be at most an eighth full. The products run on warp-level m16n8k16 matrix instructions
-// instead, whose sixteen rows hold the query heads of a KV head; at 6.1 TB/s they are busy a fifth of the time. Up to 8 heads leave half the rows free: there the eight upper rows carry the low halves of p (p = hi + lo in
-// bf16), so that rounding p costs 2^-17 and no further instruction. 9 to 16 heads take a second product for lo.
+// instead, whose sixteen rows hold the query heads of a KV head; at 6.2 TB/s they are busy a fifth of the time. Up to 8
+// heads leave half the rows free: there the eight upper rows carry the low halves of p (p = hi + lo in bf16), so that
+// rounding p costs 2^-17 and no further instruction. 9 to 16 heads take a second product for lo.
 // fp32 caches run the same schedule on fp32 multiply-adds (tf32 products would lose 13 bits).
 //
 // Work split: the tiles (64 tokens; 32 for fp32 heads of 128) of all (sequence, KV head) rows lie on one line, and each
 // CTA takes an equal run of it, whatever the lengths: one long sequence spreads over the whole GPU, a ragged batch
 // leaves no CTA idle, and a row that lies in one CTA is finished there. More query heads of a KV head than one CTA holds
-// go to neighbouring CTAs with the same run, which find each other's tiles in L2. Rows cut by a border leave (m, l, o) in the
-// workspace, and a second kernel joins them in the order of the line: no atomics, the same bits every call. The split
-// depends on the lengths alone, which only the GPU reads (a captured graph stays valid as sequences grow).
+// go to neighbouring CTAs with the same run, which find each other's tiles in L2. Rows cut by a border leave (m, l, o) in
+// the workspace, and a second kernel joins them in the order of the line: no atomics, the same bits every call. The
+// split depends on the lengths alone, which only the GPU reads (a captured graph stays valid as sequences grow).
 //
 // Inside a CTA each of 4 warps takes a quarter of every tile through its own ring of cp.async stages (16 KB) with its
 // own (m, l, o), so the main loop has no barrier; the warps' results meet at the end of a row. Two CTAs to an SM for
@@ -28,7 +29,7 @@
 // Measured on one B200, back to back: 256 sequences of 100 to 4,096 tokens in a window of 2,048 (16 / 4 heads of 128,
 // bf16, pages of 16) in 133 us (829 MB, 6.2 TB/s, 95% of the measured copy); 3 sequences of 50,001 to 65,536 tokens (16 /
 // 2 heads) in 37 us (183 MB, 75%: about 7 us of it are the start, the end and the join); 33 ragged fp32 sequences of up
-// to 2,000 tokens (12 / 6 heads of 64) in 27 us (107 MB, 61%).
+// to 2,000 tokens (12 / 6 heads of 64) in 26 us (107 MB, 63%).
 #include <math.h>
 
 #include "attn.h"

@@ -18,9 +18,9 @@
 // another: the rotation needs no exchange between lanes, a warp takes four bf16 rows of 128 channels at once, and all
 // arithmetic runs on pairs of floats. A lane keeps ONE token and walks its heads, so the coefficients (gain, cosine and
 // sine folded together) stay in registers for all of them and the token's angles are formed once, by the whole warp. All
-// lane groups of a warp share a token where its heads fill them, else several tokens share the warp. Every
-// lane feeds itself: cp.async into shared memory that only it reads, several rows deep and running on into the next
-// token, so that nothing but a warp's own exchange of angles ever waits.
+// lane groups of a warp share a token where its heads fill them, else several tokens share the warp. Every lane feeds
+// itself: cp.async into shared memory that only it reads, several rows deep and running on into the next token, so that
+// nothing but a warp's own exchange of angles ever waits.
 //
 // Measured on one B200, back to back: that batch forward in 89 us (537 MB, 6.0 TB/s, 92% of the measured copy) and
 // backward in 138 us (805 MB, 5.8 TB/s, 89%); 17,820 new tokens of 16 packed prompts (16 + 4 + 4 heads) into the pages in
@@ -37,9 +37,8 @@ constexpr int kThreads = 256, kWarps = kThreads / 32;
 // CTAs on an SM and rows of a lane in flight, measured on the training batch (B = 8, T = 4096, 16 + 16 heads of 128
 // channels, bf16), kernel times with their events (about 3 us). Forward, 2 CTAs: 92 us with 4 to 8 rows (and 16 packed
 // prompts into the cache 49.1 us with 4, 49.9 with 8); 3 CTAs: 118 to 130 us with 4 to 8 rows (spills, and more warps on
-// more tokens scatter the requests). Backward, 2 CTAs: 173 us
-// fetching row by row (4 rows ahead), 141 in bursts of 2 and 145 of 3; 1 CTA: 149 row by row, 143 and 146 in bursts of
-// 2 and 4.
+// more tokens scatter the requests). Backward, 2 CTAs: 173 us fetching row by row (4 rows ahead), 141 in bursts of 2 and
+// 145 of 3; 1 CTA: 149 row by row, 143 and 146 in bursts of 2 and 4.
 constexpr int kFwdCtas = 2, kFwdDepth = 4;
 constexpr int kBwdCtas = 2, kBwdBurst = 2, kBwdDepth = 2 * kBwdBurst;
 constexpr int kBwdGrid = kBwdCtas * kAttnSms;  // CTAs of the backward (a partial sum of dgq or dgk each)
