@@ -423,17 +423,17 @@ __device__ __forceinline__ void move_pages(const KvPagesArgs &a, const Lists &w,
         a.ref_out[dst] = n;
         a.ref_out[src] = 0;
     }
-    const int E = a.R * a.P;
-    for (int b = t.gid; b < E; b += 4 * t.threads) {
+    const uint32_t E = (uint32_t)a.R * a.P, th = t.threads;  // E < 2^31 and a step over the grid behind it: unsigned holds both
+    for (uint32_t b = t.gid; b < E; b += 4 * th) {
         int e[4], k[4];
 #pragma unroll
-        for (int x = 0; x < 4; ++x) e[x] = (long long)b + x * t.threads < E ? entry(a.table, b + x * t.threads, a.num_pages) : -1;
+        for (int x = 0; x < 4; ++x) e[x] = b + x * th < E ? entry(a.table, b + x * th, a.num_pages) : -1;
 #pragma unroll
         for (int x = 0; x < 4; ++x) k[x] = e[x] >= live ? __ldcg(w.rank + e[x]) : -1;
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
             if (k[x] >= 0) e[x] = __ldcg(w.pages + k[x]);
-            if ((long long)b + x * t.threads < E) a.table_out[b + x * t.threads] = e[x];
+            if (b + x * th < E) a.table_out[b + x * th] = e[x];
         }
     }
     copy_rows(moves, w.high, w.pages, nullptr, bl, t.warp, t.warps, t.lane);
