@@ -146,6 +146,14 @@ __device__ __forceinline__ void prefix(const int *t, int warps, int *pre, int la
         }
     if (lane == 31) pre[warps] = at;
 }
+// The warp's total. It is zero in nearly every call: then one vote tells.
+__device__ __forceinline__ long long total(long long x) {
+    if (!__any_sync(0xffffffffu, x != 0)) return 0;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    return x;
+}
+constexpr long long kMost = 0x7fffffff;  // counts are held to it
 // The free page of a rank: the strip whose list holds it, and its place there.
 __device__ __forceinline__ int free_page(const int *pages, const int *pre, int rank, int warps, int length) {
     int a = 0, e = warps;  // pre[a] <= rank < pre[e]
@@ -211,7 +219,8 @@ __global__ void __launch_bounds__(kThreads) kv_reserve_kernel(KvPagesArgs a, Lis
     const Place t = place();
     const int E = a.R * a.P, ps = a.page_size;
     follow();
-    __shared__ int need[kMaxWarps + 1], free[kMaxWarps + 1], past[kMaxWarps + 1], sums[3][kThreads / 32];
+    __shared__ int need[kMaxWarps + 1], free[kMaxWarps + 1], sums[3][kThreads / 32];
+    __shared__ long long past;
     const bool one = gridDim.x == 1;
     int *ta = one ? sums[0] : w.ta, *tb = one ? sums[1] : w.tb, *tc = one ? sums[2] : w.tc;
     const Strip es = strip(E, t.warp, t.warps), pg = strip(a.num_pages, t.warp, t.warps);
@@ -260,25 +269,30 @@ __global__ void __launch_bounds__(kThreads) kv_reserve_kernel(KvPagesArgs a, Lis
         }
         if (t.lane < kAhead && b + 32 * t.lane < es.last) w.needs[b / 32 + t.lane] = words;  // strips start at whole words
     }
-    int over = 0;  // pages past the table's end
+    long long over = 0;  // pages past the table's end
     for (int r = t.gid; r < a.R; r += t.threads) {
         const int want = a.want[r];
         if (want > 0) over += max(0, (want - 1) / ps + 1 - a.P);
     }
-    over = __reduce_add_sync(0xffffffffu, over);
+    over = min(total(over), kMost);
     if (a.window > 0) {
         cl.sync();
         nfree = list_free(a.ref_out, pg, w.pages, nullptr, t.lane);
     }
-    if (t.lane == 0) ta[t.warp] = c, tb[t.warp] = nfree, tc[t.warp] = over;
+    if (t.lane == 0) ta[t.warp] = c, tb[t.warp] = nfree, tc[t.warp] = (int)over;
     cl.sync();
     if (threadIdx.x < 32) prefix(ta, t.warps, need, t.lane);
     if (threadIdx.x / 32 == 1) prefix(tb, t.warps, free, t.lane);
-    if (threadIdx.x / 32 == 2) prefix(tc, t.warps, past, t.lane);
+    if (threadIdx.x / 32 == 2) {
+        long long x = 0;
+        for (int i = t.lane; i < t.warps; i += 32) x += *static_cast<const volatile int *>(tc + i);
+        x = total(x);
+        if (t.lane == 0) past = x;
+    }
     __syncthreads();
     const int all = free[t.warps], length = strip_length(a.num_pages, t.warps);
     int rank0 = need[t.warp];
-    if (t.gid == 0) *a.count_out = past[t.warps] + max(0, need[t.warps] - all);
+    if (t.gid == 0) *a.count_out = (int)min(past + max(0, need[t.warps] - all), kMost);
     if (c == 0) return;
     for (int g = es.first / 32; g * 32 < es.last; g += 32) {
         const int mine = (g + t.lane) * 32 < es.last ? __ldcg(w.needs + g + t.lane) : 0;
@@ -533,7 +547,8 @@ Blocks blocks(const KvPagesArgs &a) {
 // 17.6 (14.5 and 10.5); 256 forks of up to 33 MB: 26.6 and 19.7.
 constexpr long long kOwnCopy = 4 << 20;
 bool own_copy(const Blocks &bl, long long most) {
-    return most * 2 * bl.Hk * bl.page_size * bl.row_bytes <= kOwnCopy;  // most < 2^31, the block's bytes < 2^32
+    const long long page = 2LL * bl.Hk * bl.page_size * bl.row_bytes;  // below 2^43: copies_fit
+    return most <= kOwnCopy / page;
 }
 
 // CTAs of a copy over the whole GPU: a warp for each 4 KB that may move, eight CTAs an SM at most.

@@ -544,6 +544,16 @@ def _device(*tensors):
     return index
 
 
+_MOST = 2**31 - 1
+
+
+def _narrow(**sizes):
+    """Names the size that the library's 32-bit arguments do not hold."""
+    for name, n in sizes.items():
+        if not -_MOST <= n <= _MOST:
+            raise ValueError(f"gdr2: {name} = {n} is too large")
+
+
 def _p(t):
     return None if t is None else t.data_ptr()
 
@@ -717,7 +727,8 @@ def attn_prologue_cache(xq, xk, xv, gq, gk, seq, pos, freqs, k_pages, v_pages, t
                         mag=1.0, interleaved=False, q=None, stream=None):
     """gdr2_attn_prologue_cache: the prologue for new tokens xq [T, Hq, d], xk, xv [T, Hk, d]; token t is token
     pos[t] of sequence seq[t] (int32; outside [0, R): padding). Keys and values go to the pools k_pages, v_pages
-    [num_pages, Hk, page_size, d] by table int32 [R, P]; q is returned (padding rows as they were)."""
+    [num_pages, Hk, page_size, d] by table int32 [R, P]; q is returned (padding rows as they were; in a fresh q they hold
+    no value)."""
     T, Hq, Hk, d, sq, sk, dt, rot = _prologue_checks(xq, xk, gq, gk, pos, freqs, norm)
     Tv, Hv, dv, sv = _token_rows("xv", xv, xq.dtype)
     if pos is None:
@@ -730,6 +741,8 @@ def attn_prologue_cache(xq, xk, xv, gq, gk, seq, pos, freqs, k_pages, v_pages, t
         _refuse(xq.dtype, (k_pages, v_pages), table, seq=(seq, (T,)))
     num, Hp, ps, dp = shape
     R, P = tshape
+    if R > _MOST or P > _MOST:
+        _narrow(R=R, P=P)
     if Tv != T or Hv != Hk or dv != d or Hp != Hk or dp != d:
         raise ValueError("gdr2: xk, xv and the pools must agree in tokens, heads and channels")
     if q is None:
@@ -753,7 +766,8 @@ def attn_decode(q, k_pages, v_pages, table, lens, seq=None, *, scale=None, windo
                 lse=None, workspace=None, stream=None):
     """gdr2_attn_decode: attention of one new token for each row of q [N, Hq, d] over sequence seq[n] (int32 [N];
     None: n) of the cache, its last `window` tokens (0: all), lens int32 [R] with the new token counted. scale: by
-    default d^-1/2. Returns o [N, Hq, d], or (o, lse fp32 [N, Hq]) with want_lse or a given lse."""
+    default d^-1/2. Returns o [N, Hq, d], or (o, lse fp32 [N, Hq]) with want_lse or a given lse (slots whose seq is outside
+    [0, R) keep their rows; in fresh outputs those hold no value)."""
     dtype, dt = q.dtype, _dtype_code(q)
     qshape, shape, tshape, index = q.shape, k_pages.shape, table.shape, q.get_device()
     if len(qshape) != 3 or not q.is_contiguous():
@@ -765,6 +779,8 @@ def attn_decode(q, k_pages, v_pages, table, lens, seq=None, *, scale=None, windo
         _refuse(dtype, (k_pages, v_pages), table, lens=(lens, tshape[:1]), seq=(seq, qshape[:1]))
     num, Hk, ps, dp = shape
     R, P = tshape
+    if R > _MOST or P > _MOST or not -_MOST <= window <= _MOST:
+        _narrow(R=R, P=P, window=window)
     if dp != d:
         raise ValueError("gdr2: q and the pools must agree in channels")
     _device(q, o, lse)
@@ -808,6 +824,8 @@ def kv_reserve(table, lens, want, ref, *, page_size, window=0, out=None, workspa
             _fine(index, _I32, table, lens, want, ref)):
         _refuse(None, None, table, lens=(lens, rows), want=(want, rows), ref=(ref, (num,)))
     R, P = shape
+    if R > _MOST or P > _MOST or num > _MOST or not (-_MOST <= page_size <= _MOST and -_MOST <= window <= _MOST):
+        _narrow(R=R, P=P, num_pages=num, page_size=page_size, window=window)
     _device(table)
     t = r = m = None
     if out is not None:
@@ -835,6 +853,8 @@ def kv_fork(table, lens, ref, parent, k_pages, v_pages, *, out=None, workspace=N
             _fine(index, k_pages.dtype, k_pages, v_pages)):
         _refuse(None, (k_pages, v_pages), table, lens=(lens, rows), parent=(parent, rows), ref=(ref, pool[:1]))
     (R, P), (num, Hk, ps, d) = shape, pool
+    if R > _MOST or P > _MOST:
+        _narrow(R=R, P=P)
     _device(table)
     t = n = r = m = None
     if out is not None:
@@ -863,6 +883,8 @@ def kv_compact(table, ref, k_pages, v_pages, *, out=None, workspace=None, stream
             _fine(index, _I32, table, ref) and _fine(index, k_pages.dtype, k_pages, v_pages)):
         _refuse(None, (k_pages, v_pages), table, ref=(ref, pool[:1]))
     (R, P), (num, Hk, ps, d) = shape, pool
+    if R > _MOST or P > _MOST:
+        _narrow(R=R, P=P)
     _device(table)
     t = r = m = None
     if out is not None:

@@ -476,7 +476,8 @@ GDR2_API int gdr2_attn_decode(const void *q, const void *k_pages, const void *v_
  * gdr2_kv_reserve: pages for tokens [lens[r], want[r]) of every sequence: its entries j with
  * lens[r] / page_size <= j < ceil(want[r] / page_size) that have no page get one (want[r] = 0 asks for none). With
  * window > 0 the pages that lie wholly behind the window of the token at lens[r] are released first. missing (int32
- * [1]): how many pages were asked for and not found, past the table's end included; their entries stay empty.
+ * [1]): how many pages were asked for and not found, past the table's end included, held to 2^31 - 1; their entries
+ * stay empty.
  * table_out may be table and ref_out may be ref.
  *
  * gdr2_kv_fork: every sequence r takes over the content that sequence parent[r] had before the call: r itself (it

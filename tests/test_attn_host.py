@@ -194,6 +194,16 @@ def test_binding_refuses_wrong_shapes_before_it_looks_at_devices():
             f()
 
 
+def test_binding_refuses_sizes_beyond_32_bits():
+    pools = bf(9, 2, 16, 64), bf(9, 2, 16, 64)
+    for f in (lambda: gdr2.attn_decode(bf(3, 4, 64), *pools, i32(3, 5), i32(3), window=2**32 + 5),
+              lambda: gdr2.attn_decode(bf(3, 4, 64), *pools, i32(3, 5), i32(3), window=5 - 2**32),
+              lambda: gdr2.kv_reserve(i32(3, 5), i32(3), i32(3), i32(9), page_size=2**32 + 16),
+              lambda: gdr2.kv_reserve(i32(3, 5), i32(3), i32(3), i32(9), page_size=16, window=2**40)):
+        with pytest.raises(ValueError, match="too large"):
+            f()
+
+
 # ---- rotary frequencies -----------------------------------------------------------------------------------------
 
 

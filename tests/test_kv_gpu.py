@@ -128,6 +128,38 @@ def test_empty_and_full_pools():
     assert m.tolist() == [1] and t.tolist() == [[4, 2, 0, 1, 3, -1]]
 
 
+def test_missing_pages_are_held_to_32_bits():
+    table = [[-1, -1], [0, -1], [-1, -1]]
+    for want in ([2**31 - 1, 5, 0], [2**31 - 1] * 3, [2**31 - 1, 3, 2], [2, 3, 4]):
+        t, r, m = ref.reserve(table, [0, 1, 0], want, [1, 0, 0], 1)
+        to, ro, mo = gdr2.kv_reserve(ints(table), ints([0, 1, 0]), ints(want), ints([1, 0, 0]), page_size=1)
+        assert (to.tolist(), ro.tolist(), mo.tolist()) == (t, r, [min(m, 2**31 - 1)])
+
+
+@pytest.mark.parametrize("num", [4, 40000])
+def test_compact_largest_table(num):
+    """The table of the largest allowed size, in place (8.6 GB): places up to its end and a step of the grid behind."""
+    P = 0x7fff0000
+    table = torch.full((1, P), -1, dtype=torch.int32, device="cuda")
+    last = [num - 1, num - 2, 0]
+    table[0, -3:] = ints(last)
+    table[0, 5] = num - 2
+    refs = torch.zeros(num, dtype=torch.int32, device="cuda")
+    refs[num - 1], refs[num - 2], refs[0] = 1, 2, 1
+    k = torch.randn(num, 1, 1, 64, device="cuda").bfloat16()
+    v = torch.randn(num, 1, 1, 64, device="cuda").bfloat16()
+    k0, v0 = k.clone(), v.clone()
+    t, r, live = gdr2.kv_compact(table, refs, k, v, out={"table": table})
+    assert t is table and live.tolist() == [3]
+    moved = {0: 0, num - 2: 1 if num > 4 else 2, num - 1: 2 if num > 4 else 1}  # 4 pages: 3 moves to 1, 2 stays
+    assert t[0, -3:].tolist() == [moved[x] for x in last] and t[0, 5].item() == moved[num - 2]
+    assert int((t >= 0).sum()) == 4 and r[:3].sum().item() == 4 and int((r > 0).sum()) == 3
+    for a, b in moved.items():
+        assert torch.equal(k[b], k0[a]) and torch.equal(v[b], v0[a])
+    del table, t
+    torch.cuda.empty_cache()
+
+
 def test_captured_bookkeeping():
     """reserve, fork and compact as one captured graph, replayed twice on the same inputs."""
     rng = random.Random(3)
