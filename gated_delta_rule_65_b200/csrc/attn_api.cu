@@ -69,6 +69,11 @@ bool copies_fit(int Hk, int page_size, int d, int num_pages, int dtype) {
 
 int done(cudaError_t e) { return e == cudaSuccess ? GDR2_OK : GDR2_ERR_CUDA; }
 
+// The record of a call, if it is one.
+template <typename A> const A *record(const void *args, size_t bytes) {
+    return args != nullptr && aligned(args, 8) && bytes == sizeof(A) ? static_cast<const A *>(args) : nullptr;
+}
+
 }  // namespace
 
 extern "C" {
@@ -248,6 +253,58 @@ int gdr2_kv_compact(const int *table, const int *ref, int *table_out, int *ref_o
     a.R = R; a.P = P; a.page_size = page_size; a.num_pages = num_pages; a.Hk = Hk; a.d = d; a.dtype = dtype;
     a.workspace = workspace;
     return done(gdr2::launch_kv_compact(a, (cudaStream_t)stream));
+}
+
+int gdr2_attn_call(int call, const void *args, size_t bytes) {
+    switch (call) {
+    case GDR2_CALL_ATTN_PROLOGUE_FWD:
+        if (const auto *r = record<gdr2_attn_prologue_fwd_args>(args, bytes))
+            return gdr2_attn_prologue_fwd(
+                r->xq, r->xk, r->gq, r->gk, r->norm, r->eps, r->pos, r->freqs, r->mag, r->rot, r->interleaved,
+                r->q, r->k, r->T, r->Hq, r->Hk, r->d, r->dtype, r->xq_stride, r->xk_stride, r->stream);
+        break;
+    case GDR2_CALL_ATTN_PROLOGUE_BWD:
+        if (const auto *r = record<gdr2_attn_prologue_bwd_args>(args, bytes))
+            return gdr2_attn_prologue_bwd(
+                r->xq, r->xk, r->gq, r->gk, r->norm, r->eps, r->pos, r->freqs, r->mag, r->rot, r->interleaved,
+                r->dq, r->dk, r->dxq, r->dxk, r->dgq, r->dgk, r->T, r->Hq, r->Hk, r->d, r->dtype, r->xq_stride,
+                r->xk_stride, r->dxq_stride, r->dxk_stride, r->workspace, r->workspace_bytes, r->stream);
+        break;
+    case GDR2_CALL_ATTN_PROLOGUE_CACHE:
+        if (const auto *r = record<gdr2_attn_prologue_cache_args>(args, bytes))
+            return gdr2_attn_prologue_cache(
+                r->xq, r->xk, r->xv, r->gq, r->gk, r->norm, r->eps, r->seq, r->pos, r->freqs, r->mag, r->rot,
+                r->interleaved, r->q, r->k_pages, r->v_pages, r->table, r->T, r->Hq, r->Hk, r->d, r->R, r->P,
+                r->page_size, r->num_pages, r->dtype, r->xq_stride, r->xk_stride, r->xv_stride, r->stream);
+        break;
+    case GDR2_CALL_ATTN_DECODE:
+        if (const auto *r = record<gdr2_attn_decode_args>(args, bytes))
+            return gdr2_attn_decode(
+                r->q, r->k_pages, r->v_pages, r->table, r->lens, r->seq, r->scale, r->window, r->o, r->lse, r->N,
+                r->Hq, r->Hk, r->d, r->R, r->P, r->page_size, r->num_pages, r->dtype, r->workspace,
+                r->workspace_bytes, r->stream);
+        break;
+    case GDR2_CALL_KV_RESERVE:
+        if (const auto *r = record<gdr2_kv_reserve_args>(args, bytes))
+            return gdr2_kv_reserve(
+                r->table, r->lens, r->want, r->ref, r->table_out, r->ref_out, r->missing, r->R, r->P, r->page_size,
+                r->num_pages, r->window, r->workspace, r->workspace_bytes, r->stream);
+        break;
+    case GDR2_CALL_KV_FORK:
+        if (const auto *r = record<gdr2_kv_fork_args>(args, bytes))
+            return gdr2_kv_fork(
+                r->table, r->lens, r->ref, r->parent, r->table_out, r->lens_out, r->ref_out, r->missing,
+                r->k_pages, r->v_pages, r->R, r->P, r->Hk, r->page_size, r->d, r->num_pages, r->dtype,
+                r->workspace, r->workspace_bytes, r->stream);
+        break;
+    case GDR2_CALL_KV_COMPACT:
+        if (const auto *r = record<gdr2_kv_compact_args>(args, bytes))
+            return gdr2_kv_compact(
+                r->table, r->ref, r->table_out, r->ref_out, r->live, r->k_pages, r->v_pages, r->R, r->P, r->Hk,
+                r->page_size, r->d, r->num_pages, r->dtype, r->workspace, r->workspace_bytes, r->stream);
+        break;
+    }
+    return GDR2_ERR_INVALID_ARG;
 }
 
 }  // extern "C"

@@ -194,6 +194,27 @@ def test_binding_refuses_wrong_shapes_before_it_looks_at_devices():
             f()
 
 
+@pytest.mark.parametrize("name,base,cases", [
+    ("gdr2_attn_prologue_fwd", FWD, COMMON + [(dict(q=None), ARG), (dict(k=OFF8), ARG)]),
+    ("gdr2_attn_prologue_bwd", BWD, COMMON + [(dict(dxk=None), ARG), (dict(dgq=ODD), ARG), (dict(sdk=132), ARG), (dict(wsb=16), WS)]),
+    ("gdr2_attn_prologue_cache", CACHE, COMMON + [(dict(table=ODD), ARG), (dict(num=-1), ARG), (dict(sv=4), ARG)]),
+    ("gdr2_attn_decode", DECODE, [(dict(seq=ODD), ARG), (dict(lse=ODD), ARG), (dict(window=-1), ARG), (dict(Hq=5), ARG),
+                                  (dict(dtype=-1), ARG), (dict(ps=-4), ARG), (dict(ws=None), WS), (dict(wsb=1000), WS)]),
+    ("gdr2_kv_reserve", RESERVE, PAGES + [(dict(want=None), ARG), (dict(m=None), ARG), (dict(window=-1), ARG)]),
+    ("gdr2_kv_fork", FORK, PAGES + [(dict(parent=None), ARG), (dict(n=FAKE), ARG), (dict(kp=OFF8), ARG), (dict(dtype=3), ARG)]),
+    ("gdr2_kv_compact", COMPACT, PAGES + [(dict(live=None), ARG), (dict(vp=None), ARG), (dict(d=100), UNS)])],
+    ids=lambda x: x if isinstance(x, str) else "")
+def test_records(name, base, cases):
+    """A call by its record refuses what the call itself refuses, and a record of another size."""
+    number, record = gdr2._CALLS[name]
+    for over, status in cases:
+        packed = record.pack(*(0 if x is None else x for x in {**base, **over}.values()))
+        assert gdr2.lib().gdr2_attn_call(number, packed, record.size) == status, over
+    assert gdr2.lib().gdr2_attn_call(number, packed, record.size - 8) == ARG
+    assert gdr2.lib().gdr2_attn_call(number, None, record.size) == ARG
+    assert gdr2.lib().gdr2_attn_call(7, packed, record.size) == ARG
+
+
 def test_binding_refuses_sizes_beyond_32_bits():
     pools = bf(9, 2, 16, 64), bf(9, 2, 16, 64)
     for f in (lambda: gdr2.attn_decode(bf(3, 4, 64), *pools, i32(3, 5), i32(3), window=2**32 + 5),
