@@ -544,7 +544,8 @@ Blocks blocks(const KvPagesArgs &a) {
 // Up to so many bytes of pages (the most that a call can move) the cluster copies them itself: eight SMs move them in
 // the time that another launch takes. 32 forks of up to 1 MB: 17.7 us a call with the copies inside and 19.8 with a
 // kernel for them (host-bound; 16.5 and 14.5 us on the device alone); a compaction of 512 pages (1.8 MB): 15.2 and
-// 17.6 (14.5 and 10.5); 256 forks of up to 33 MB: 26.6 and 19.7.
+// 17.6 (14.5 and 10.5); 256 forks of up to 33 MB: 26.6 and 19.7. (Calls with their
+// arguments one by one; by the record the 32 forks take 17.0 us and the compaction 14.7 with the copies inside.)
 constexpr long long kOwnCopy = 4 << 20;
 bool own_copy(const Blocks &bl, long long most) {
     const long long page = 2LL * bl.Hk * bl.page_size * bl.row_bytes;  // below 2^43: copies_fit
