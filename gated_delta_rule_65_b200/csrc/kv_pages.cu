@@ -269,10 +269,10 @@ __global__ void __launch_bounds__(kThreads) kv_reserve_kernel(KvPagesArgs a, Lis
         }
         if (t.lane < kAhead && b + 32 * t.lane < es.last) w.needs[b / 32 + t.lane] = words;  // strips start at whole words
     }
-    long long over = 0;  // pages past the table's end
+    long long over = 0;  // entries past the table's end: from the one of token lens[r] on, if that lies there too
     for (int r = t.gid; r < a.R; r += t.threads) {
-        const int want = a.want[r];
-        if (want > 0) over += max(0, (want - 1) / ps + 1 - a.P);
+        const int want = a.want[r], last = want > 0 ? (want - 1) / ps + 1 : 0;
+        if (last > a.P) over += max(0, last - max(a.P, a.lens[r] / ps));
     }
     over = min(total(over), kMost);
     if (a.window > 0) {

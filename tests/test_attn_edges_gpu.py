@@ -1,0 +1,60 @@
+"""Calls of the attention half at the edges of what its header allows, on the GPU: lengths beyond the page table."""
+from __future__ import annotations
+
+import pytest
+import torch
+
+from gated_delta_rule_65_b200 import gdr2
+
+pytestmark = pytest.mark.gpu
+
+
+def ints(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def reserve_by_entries(table, lens, want, ref, ps):
+    """The rule of the header entry by entry: j from lens / ps up to, but not with, ceil(want / ps); lowest pages first,
+    past the table's end none to be had."""
+    table, ref, missing = [list(row) for row in table], list(ref), 0
+    for r, row in enumerate(table):
+        for j in range(max(lens[r], 0) // ps, -(-max(want[r], 0) // ps)):
+            if j < len(row) and 0 <= row[j] < len(ref):
+                continue
+            page = min((i for i, n in enumerate(ref) if n <= 0), default=-1) if j < len(row) else -1
+            if page < 0:
+                missing += 1
+            else:
+                row[j], ref[page] = page, 1
+    return table, ref, missing
+
+
+@pytest.mark.parametrize("P,ps,lens,want", [
+    (2, 1, [5], [6]),              # one page asked for, past the table
+    (2, 1, [5], [5]),              # none
+    (4, 16, [100], [101]),         # entry 6 of 4
+    (4, 16, [100], [80]),          # fewer than there are: none
+    (4, 16, [64], [65]),           # the first entry past the table
+    (4, 16, [63], [129]),          # the last entry of the table and five past it
+    (4, 16, [-3], [200]),          # all of the table and nine past it
+    (4, 16, [100, 0, 2**31 - 1, 40], [100, 17, 2**31 - 1, 90]),
+    (3, 7, [21, 22, 2**31 - 1, 0], [22, 22, 0, -5]),
+], ids=str)
+@pytest.mark.parametrize("pages", [1, 9])
+def test_missing_counts_what_was_asked_for(P, ps, lens, want, pages):
+    R = len(lens)
+    table, refs = [[-1] * P for _ in range(R)], [0] * pages
+    et, er, em = reserve_by_entries(table, lens, want, refs, ps)
+    t, r, m = gdr2.kv_reserve(ints(table), ints(lens), ints(want), ints(refs), page_size=ps)
+    assert (t.tolist(), r.tolist(), m.tolist()) == (et, er, [em])
+
+
+def test_missing_of_many_sequences_beyond_the_table():
+    """A cluster of CTAs: only the sequences that ask for more count."""
+    R, P, ps = 9000, 3, 4
+    lens = [12 + r % 50 for r in range(R)]
+    want = [x + r % 3 for r, x in enumerate(lens)]
+    table = [[-1] * P for _ in range(R)]
+    em = reserve_by_entries(table, lens, want, [0] * 5, ps)[2]
+    t, r, m = gdr2.kv_reserve(ints(table), ints(lens), ints(want), ints([0] * 5), page_size=ps)
+    assert m.tolist() == [em] and int((t >= 0).sum()) == 0 and r.tolist() == [0] * 5
