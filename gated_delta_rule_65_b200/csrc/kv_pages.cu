@@ -378,7 +378,7 @@ __global__ void __launch_bounds__(kThreads) kv_fork_kernel(KvPagesArgs a, Lists 
                     if (e >= 0) atomicAdd(a.ref_out + e, 1);
                 }
                 a.table_out[i] = e;
-                if (j[x] == 0) a.lens_out[r[x]] = len[x];
+                if (j[x] == 0) a.lens_out[r[x]] = p[x] >= 0 ? __ldcg(a.lens + p[x]) : 0;  // as it is, inside the table or not
             }
         }
     }

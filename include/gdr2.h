@@ -485,7 +485,8 @@ GDR2_API int gdr2_attn_decode(const void *q, const void *k_pages, const void *v_
  * is 0). Full pages are shared. The last, partly filled page of a parent stays with one taker, together with pages
  * reserved beyond it: with the parent if it stays, else with the lowest r; every other taker gets the tokens of that
  * page copied to a fresh one (the rest of the fresh page is left as it was). missing: how many copies found no page;
- * those sequences end at their last full page. table_out and lens_out must not be table and lens; ref_out may be ref.
+ * those sequences end at their last full page. A length outside [0, P page_size] is taken over as it is; the pages then
+ * follow as for the nearest length inside. table_out and lens_out must not be table and lens; ref_out may be ref.
  *
  * gdr2_kv_compact: the live pages end up in [0, live): those numbered live or above move, in order, to the free numbers
  * below. table_out and ref_out follow, live (int32 [1]) is written. table_out may be table and ref_out may be ref.

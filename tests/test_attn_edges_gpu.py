@@ -58,3 +58,33 @@ def test_missing_of_many_sequences_beyond_the_table():
     em = reserve_by_entries(table, lens, want, [0] * 5, ps)[2]
     t, r, m = gdr2.kv_reserve(ints(table), ints(lens), ints(want), ints([0] * 5), page_size=ps)
     assert m.tolist() == [em] and int((t >= 0).sum()) == 0 and r.tolist() == [0] * 5
+
+
+@pytest.mark.parametrize("P", [4, 300])
+def test_fork_takes_lengths_over_as_they_are(P):
+    """A sequence that stays keeps its length, one that takes another's content gets that length, also where it lies
+    outside the table; a released one ends at 0."""
+    ps, R = 16, 7
+    lens = [P * ps + 5, -4, P * ps, 2**31 - 1, 20, 7, -2**31]
+    parent = [0, 1, 0, 3, 3, -1, 1]
+    table = [[-1] * P for _ in range(R)]
+    for r in (0, 3):
+        table[r] = list(range(r * P, r * P + P))
+    table[1][0], table[5][0] = 6 * P, 6 * P + 1
+    num = 6 * P + 2
+    refs = [0] * num
+    for row in table:
+        for e in row:
+            if e >= 0:
+                refs[e] += 1
+    k = torch.randn(num, 1, ps, 64, device="cuda")
+    v = torch.randn(num, 1, ps, 64, device="cuda")
+    k0, v0 = k.clone(), v.clone()
+    t, n, r, m = gdr2.kv_fork(ints(table), ints(lens), ints(refs), ints(parent), k, v)
+    assert n.tolist() == [lens[p] if p >= 0 else 0 for p in parent] and m.tolist() == [0]
+    # whole pages are shared, nothing is copied; a length below 0 shares none, and the one that stays keeps its page
+    assert t.tolist() == [table[0], table[1], table[0], table[3], table[3], [-1] * P, [-1] * P]
+    counts = [0] * num
+    for e in (e for row in t.tolist() for e in row if e >= 0):
+        counts[e] += 1
+    assert r.tolist() == counts and torch.equal(k, k0) and torch.equal(v, v0)
