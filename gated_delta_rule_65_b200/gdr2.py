@@ -585,25 +585,36 @@ def _call(name, *args):
         raise GDR2Error(name, st)
 
 
-def _keep(stream, *tensors):
-    """Fresh tensors that an explicit stream is about to use: their memory is not handed out again before that stream
-    has passed the call."""
-    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
-    for t in tensors:
+def _on(stream, call, args):
+    """call(**args) with `stream`, given explicitly, as the current one, so that the outputs and the workspace that the
+    call makes come from that stream's memory. (Out of the memory of the caller's current stream they could be what work
+    still queued there writes, which `stream` does not wait for.) The results are kept for the caller's stream too, which
+    may use them once it has waited."""
+    del args["stream"]
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+        stream = torch.cuda.ExternalStream(0 if handle == 1 else handle)  # 1: the runtime's name for the legacy stream
+    here = torch.cuda.current_stream()
+    if stream == here:
+        return call(**args)
+    if stream.device != here.device:
+        raise ValueError(f"gdr2: the stream is on {stream.device}, which is not the current CUDA device")
+    with torch.cuda.stream(stream):
+        out = call(**args)
+    for t in out.values() if isinstance(out, dict) else out if isinstance(out, tuple) else (out,):
         if t is not None:
-            t.record_stream(s)
+            t.record_stream(here)
+    return out
 
 
-def _raw_stream(stream, index):
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(index)
-    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+def _raw_stream(index):
+    return torch._C._cuda_getCurrentRawStream(index)
 
 
 _sizes = {}
 
 
-def _scratch(like, workspace, stream, name, *args):
+def _scratch(like, workspace, name, *args):
     """(workspace or None, its bytes): the one given, or a fresh one of the size that the query `name` gives for these
     arguments (it depends on them alone); None where the call needs none."""
     if workspace is not None:
@@ -615,10 +626,7 @@ def _scratch(like, workspace, stream, name, *args):
         n = _sizes[(name, args)] = int(getattr(lib(), name)(*args))
     if n == 0:
         return None, 0
-    workspace = like.new_empty(-(-n // like.element_size()))
-    if stream is not None:
-        _keep(stream, workspace)
-    return workspace, n
+    return like.new_empty(-(-n // like.element_size())), n
 
 
 def rope_freqs(rot, base=10000.0, *, scaling="none", factor=1.0, orig_len=0, turns_low=1.0, turns_high=32.0,
@@ -662,20 +670,20 @@ def attn_prologue_fwd(xq, xk, gq=None, gk=None, pos=None, freqs=None, *, norm=Tr
     """gdr2_attn_prologue_fwd: per-head RMS norm (unless norm=False) with gains gq, gk [d] fp32 (None: ones) and
     rotary positions of xq [.., T, Hq, d] and xk [.., T, Hk, d] (views of a fused projection allowed), pos int32 for
     each token and freqs float64 (rope_freqs; None: no rotation). Returns a dict q, k (contiguous)."""
+    if stream is not None:
+        return _on(stream, attn_prologue_fwd, locals())
     T, Hq, Hk, d, sq, sk, dt, rot = _prologue_checks(xq, xk, gq, gk, pos, freqs, norm)
     if out is None:
         index = _device(xq, xk, gq, gk, pos, freqs)
         q, k = torch.empty_like(xq), torch.empty_like(xk)  # contiguous, whatever the token stride of the inputs
         out = {"q": q, "k": k}
-        if stream is not None:
-            _keep(stream, q, k)
     else:
         q, k = _shaped("q", out["q"], xq.shape, xq.dtype), _shaped("k", out["k"], xk.shape, xq.dtype)
         index = _device(xq, xk, gq, gk, pos, freqs, q, k)
     _call(
         "gdr2_attn_prologue_fwd",
         xq.data_ptr(), xk.data_ptr(), _p(gq), _p(gk), 1 if norm else 0, eps, _p(pos), _p(freqs), mag, rot,
-        1 if interleaved else 0, q.data_ptr(), k.data_ptr(), T, Hq, Hk, d, dt, sq, sk, _raw_stream(stream, index))
+        1 if interleaved else 0, q.data_ptr(), k.data_ptr(), T, Hq, Hk, d, dt, sq, sk, _raw_stream(index))
     return out
 
 
@@ -684,6 +692,8 @@ def attn_prologue_bwd(xq, xk, gq, gk, pos, freqs, dq, dk, *, norm=True, eps=1e-6
     """gdr2_attn_prologue_bwd: returns a dict dxq, dxk and, with the norm, dgq, dgk [d] fp32 (written for gains of
     None too, as the gradient of a gain of ones). `out` may hold dxq, dxk as views of one fused gradient, and may
     leave dgq, dgk out or None when they are not wanted."""
+    if stream is not None:
+        return _on(stream, attn_prologue_bwd, locals())
     T, Hq, Hk, d, sq, sk, dt, rot = _prologue_checks(xq, xk, gq, gk, pos, freqs, norm)
     dtype = xq.dtype
     if not (dq.shape == xq.shape and dq.dtype is dtype and dq.is_contiguous() and dk.shape == xk.shape and
@@ -699,8 +709,6 @@ def attn_prologue_bwd(xq, xk, gq, gk, pos, freqs, dq, dk, *, norm=True, eps=1e-6
             dgq = xq.new_empty(d, dtype=_F32)
             dgk = torch.empty_like(dgq)
             out["dgq"], out["dgk"] = dgq, dgk
-        if stream is not None:
-            _keep(stream, dxq, dxk, dgq, dgk)
     else:
         dxq, dxk, dgq, dgk = out["dxq"], out["dxk"], out.get("dgq"), out.get("dgk")
         Tq, hq, eq, sdq = _token_rows("dxq", dxq, dtype)
@@ -713,12 +721,12 @@ def attn_prologue_bwd(xq, xk, gq, gk, pos, freqs, dq, dk, *, norm=True, eps=1e-6
         _device(xq, dxq, dxk, dgq, dgk)
     nbytes = 0
     if dgq is not None or dgk is not None:
-        workspace, nbytes = _scratch(xq, workspace, stream, "gdr2_attn_prologue_workspace_bytes", d)
+        workspace, nbytes = _scratch(xq, workspace, "gdr2_attn_prologue_workspace_bytes", d)
     _call(
         "gdr2_attn_prologue_bwd",
         xq.data_ptr(), xk.data_ptr(), _p(gq), _p(gk), 1 if norm else 0, eps, _p(pos), _p(freqs), mag, rot,
         1 if interleaved else 0, dq.data_ptr(), dk.data_ptr(), dxq.data_ptr(), dxk.data_ptr(), _p(dgq), _p(dgk), T, Hq,
-        Hk, d, dt, sq, sk, sdq, sdk, _p(workspace), nbytes, _raw_stream(stream, index))
+        Hk, d, dt, sq, sk, sdq, sdk, _p(workspace), nbytes, _raw_stream(index))
     return out
 
 
@@ -754,6 +762,8 @@ def attn_prologue_cache(xq, xk, xv, gq, gk, seq, pos, freqs, k_pages, v_pages, t
     pos[t] of sequence seq[t] (int32; outside [0, R): padding). Keys and values go to the pools k_pages, v_pages
     [num_pages, Hk, page_size, d] by table int32 [R, P]; q is returned (padding rows as they were; in a fresh q they hold
     no value)."""
+    if stream is not None:
+        return _on(stream, attn_prologue_cache, locals())
     T, Hq, Hk, d, sq, sk, dt, rot = _prologue_checks(xq, xk, gq, gk, pos, freqs, norm)
     Tv, Hv, dv, sv = _token_rows("xv", xv, xq.dtype)
     if pos is None:
@@ -773,8 +783,6 @@ def attn_prologue_cache(xq, xk, xv, gq, gk, seq, pos, freqs, k_pages, v_pages, t
     if q is None:
         _device(xq, xk, xv, gq, gk, pos, freqs)
         q = torch.empty_like(xq)
-        if stream is not None:
-            _keep(stream, q)
     else:
         _shaped("q", q, xq.shape, xq.dtype)
         _device(xq, xk, xv, gq, gk, pos, freqs, q)
@@ -782,7 +790,7 @@ def attn_prologue_cache(xq, xk, xv, gq, gk, seq, pos, freqs, k_pages, v_pages, t
         "gdr2_attn_prologue_cache",
         xq.data_ptr(), xk.data_ptr(), xv.data_ptr(), _p(gq), _p(gk), 1 if norm else 0, eps, seq.data_ptr(),
         pos.data_ptr(), _p(freqs), mag, rot, 1 if interleaved else 0, q.data_ptr(), k_pages.data_ptr(),
-        v_pages.data_ptr(), table.data_ptr(), T, Hq, Hk, d, R, P, ps, num, dt, sq, sk, sv, _raw_stream(stream, index))
+        v_pages.data_ptr(), table.data_ptr(), T, Hq, Hk, d, R, P, ps, num, dt, sq, sk, sv, _raw_stream(index))
     return q
 
 
@@ -792,6 +800,8 @@ def attn_decode(q, k_pages, v_pages, table, lens, seq=None, *, scale=None, windo
     None: n) of the cache, its last `window` tokens (0: all), lens int32 [R] with the new token counted. scale: by
     default d^-1/2. Returns o [N, Hq, d], or (o, lse fp32 [N, Hq]) with want_lse or a given lse (slots whose seq is outside
     [0, R) keep their rows; in fresh outputs those hold no value)."""
+    if stream is not None:
+        return _on(stream, attn_decode, locals())
     dtype, dt = q.dtype, _dtype_code(q)
     qshape, shape, tshape, index = q.shape, k_pages.shape, table.shape, q.get_device()
     if len(qshape) != 3 or not q.is_contiguous():
@@ -810,22 +820,18 @@ def attn_decode(q, k_pages, v_pages, table, lens, seq=None, *, scale=None, windo
     _device(q, o, lse)
     if o is None:
         o = torch.empty_like(q)
-        if stream is not None:
-            _keep(stream, o)
     else:
         _shaped("o", o, qshape, dtype)
     if lse is not None:
         _shaped("lse", lse, (N, Hq), _F32)
     elif want_lse:
         lse = q.new_empty(N, Hq, dtype=_F32)
-        if stream is not None:
-            _keep(stream, lse)
-    workspace, nbytes = _scratch(q, workspace, stream, "gdr2_attn_decode_workspace_bytes", N, Hq, Hk, d, P, ps, window, dt)
+    workspace, nbytes = _scratch(q, workspace, "gdr2_attn_decode_workspace_bytes", N, Hq, Hk, d, P, ps, window, dt)
     _call(
         "gdr2_attn_decode",
         q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), table.data_ptr(), lens.data_ptr(), _p(seq),
         d ** -0.5 if scale is None else scale, window, o.data_ptr(), _p(lse), N, Hq, Hk, d, R, P, ps, num, dt,
-        _p(workspace), nbytes, _raw_stream(stream, index))
+        _p(workspace), nbytes, _raw_stream(index))
     return o if lse is None else (o, lse)
 
 
@@ -842,6 +848,8 @@ def _given(out, name, like, shape):
 def kv_reserve(table, lens, want, ref, *, page_size, window=0, out=None, workspace=None, stream=None):
     """gdr2_kv_reserve: pages for tokens [lens[r], want[r]) of every sequence (pages behind the window released
     first). Returns (table, ref, missing int32 [1]) after the call; `out` may name them (also the inputs)."""
+    if stream is not None:
+        return _on(stream, kv_reserve, locals())
     shape, rows, index, num = table.shape, table.shape[:1], table.get_device(), ref.numel()
     if not (len(shape) == 2 and lens.shape == rows and want.shape == rows and ref.dim() == 1 and
             _fine(index, _I32, table, lens, want, ref)):
@@ -856,19 +864,19 @@ def kv_reserve(table, lens, want, ref, *, page_size, window=0, out=None, workspa
     t = torch.empty_like(table) if t is None else t
     r = torch.empty_like(ref) if r is None else r
     m = ref.new_empty(1) if m is None else m
-    if stream is not None:
-        _keep(stream, t, r, m)
-    workspace, nbytes = _scratch(ref, workspace, stream, "gdr2_kv_workspace_bytes", R, P, num)
+    workspace, nbytes = _scratch(ref, workspace, "gdr2_kv_workspace_bytes", R, P, num)
     _call(
         "gdr2_kv_reserve",
         table.data_ptr(), lens.data_ptr(), want.data_ptr(), ref.data_ptr(), t.data_ptr(), r.data_ptr(), m.data_ptr(),
-        R, P, page_size, num, window, _p(workspace), nbytes, _raw_stream(stream, index))
+        R, P, page_size, num, window, _p(workspace), nbytes, _raw_stream(index))
     return t, r, m
 
 
 def kv_fork(table, lens, ref, parent, k_pages, v_pages, *, out=None, workspace=None, stream=None):
     """gdr2_kv_fork: sequence r takes over the content of sequence parent[r] (int32 [R]; r: stays, outside [0, R):
     released). Partly filled last pages are copied in the pools. Returns (table, lens, ref, missing int32 [1])."""
+    if stream is not None:
+        return _on(stream, kv_fork, locals())
     shape, rows, pool, index, dt = table.shape, table.shape[:1], k_pages.shape, table.get_device(), _dtype_code(k_pages)
     if not (len(shape) == 2 and len(pool) == 4 and v_pages.shape == pool and lens.shape == rows and
             parent.shape == rows and ref.shape == pool[:1] and _fine(index, _I32, table, lens, parent, ref) and
@@ -886,19 +894,19 @@ def kv_fork(table, lens, ref, parent, k_pages, v_pages, *, out=None, workspace=N
     n = torch.empty_like(lens) if n is None else n
     r = torch.empty_like(ref) if r is None else r
     m = ref.new_empty(1) if m is None else m
-    if stream is not None:
-        _keep(stream, t, n, r, m)
-    workspace, nbytes = _scratch(ref, workspace, stream, "gdr2_kv_workspace_bytes", R, P, num)
+    workspace, nbytes = _scratch(ref, workspace, "gdr2_kv_workspace_bytes", R, P, num)
     _call(
         "gdr2_kv_fork",
         table.data_ptr(), lens.data_ptr(), ref.data_ptr(), parent.data_ptr(), t.data_ptr(), n.data_ptr(), r.data_ptr(),
         m.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), R, P, Hk, ps, d, num, dt, _p(workspace), nbytes,
-        _raw_stream(stream, index))
+        _raw_stream(index))
     return t, n, r, m
 
 
 def kv_compact(table, ref, k_pages, v_pages, *, out=None, workspace=None, stream=None):
     """gdr2_kv_compact: the live pages moved to [0, live). Returns (table, ref, live int32 [1])."""
+    if stream is not None:
+        return _on(stream, kv_compact, locals())
     shape, pool, index, dt = table.shape, k_pages.shape, table.get_device(), _dtype_code(k_pages)
     if not (len(shape) == 2 and len(pool) == 4 and v_pages.shape == pool and ref.shape == pool[:1] and
             _fine(index, _I32, table, ref) and _fine(index, k_pages.dtype, k_pages, v_pages)):
@@ -913,13 +921,11 @@ def kv_compact(table, ref, k_pages, v_pages, *, out=None, workspace=None, stream
     t = torch.empty_like(table) if t is None else t
     r = torch.empty_like(ref) if r is None else r
     m = ref.new_empty(1) if m is None else m
-    if stream is not None:
-        _keep(stream, t, r, m)
-    workspace, nbytes = _scratch(ref, workspace, stream, "gdr2_kv_workspace_bytes", R, P, num)
+    workspace, nbytes = _scratch(ref, workspace, "gdr2_kv_workspace_bytes", R, P, num)
     _call(
         "gdr2_kv_compact",
         table.data_ptr(), ref.data_ptr(), t.data_ptr(), r.data_ptr(), m.data_ptr(), k_pages.data_ptr(),
-        v_pages.data_ptr(), R, P, Hk, ps, d, num, dt, _p(workspace), nbytes, _raw_stream(stream, index))
+        v_pages.data_ptr(), R, P, Hk, ps, d, num, dt, _p(workspace), nbytes, _raw_stream(index))
     return t, r, m
 
 

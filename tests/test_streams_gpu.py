@@ -1,0 +1,125 @@
+"""Calls on an explicit stream: what they allocate must not be memory that work still queued on the caller's current
+stream writes."""
+from __future__ import annotations
+
+import pytest
+import torch
+
+from gated_delta_rule_65_b200 import gdr2
+
+pytestmark = pytest.mark.gpu
+
+
+def ints(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def randn(*shape):
+    return torch.randn(*shape, device="cuda").bfloat16()
+
+
+def attention_calls():
+    """name -> (call(stream), tensors that it changes in place)"""
+    torch.manual_seed(1)
+    T, Hq, Hk, d, ps, R, P = 600, 8, 2, 64, 16, 3, 200
+    num = R * P
+    x, dy = randn(T, Hq + 2 * Hk, d), randn(T, Hq + Hk, d)
+    q, k, v = x[:, :Hq], x[:, Hq:Hq + Hk], x[:, Hq + Hk:]
+    dq, dk = dy[:, :Hq].contiguous(), dy[:, Hq:].contiguous()
+    gain = torch.rand(d, device="cuda")
+    pos, seq = torch.arange(T, device="cuda").int(), torch.zeros(T, dtype=torch.int32, device="cuda")
+    freqs, _ = gdr2.rope_freqs(d)
+    pools = randn(num, Hk, ps, d), randn(num, Hk, ps, d)
+    table = torch.randperm(num, device="cuda").view(R, P).int()
+    lens, want, ref = ints([3100, 20, 901]), ints([3190, 60, 1000]), ints([1] * num)
+    parent = ints([2, 1, 2])
+    half, fewer = table.clone(), ref.clone()
+    half[:, 100:] = -1
+    fewer[table[:, 100:].flatten().long()] = 0
+    a = (q, k, gain, gain, pos, freqs)
+    return {
+        "fwd": (lambda s: gdr2.attn_prologue_fwd(*a, stream=s), ()),
+        "bwd": (lambda s: gdr2.attn_prologue_bwd(*a, dq, dk, stream=s), ()),
+        "cache": (lambda s: gdr2.attn_prologue_cache(q, k, v, gain, gain, seq, pos, freqs, *pools, table, stream=s), pools),
+        "decode": (lambda s: gdr2.attn_decode(dq[:R], *pools, table, lens, want_lse=True, stream=s), ()),
+        "reserve": (lambda s: gdr2.kv_reserve(half, lens, want, fewer, page_size=ps, stream=s), ()),
+        "fork": (lambda s: gdr2.kv_fork(half, lens, fewer, parent, *pools, stream=s), pools),
+        "compact": (lambda s: gdr2.kv_compact(half, fewer, *pools, stream=s), pools),
+    }
+
+
+def results(out):
+    return [t for t in (out.values() if isinstance(out, dict) else out if isinstance(out, tuple) else (out,)) if t is not None]
+
+
+def fresh_on_a_busy_stream(call, changed):
+    """The caller's stream has 20 ms or more of copies queued, then writes to blocks of every size, which are let go on
+    the host at once: a call on another stream, which has nothing to wait for, must not be given any of them."""
+    before = [t.clone() for t in changed]
+    want = [t.clone() for t in results(call(None))]
+    after = [t.clone() for t in changed]
+    for t, b in zip(changed, before):
+        t.copy_(b)
+    big = torch.empty(2, 1 << 29, dtype=torch.uint8, device="cuda")
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for how in (side, side.cuda_stream):
+        for _ in range(100):
+            big[0].copy_(big[1])
+        for n in range(2, 27):
+            for _ in range(6):
+                torch.full((1 << n,), 0xff, dtype=torch.uint8, device="cuda")
+        got = call(how)
+        with torch.cuda.stream(side):
+            changes = [t.clone() for t in changed]
+            for t, b in zip(changed, before):
+                t.copy_(b)
+        torch.cuda.synchronize()
+        for x, y in zip(results(got), want, strict=True):
+            assert torch.equal(x, y)
+        for x, y in zip(changes, after):
+            assert torch.equal(x, y)
+        del got
+
+
+@pytest.mark.parametrize("name", ["fwd", "bwd", "cache", "decode", "reserve", "fork", "compact"])
+def test_attention_half(name):
+    fresh_on_a_busy_stream(*attention_calls()[name])
+
+
+def test_current_and_default_streams_by_handle():
+    """A handle of the current stream, 0 and 1 (the legacy stream's two names) are streams as any other."""
+    call, _ = attention_calls()["decode"]
+    want = results(call(None))
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        got = [call(s) for s in (side, side.cuda_stream, 0, 1)]
+    torch.cuda.synchronize()
+    got += [call(s) for s in (torch.cuda.current_stream(), 0, 1, side.cuda_stream)]
+    torch.cuda.synchronize()
+    for out in got:
+        for x, y in zip(results(out), want, strict=True):
+            assert torch.equal(x, y)
+
+
+def test_results_outlive_their_use_on_the_callers_stream():
+    """A result that the caller's stream still reads when the host lets it go is not handed to the next call."""
+    call, _ = attention_calls()["decode"]
+    want = results(call(None))
+    big = torch.empty(2, 1 << 29, dtype=torch.uint8, device="cuda")
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    out = call(side)
+    torch.cuda.current_stream().wait_stream(side)
+    for _ in range(100):
+        big[0].copy_(big[1])
+    copies = [t.clone() for t in results(out)]
+    shapes = [(t.shape, t.dtype) for t in results(out)]
+    del out
+    with torch.cuda.stream(side):
+        for shape, dtype in shapes * 4:
+            torch.empty(shape, dtype=dtype, device="cuda").fill_(7)
+    torch.cuda.synchronize()
+    for x, y in zip(copies, want, strict=True):
+        assert torch.equal(x, y)
