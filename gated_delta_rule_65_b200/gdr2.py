@@ -188,6 +188,28 @@ def _stream(stream):
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 
+def _on(stream, call, args):
+    """call(**args) with `stream`, given explicitly, as the current one, so that the outputs and the workspace that the
+    call makes come from that stream's memory. (Out of the memory of the caller's current stream they could be what work
+    still queued there writes, which `stream` does not wait for.) The results are kept for the caller's stream too, which
+    may use them once it has waited."""
+    del args["stream"]
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+        stream = torch.cuda.ExternalStream(0 if handle == 1 else handle)  # 1: the runtime's name for the legacy stream
+    here = torch.cuda.current_stream()
+    if stream == here:
+        return call(**args)
+    if stream.device != here.device:
+        raise ValueError(f"gdr2: the stream is on {stream.device}, which is not the current CUDA device")
+    with torch.cuda.stream(stream):
+        out = call(**args)
+    for t in out.values() if isinstance(out, dict) else out if isinstance(out, tuple) else (out,):
+        if t is not None:
+            t.record_stream(here)
+    return out
+
+
 def _check(fn, st):
     if st != OK:
         raise GDR2Error(fn, st)
@@ -218,6 +240,8 @@ def chunk_fwd(q, k, v, log_alpha, b, w, initial_state=None, *, output_final_stat
               o=None, final_state=None, workspace=None, stream=None, train=False):
     """gdr2_chunk_fwd, or gdr2_chunk_fwd_train when train=True (then `workspace` must be the
     backward-sized buffer that gdr2_chunk_bwd_saved will read). Returns (o, final_state or None)."""
+    if stream is not None:
+        return _on(stream, chunk_fwd, locals())
     B, T, H, dk = q.shape
     dv = v.shape[-1]
     dt = _dtype_code(q)
@@ -244,6 +268,8 @@ def chunk_fwd_noalloc(q, k, v, log_alpha, b, w, initial_state=None, *, output_fi
     """gdr2_chunk_fwd_noalloc: the forward with the library's fixed scratch instead of a workspace,
     for callers that cannot allocate device memory (the outputs here are still allocated by torch
     when not given). Returns (o, final_state or None)."""
+    if stream is not None:
+        return _on(stream, chunk_fwd_noalloc, locals())
     B, T, H, dk = q.shape
     dv = v.shape[-1]
     if o is None:
@@ -264,6 +290,8 @@ def chunk_bwd(q, k, v, log_alpha, b, w, initial_state=None, d_o=None, d_final_st
     """gdr2_chunk_bwd, or gdr2_chunk_bwd_saved when saved=True (then `workspace` is the buffer a
     chunk_fwd(..., train=True) call with the same inputs filled). Returns a dict dq, dk, dv,
     dlog_alpha, db, dw, dS0 (dS0 None if not wanted)."""
+    if stream is not None:
+        return _on(stream, chunk_bwd, locals())
     B, T, H, dk = q.shape
     dv = v.shape[-1]
     dt = _dtype_code(q)
@@ -300,6 +328,8 @@ def chunk_fwd_gva(q, k, v, log_alpha, b, w, initial_state=None, *, output_final_
                   final_state=None, workspace=None, stream=None, train=False):
     """gdr2_chunk_fwd_gva (or the _train variant): grouped value heads. q, k, log_alpha, b [B,T,H,dk];
     v, w [B,T,Hv,dv] with Hv a multiple of H; states [B,Hv,dk,dv]. Returns (o [B,T,Hv,dv], final_state)."""
+    if stream is not None:
+        return _on(stream, chunk_fwd_gva, locals())
     B, T, H, dk = q.shape
     Hv, dv = v.shape[2], v.shape[3]
     dt = _dtype_code(q)
@@ -325,6 +355,8 @@ def chunk_bwd_gva(q, k, v, log_alpha, b, w, initial_state=None, d_o=None, d_fina
                   want_d_initial_state=True, out=None, workspace=None, stream=None, saved=False):
     """gdr2_chunk_bwd_gva (or the _saved variant): returns a dict dq, dk, dlog_alpha, db [B,T,H,dk],
     dv, dw [B,T,Hv,dv], dS0 [B,Hv,dk,dv] (or None)."""
+    if stream is not None:
+        return _on(stream, chunk_bwd_gva, locals())
     B, T, H, dk = q.shape
     Hv, dv = v.shape[2], v.shape[3]
     dt = _dtype_code(q)
@@ -375,6 +407,8 @@ def chunk_fwd_varlen(q, k, v, log_alpha, b, w, cu_seqlens, initial_state=None, *
     """gdr2_chunk_fwd_varlen (or the _train variant): packed token tensors [T, H, d] (or [1, T, H, d]),
     cu_seqlens int32 [N + 1] on the device, states [N, Hv, dk, dv]. v and w with more heads than q (Hv =
     G H value heads) select gdr2_chunk_fwd_varlen_gva. Returns (o shaped like v, final_state)."""
+    if stream is not None:
+        return _on(stream, chunk_fwd_varlen, locals())
     N, T, H, dk = _packed_shape(q, cu_seqlens)
     dv, Hv = v.shape[-1], v.shape[-2]
     dt = _dtype_code(q)
@@ -406,6 +440,8 @@ def chunk_bwd_varlen(q, k, v, log_alpha, b, w, cu_seqlens, initial_state=None, d
     """gdr2_chunk_bwd_varlen (or the _saved variant after chunk_fwd_varlen(..., train=True) on the same
     workspace); v and w with more heads than q select the _gva entry points. Returns a dict dq, dk, dv,
     dlog_alpha, db, dw, dS0 ([N, Hv, dk, dv] or None)."""
+    if stream is not None:
+        return _on(stream, chunk_bwd_varlen, locals())
     N, T, H, dk = _packed_shape(q, cu_seqlens)
     dv, Hv = v.shape[-1], v.shape[-2]
     dt = _dtype_code(q)
@@ -436,6 +472,8 @@ def chunk_bwd_varlen(q, k, v, log_alpha, b, w, cu_seqlens, initial_state=None, d
 def gate_prologue_fwd(xq, xk, xf, xb, xw, a, delta, *, neg_eig=False, out=None, stream=None):
     """gdr2_gate_prologue_fwd: q, k (L2-normalised), log_alpha (fp32), b, w from the pre-activations
     [B,T,H,d] and a, delta [H,dk]. Returns a dict q, k, log_alpha, b, w."""
+    if stream is not None:
+        return _on(stream, gate_prologue_fwd, locals())
     B, T, H, dk = xq.shape
     dv = xw.shape[-1]
     if out is None:
@@ -453,6 +491,8 @@ def gate_prologue_fwd(xq, xk, xf, xb, xw, a, delta, *, neg_eig=False, out=None, 
 def gate_prologue_bwd(xq, xk, xf, xb, xw, a, delta, dq, dk, dlog_alpha, db, dw, *, neg_eig=False, out=None,
                       workspace=None, stream=None):
     """gdr2_gate_prologue_bwd: returns a dict dxq, dxk, dxf, dxb, dxw, da, ddelta."""
+    if stream is not None:
+        return _on(stream, gate_prologue_bwd, locals())
     B, T, H, dk_ = xq.shape
     dv = xw.shape[-1]
     dt = _dtype_code(xq)
@@ -476,6 +516,8 @@ def gate_prologue_bwd(xq, xk, xf, xb, xw, a, delta, dq, dk, dlog_alpha, db, dw, 
 
 def decode_step(q, k, v, log_alpha, b, w, state, o=None, *, stream=None):
     """gdr2_decode_step: updates `state` in place and returns o [B,H,dv]."""
+    if stream is not None:
+        return _on(stream, decode_step, locals())
     B, H, dk = q.shape
     dv = v.shape[-1]
     if o is None:
@@ -583,28 +625,6 @@ def _call(name, *args):
     st = (_lib or lib()).gdr2_attn_call(n, packed, record.size)
     if st != OK:
         raise GDR2Error(name, st)
-
-
-def _on(stream, call, args):
-    """call(**args) with `stream`, given explicitly, as the current one, so that the outputs and the workspace that the
-    call makes come from that stream's memory. (Out of the memory of the caller's current stream they could be what work
-    still queued there writes, which `stream` does not wait for.) The results are kept for the caller's stream too, which
-    may use them once it has waited."""
-    del args["stream"]
-    if not isinstance(stream, torch.cuda.Stream):
-        handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-        stream = torch.cuda.ExternalStream(0 if handle == 1 else handle)  # 1: the runtime's name for the legacy stream
-    here = torch.cuda.current_stream()
-    if stream == here:
-        return call(**args)
-    if stream.device != here.device:
-        raise ValueError(f"gdr2: the stream is on {stream.device}, which is not the current CUDA device")
-    with torch.cuda.stream(stream):
-        out = call(**args)
-    for t in out.values() if isinstance(out, dict) else out if isinstance(out, tuple) else (out,):
-        if t is not None:
-            t.record_stream(here)
-    return out
 
 
 def _raw_stream(index):

@@ -48,6 +48,37 @@ def attention_calls():
     }
 
 
+def mixer_calls():
+    torch.manual_seed(2)
+    B, T, H, d = 1, 256, 2, 128
+    lens = ints([0, 100, 256])
+
+    def inputs(H, Hv, T=T):
+        shape, wide = (B, T, H, d) if T else (B, H, d), (B, T, Hv, d) if T else (B, Hv, d)
+        q, k = (torch.nn.functional.normalize(torch.randn(*shape, device="cuda"), dim=-1).bfloat16() for _ in range(2))
+        gate = lambda s: torch.rand(*s, device="cuda").bfloat16()  # noqa: E731
+        return q, k, randn(*wide), -0.1 * torch.rand(*shape, device="cuda"), gate(shape), gate(wide)
+
+    x, y, one = inputs(H, H), inputs(H, 2 * H), inputs(H, H, 0)
+    f = tuple(t.float() for t in x)
+    S = torch.randn(B, H, d, d, device="cuda")
+    pre = tuple(randn(B, T, H, d) for _ in range(5)) + (torch.randn(H, d, device="cuda"), torch.randn(H, d, device="cuda"))
+    grads = (*(randn(B, T, H, d) for _ in range(2)), torch.randn(B, T, H, d, device="cuda"), *(randn(B, T, H, d) for _ in range(2)))
+    return {
+        "chunk_fwd": (lambda s: gdr2.chunk_fwd(*x, stream=s), ()),
+        "chunk_fwd f32": (lambda s: gdr2.chunk_fwd(*f, stream=s), ()),
+        "chunk_fwd_noalloc": (lambda s: gdr2.chunk_fwd_noalloc(*x, stream=s), ()),
+        "chunk_bwd": (lambda s: gdr2.chunk_bwd(*x, d_o=x[2], stream=s), ()),
+        "chunk_fwd_gva": (lambda s: gdr2.chunk_fwd_gva(*y, stream=s), ()),
+        "chunk_bwd_gva": (lambda s: gdr2.chunk_bwd_gva(*y, d_o=y[2], stream=s), ()),
+        "chunk_fwd_varlen": (lambda s: gdr2.chunk_fwd_varlen(*x, lens, stream=s), ()),
+        "chunk_bwd_varlen": (lambda s: gdr2.chunk_bwd_varlen(*x, lens, d_o=x[2], stream=s), ()),
+        "gate_prologue_fwd": (lambda s: gdr2.gate_prologue_fwd(*pre, stream=s), ()),
+        "gate_prologue_bwd": (lambda s: gdr2.gate_prologue_bwd(*pre, *grads, stream=s), ()),
+        "decode_step": (lambda s: gdr2.decode_step(*one, S, stream=s), (S,)),
+    }
+
+
 def results(out):
     return [t for t in (out.values() if isinstance(out, dict) else out if isinstance(out, tuple) else (out,)) if t is not None]
 
@@ -85,6 +116,13 @@ def fresh_on_a_busy_stream(call, changed):
 @pytest.mark.parametrize("name", ["fwd", "bwd", "cache", "decode", "reserve", "fork", "compact"])
 def test_attention_half(name):
     fresh_on_a_busy_stream(*attention_calls()[name])
+
+
+@pytest.mark.parametrize("name", ["chunk_fwd", "chunk_fwd f32", "chunk_fwd_noalloc", "chunk_bwd", "chunk_fwd_gva", "chunk_bwd_gva",
+                                  "chunk_fwd_varlen", "chunk_bwd_varlen", "gate_prologue_fwd", "gate_prologue_bwd",
+                                  "decode_step"])
+def test_mixer(name):
+    fresh_on_a_busy_stream(*mixer_calls()[name])
 
 
 def test_current_and_default_streams_by_handle():
