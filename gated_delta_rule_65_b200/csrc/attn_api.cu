@@ -172,7 +172,7 @@ size_t gdr2_attn_decode_workspace_bytes(int N, int Hq, int Hk, int d, int P, int
     gdr2::AttnDecodeArgs a{};
     a.N = N; a.Hq = Hq; a.Hk = Hk; a.d = d; a.P = P; a.page_size = page_size; a.num_pages = 1; a.window = window;
     a.dtype = dtype;
-    return check_decode(a, N) == GDR2_OK ? gdr2::attn_decode_workspace_bytes(a) : 0;
+    return check_decode(a, 1) == GDR2_OK ? gdr2::attn_decode_workspace_bytes(a) : 0;  // R: any, slots may share sequences
 }
 
 int gdr2_attn_decode(const void *q, const void *k_pages, const void *v_pages, const int *table, const int *lens,

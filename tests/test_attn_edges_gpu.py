@@ -1,10 +1,12 @@
-"""Calls of the attention half at the edges of what its header allows, on the GPU: lengths beyond the page table."""
+"""Calls of the attention half at the edges of what its header allows, on the GPU: lengths beyond the page table, more
+slots than sequences."""
 from __future__ import annotations
 
 import pytest
 import torch
 
 from gated_delta_rule_65_b200 import gdr2
+from tests import attn_ref as ref
 
 pytestmark = pytest.mark.gpu
 
@@ -88,3 +90,18 @@ def test_fork_takes_lengths_over_as_they_are(P):
     for e in (e for row in t.tolist() for e in row if e >= 0):
         counts[e] += 1
     assert r.tolist() == counts and torch.equal(k, k0) and torch.equal(v, v0)
+
+
+def test_decode_of_more_slots_than_a_table_of_their_own_allows():
+    """2,100 slots of one sequence with 2^20 table entries: N P is past the bound of a table, R P is not."""
+    N, P, n = 2100, 1 << 20, 700
+    torch.manual_seed(3)
+    k, v = torch.randn(2, n + 3, 2, 1, 64, device="cuda").bfloat16()
+    table = torch.full((1, P), -1, dtype=torch.int32, device="cuda")
+    table[0, :n] = torch.randperm(n + 3, device="cuda")[:n].int()
+    q, seq = torch.randn(N, 8, 64, device="cuda").bfloat16(), torch.zeros(N, dtype=torch.int32, device="cuda")
+    o, lse = gdr2.attn_decode(q, k, v, table, ints([n]), seq, want_lse=True)
+    for rows in ([0, 1, 1047], [1048, 2098, 2099]):
+        ro, rl, to, tl, _ = ref.attention(q[rows], k, v, table, ints([n]), seq[rows])
+        ref.check("o", o[rows], ro, to)
+        ref.check("lse", lse[rows], rl, tl)

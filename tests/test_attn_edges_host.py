@@ -1,0 +1,17 @@
+"""Host-side edges of the attention half (no GPU: nothing here launches a kernel)."""
+from __future__ import annotations
+
+from gated_delta_rule_65_b200 import gdr2
+
+
+def test_decode_workspace_of_more_slots_than_sequences():
+    """Slots may share sequences (seq), so that N P may pass the bound of a table, R P: the workspace, which depends on
+    neither R nor the pool, is still asked for."""
+    f = gdr2.lib().gdr2_attn_decode_workspace_bytes  # N, Hq, Hk, d, P, page_size, window, dtype
+    P = 1 << 20
+    few = f(3, 8, 2, 64, P, 16, 0, gdr2.GDR2_BF16)
+    assert few > 0
+    for n in (2047, 2048, 4096, 1 << 20):
+        assert f(n, 8, 2, 64, P, 16, 0, gdr2.GDR2_BF16) == few
+    assert f(1 << 28, 8, 2, 64, P, 16, 0, gdr2.GDR2_BF16) == 0  # N Hq past 32 bits: no such call
+    assert f(3, 8, 2, 64, P, 2048, 0, gdr2.GDR2_BF16) == 0      # P page_size past 32 bits
