@@ -86,9 +86,13 @@ int status_take_kv_pages();
 
 // The launch of every kernel here: its blocks may become resident while the kernel before it on the stream still runs.
 // So each kernel begins with follow(), which lets the next one do the same and waits until everything before it on
-// the stream has finished and can be read; nothing of global memory is touched before. (Two launches of a pair are
-// 1.3 us apart this way, measured on an empty second kernel.) Shared memory above 48 KB is allowed to the kernel on its
-// first launch on a device; a launch refused later (the device was reset since) allows it again.
+// the stream has finished and can be read; nothing of global memory is touched before. What a kernel before may have
+// written (tables, lengths, workspaces) is read by ordinary loads, which that wait orders, not by __ldg, which asks that
+// nobody writes the data while the kernel is resident. (Two launches of a pair are 1.3 us apart this way, measured on an
+// empty second kernel. __ldcg for the table costs an attention of one short sequence 0.2 us of 6.8 and 16 packed
+// prompts 0.8 of 47.3: a page's tokens look their entry up one by one, and find it in L1.) Shared memory above 48 KB is
+// allowed to the kernel on its first launch on a device; a launch refused later (the device was reset since) allows it
+// again.
 template <typename... P, typename... A>
 cudaError_t launch(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, int cluster, cudaStream_t st, A... args) {
     cudaLaunchConfig_t cfg{};

@@ -714,7 +714,7 @@ __global__ void __launch_bounds__(kThreads, M::kPerSm) attn_decode_kernel(AttnDe
         const int tok = ahead.first + warp * M::kTok + lane;
         if (xa < end && lane < M::kTok && tok < ahead.len) {
             const uint32_t j = ln.by_page.divide(tok);
-            page = __ldg(ahead.pages + j);
+            page = ahead.pages[j];
             off = tok - (int)j * p.page_size;
         }
     };

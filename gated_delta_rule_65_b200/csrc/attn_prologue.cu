@@ -248,7 +248,7 @@ __global__ void __launch_bounds__(kThreads, kFwdCtas) attn_prologue_fwd_kernel(A
     auto find_page = [&](int q, int s) {
         if (s < 0 || s >= p.R || q < 0) return -1;
         const int j = (int)p.by_page.divide(q);
-        return j < p.P ? __ldg(p.table + (size_t)s * p.P + j) : -1;
+        return j < p.P ? p.table[(size_t)s * p.P + j] : -1;
     };
     if (p.rot || kCache) {
         pos = p.pos[token(u)];
@@ -491,7 +491,7 @@ __global__ void __launch_bounds__(kThreads, kBwdCtas) attn_prologue_bwd_kernel(A
 
 // dg[c] = the partial sums of its CTAs: slice s adds the CTAs s, s + 32, ... in order, then the slices in order.
 template <int D>
-__global__ void __launch_bounds__(1024) attn_prologue_reduce_kernel(const float *__restrict__ partial, int cq, int ctas,
+__global__ void __launch_bounds__(1024) attn_prologue_reduce_kernel(const float *partial, int cq, int ctas,
                                                                     float *dgq, float *dgk) {
     __shared__ float red[32][33];
     const int which = blockIdx.x, c = blockIdx.y * 32 + threadIdx.x % 32, sl = threadIdx.x / 32;

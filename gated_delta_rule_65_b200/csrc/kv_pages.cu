@@ -244,8 +244,8 @@ __global__ void __launch_bounds__(kThreads) kv_reserve_kernel(KvPagesArgs a, Lis
             const bool in = i < es.last;
             tok[x] = at.j * ps;
             e[x] = in ? __ldcg(a.table + i) : 0;
-            len[x] = in ? __ldg(a.lens + at.r) : 0;
-            want[x] = in ? __ldg(a.want + at.r) : 0;
+            len[x] = in ? a.lens[at.r] : 0;
+            want[x] = in ? a.want[at.r] : 0;
             at.next(a.P);
         }
         int words = 0;
@@ -345,7 +345,7 @@ __global__ void __launch_bounds__(kThreads) kv_fork_kernel(KvPagesArgs a, Lists 
             if (b + 32 * x + t.lane < pg.last) a.ref_out[b + 32 * x + t.lane] = n[x];
     }
     cl.sync();
-    auto length = [&](int p) { return (int)min((long long)max(__ldg(a.lens + p), 0), (long long)a.P * ps); };
+    auto length = [&](int p) { return (int)min((long long)max(a.lens[p], 0), (long long)a.P * ps); };
     auto owns = [&](int r, int p) { return (here ? owner_here[p] : __ldcg(w.owner + p)) == (r == p ? -1 : r); };
     constexpr int kFew = 4;
     Cell at(es.first + t.lane, a.P);
@@ -357,7 +357,7 @@ __global__ void __launch_bounds__(kThreads) kv_fork_kernel(KvPagesArgs a, Lists 
             const int i = b + 32 * x + t.lane;
             r[x] = at.r, j[x] = at.j;
             at.next(a.P);
-            p[x] = i < es.last ? __ldg(a.parent + r[x]) : -1;
+            p[x] = i < es.last ? a.parent[r[x]] : -1;
             was[x] = i < es.last ? __ldcg(a.table + i) : -1;
             if (p[x] >= a.R) p[x] = -1;
         }
@@ -378,7 +378,7 @@ __global__ void __launch_bounds__(kThreads) kv_fork_kernel(KvPagesArgs a, Lists 
                     if (e >= 0) atomicAdd(a.ref_out + e, 1);
                 }
                 a.table_out[i] = e;
-                if (j[x] == 0) a.lens_out[r[x]] = p[x] >= 0 ? __ldcg(a.lens + p[x]) : 0;  // as it is, inside the table or not
+                if (j[x] == 0) a.lens_out[r[x]] = p[x] >= 0 ? a.lens[p[x]] : 0;  // as it is, inside the table or not
             }
         }
     }

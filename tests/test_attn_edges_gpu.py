@@ -105,3 +105,53 @@ def test_decode_of_more_slots_than_a_table_of_their_own_allows():
         ro, rl, to, tl, _ = ref.attention(q[rows], k, v, table, ints([n]), seq[rows])
         ref.check("o", o[rows], ro, to)
         ref.check("lse", lse[rows], rl, tl)
+
+
+def serving_inputs():
+    g = torch.Generator(device="cuda")
+    g.manual_seed(4)
+    R, Hk, d = 24, 2, 64
+    x = torch.randn(40, R, 4 + 2 * Hk, d, generator=g, device="cuda").bfloat16()
+    return x, torch.randint(0, R, (40, R), generator=g, device="cuda").int(), gdr2.rope_freqs(d)[0]
+
+
+def serve(x, parents, freqs, chained):
+    """Steps of a small server whose table, counts and pools change in place; `chained`, or the GPU waited for after each
+    call. Every launch overlaps the end of the one before, which has just written what it reads."""
+    R, P, ps, Hk, d, num = 24, 40, 8, 2, 64, 400
+    pools = [torch.zeros(num, Hk, ps, d, device="cuda").bfloat16() for _ in range(2)]
+    table, refs = torch.full((R, P), -1, dtype=torch.int32, device="cuda"), torch.zeros(num, dtype=torch.int32, device="cuda")
+    seq, lens = torch.arange(R, device="cuda").int(), torch.arange(R, device="cuda").int()
+    wait = (lambda: None) if chained else torch.cuda.synchronize
+    wait()
+    out = []
+    for i in range(40):
+        want = lens + 1
+        wait()
+        table, refs, _ = gdr2.kv_reserve(table, lens, want, refs, page_size=ps, window=100, out={"table": table, "ref": refs})
+        wait()
+        q = gdr2.attn_prologue_cache(x[i, :, :4], x[i, :, 4:4 + Hk], x[i, :, 4 + Hk:], None, None, seq, lens, freqs, *pools, table)
+        wait()
+        out.append(gdr2.attn_decode(q, *pools, table, want, window=100))
+        wait()
+        table, lens, refs, _ = gdr2.kv_fork(table, want, refs, parents[i], *pools)
+        wait()
+        table, refs, _ = gdr2.kv_compact(table, refs, *pools, out={"table": table, "ref": refs})
+        wait()
+        out.append(gdr2.attn_decode(q, *pools, table, lens, window=100))
+        wait()
+    return out + [table, lens, refs, *pools]
+
+
+def test_calls_in_a_chain_see_what_the_call_before_wrote():
+    x = serving_inputs()
+    want = [t.clone() for t in serve(*x, False)]
+    for _ in range(3):
+        assert all(torch.equal(a, b) for a, b in zip(serve(*x, True), want, strict=True))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = serve(*x, True)
+    for _ in range(3):
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want, strict=True))

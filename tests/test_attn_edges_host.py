@@ -1,7 +1,10 @@
 """Host-side edges of the attention half (no GPU: nothing here launches a kernel)."""
 from __future__ import annotations
 
-from gated_delta_rule_65_b200 import gdr2
+import os
+import re
+
+from gated_delta_rule_65_b200 import build, gdr2
 
 
 def test_decode_workspace_of_more_slots_than_sequences():
@@ -15,3 +18,14 @@ def test_decode_workspace_of_more_slots_than_sequences():
         assert f(n, 8, 2, 64, P, 16, 0, gdr2.GDR2_BF16) == few
     assert f(1 << 28, 8, 2, 64, P, 16, 0, gdr2.GDR2_BF16) == 0  # N Hq past 32 bits: no such call
     assert f(3, 8, 2, 64, P, 2048, 0, gdr2.GDR2_BF16) == 0      # P page_size past 32 bits
+
+
+def test_no_non_coherent_loads_where_launches_overlap():
+    """The kernels of the attention half become resident while their predecessors still write what they will read; a
+    non-coherent load asks that nobody does."""
+    names = [p for p in build.sources() if os.path.basename(p).startswith(("attn_", "kv_"))]
+    assert len(names) == 4
+    for path in names + [os.path.join(build.CSRC, n) for n in ("attn.h", "attn_vec.cuh")]:
+        with open(path) as f:
+            code = re.sub(r"//[^\n]*", "", f.read())
+        assert not re.search(r"__ldg\b|ld\.global\.nc|\bconst\b[^;,()]*\*\s*__restrict__", code), path
