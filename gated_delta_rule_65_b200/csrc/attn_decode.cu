@@ -270,18 +270,18 @@ template <int D, bool kPacked> struct Bf16Math {
     }
 };
 
-// The products of one warp's tile, fp32: GB query heads against kTok tokens (4 KB of K), on pairs of floats. Scores: four
-// lanes of a token take 16-byte chunks t, t + 4, ... of its row, each lane one token of every eight, and the exchange
-// that adds their parts leaves lane t with heads t, t + 4, ... Output: a lane owns four channels (d = 64: of every other
+// The products of one warp's tile, fp32: GB <= 4 query heads against kTok tokens (4 KB of K), on pairs of floats. Scores:
+// four lanes of a token take 16-byte chunks t, t + 4, ... of its row, each lane one token of every eight, and the exchange
+// that adds their parts leaves lane t with head t. Output: a lane owns four channels (d = 64: of every other
 // token).
 template <int D, int GB> struct F32Math {
     using T = float;
-    static constexpr int kTok = 1024 / D, kRows = GB, kRowBytes = 4 * D, kPer = kTok / 8, kPerSm = GB <= 4 ? 3 : 2;
+    static constexpr int kTok = 1024 / D, kRows = GB, kRowBytes = 4 * D, kPer = kTok / 8, kPerSm = 3;
     static constexpr int kCols = D / 2;  // columns merged at a time: all of them leave no room for a third CTA
-    static constexpr int kHeads = (GB + 3) / 4;  // heads whose statistics a lane keeps
-    static constexpr int kLanes = D / 4;         // lanes of an output row
+    static constexpr int kLanes = D / 4;   // lanes of an output row
+    static_assert(GB <= 4, "a lane keeps the statistics of one head");
     F2 o[GB][2];
-    float m[kHeads], ms[kHeads], l[kHeads];
+    float m, ms, l;
     // rows 2 i and 2 i + 1 share a quarter-warp's access to four neighbouring chunks: bit 2 keeps them apart
     static __device__ __forceinline__ int swizzle(int row) { return ((row & 1) << 2) | ((row >> 1) & 3); }
     static __device__ __forceinline__ void load(const void *p, F2 (&x)[2]) {
@@ -293,8 +293,7 @@ template <int D, int GB> struct F32Math {
         for (int x = threadIdx.x; x < GB * D; x += kThreads) sq[x] = x / D < heads && scale != 0.f ? sign * q[x] : 0.f;
 #pragma unroll
         for (int h = 0; h < GB; ++h) o[h][0] = o[h][1] = f2(0.f, 0.f);
-#pragma unroll
-        for (int i = 0; i < kHeads; ++i) m[i] = -INFINITY, ms[i] = 0.f, l[i] = 0.f;
+        m = -INFINITY, ms = 0.f, l = 0.f;
         __syncthreads();
     }
     // Sums over the four lanes of a token of four heads' parts; lane t gets head t's.
@@ -327,50 +326,44 @@ template <int D, int GB> struct F32Math {
                     s[y][h] = fma(qq[1], kk[y][1], i ? fma(qq[0], kk[y][0], s[y][h]) : mul(qq[0], kk[y][0]));
             }
         }
-        bool moved = false;
+        float x[kPer], mx = m;
 #pragma unroll
-        for (int i = 0; i < kHeads; ++i) {
-            float x[kPer];
-            float mx = m[i];
+        for (int y = 0; y < kPer; ++y) {
+            float a[4];
 #pragma unroll
-            for (int y = 0; y < kPer; ++y) {
-                float a[4];
-#pragma unroll
-                for (int c = 0; c < 4; ++c) a[c] = 4 * i + c < GB ? sum2(s[y][4 * i + c < GB ? 4 * i + c : 0]) : 0.f;
-                x[y] = spread(a[0], a[1], a[2], a[3], t);
-                if (4 * i + t >= GB || !(on >> (8 * y + g) & 1)) x[y] = -INFINITY;
-                mx = fmaxf(mx, x[y]);
-            }
-#pragma unroll
-            for (int w = 4; w < 32; w <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
-            const float was = m[i] == -INFINITY ? -INFINITY : ms[i];
-            m[i] = mx;
-            ms[i] = mx == -INFINITY ? 0.f : mx * sc;
-            const float al = pow2(was - ms[i]);
-            moved |= 4 * i + t < GB && al != 1.f;
-            l[i] *= al;
-#pragma unroll
-            for (int y = 0; y < kPer; ++y) {
-                const float pr = pow2(fmaf(x[y], sc, -ms[i]));
-                l[i] += pr;
-                if (4 * i + t < GB) pp[(8 * y + g) * GB + 4 * i + t] = make_float2(pr, pr);
-            }
-            if (4 * i + t < GB && g == 0) pp[kTok * GB + 4 * i + t] = make_float2(al, al);
+            for (int c = 0; c < 4; ++c) a[c] = c < GB ? sum2(s[y][c < GB ? c : 0]) : 0.f;
+            x[y] = spread(a[0], a[1], a[2], a[3], t);
+            if (t >= GB || !(on >> (8 * y + g) & 1)) x[y] = -INFINITY;
+            mx = fmaxf(mx, x[y]);
         }
+#pragma unroll
+        for (int w = 4; w < 32; w <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
+        const float was = m == -INFINITY ? -INFINITY : ms;
+        m = mx;
+        ms = mx == -INFINITY ? 0.f : mx * sc;
+        const float al = pow2(was - ms);
+        l *= al;
+#pragma unroll
+        for (int y = 0; y < kPer; ++y) {
+            const float pr = pow2(fmaf(x[y], sc, -ms));
+            l += pr;
+            if (t < GB) pp[(8 * y + g) * GB + t] = make_float2(pr, pr);
+        }
+        if (t < GB && g == 0) pp[kTok * GB + t] = make_float2(al, al);
         __syncwarp();
-        if (__any_sync(0xffffffffu, moved)) {
+        if (__any_sync(0xffffffffu, t < GB && al != 1.f)) {
 #pragma unroll
             for (int h = 0; h < GB; ++h) {
-                F2 al;
-                al.v = *reinterpret_cast<const unsigned long long *>(pp + kTok * GB + h);
-                o[h][0] = mul(o[h][0], al), o[h][1] = mul(o[h][1], al);
+                F2 f;
+                f.v = *reinterpret_cast<const unsigned long long *>(pp + kTok * GB + h);
+                o[h][0] = mul(o[h][0], f), o[h][1] = mul(o[h][1], f);
             }
         }
         const int c = lane % kLanes, sub = lane / kLanes;
 #pragma unroll
         for (int i = 0; i < kTok; i += 32 / kLanes) {
             const int tok = i + sub;
-            F2 vv[2], pr[GB < 2 ? 2 : GB];
+            F2 vv[2], pr[GB];
             load(v + tok * kRowBytes + ((c ^ swizzle(tok & 7)) << 4), vv);
             if constexpr (GB == 1) {
                 pr[0].v = *reinterpret_cast<const unsigned long long *>(pp + tok);
@@ -389,13 +382,10 @@ template <int D, int GB> struct F32Math {
     }
     __device__ __forceinline__ void stats(float *wm, float *wl, int lane) {
         const int g = lane >> 2, t = lane & 3;
+        float x = l;
 #pragma unroll
-        for (int i = 0; i < kHeads; ++i) {
-            float x = l[i];
-#pragma unroll
-            for (int w = 4; w < 32; w <<= 1) x += __shfl_xor_sync(0xffffffffu, x, w);
-            if (g == 0 && 4 * i + t < GB) wm[4 * i + t] = m[i] == -INFINITY ? -INFINITY : ms[i], wl[4 * i + t] = x;
-        }
+        for (int w = 4; w < 32; w <<= 1) x += __shfl_xor_sync(0xffffffffu, x, w);
+        if (g == 0 && t < GB) wm[t] = m == -INFINITY ? -INFINITY : ms, wl[t] = x;
         if constexpr (D == 64) {
 #pragma unroll
             for (int h = 0; h < GB; ++h)
