@@ -7,6 +7,7 @@ calls raise; there is no fallback of any kind.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import struct
 import threading
@@ -631,7 +632,9 @@ def _raw_stream(index):
     return torch._C._cuda_getCurrentRawStream(index)
 
 
-_sizes = {}
+@functools.lru_cache(maxsize=1024)  # one entry for each batch size, table and window in use; a server's come back
+def _need(name, args):
+    return int(getattr(lib(), name)(*args))
 
 
 def _scratch(like, workspace, name, *args):
@@ -641,9 +644,7 @@ def _scratch(like, workspace, name, *args):
         if workspace.get_device() != like.get_device() or not workspace.is_contiguous():
             raise ValueError("gdr2: the workspace must be contiguous and on the tensors' device")
         return workspace, workspace.numel() * workspace.element_size()
-    n = _sizes.get((name, args))
-    if n is None:
-        n = _sizes[(name, args)] = int(getattr(lib(), name)(*args))
+    n = _need(name, args)
     if n == 0:
         return None, 0
     return like.new_empty(-(-n // like.element_size())), n

@@ -4,6 +4,8 @@ from __future__ import annotations
 import os
 import re
 
+import torch
+
 from gated_delta_rule_65_b200 import build, gdr2
 
 
@@ -29,3 +31,15 @@ def test_no_non_coherent_loads_where_launches_overlap():
         with open(path) as f:
             code = re.sub(r"//[^\n]*", "", f.read())
         assert not re.search(r"__ldg\b|ld\.global\.nc|\bconst\b[^;,()]*\*\s*__restrict__", code), path
+
+
+def test_workspace_sizes_are_kept_for_a_bounded_number_of_calls():
+    """A process whose batches and tables keep changing does not grow by an entry for each of them."""
+    like = torch.zeros(16)
+    held = [n for n, x in vars(gdr2).items() if isinstance(x, (dict, list, set))]
+    before = {n: len(getattr(gdr2, n)) for n in held}
+    for n in range(1, 5000):
+        ws, size = gdr2._scratch(like, None, "gdr2_kv_workspace_bytes", n, 3, 10)
+        assert size == gdr2.lib().gdr2_kv_workspace_bytes(n, 3, 10) and ws.numel() * 4 >= size
+    assert {n: len(getattr(gdr2, n)) for n in held} == before
+    assert gdr2._need.cache_info().currsize <= 1024
