@@ -155,3 +155,44 @@ def test_calls_in_a_chain_see_what_the_call_before_wrote():
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, want, strict=True))
+
+
+@pytest.mark.parametrize("B,steps", [(5, 1), (1, 1), (5, 3), (40, 2)])
+def test_prologue_of_a_batched_decode_step(B, steps):
+    """[B, 1, H, d] views of a fused projection [B, 1, W], or of the last of several steps [B, steps, W]: forward, the
+    cache form, and the gradients into a fused gradient of the same layout."""
+    Hq, Hk, d, ps = 6, 2, 64, 16
+    torch.manual_seed(6)
+    W = (Hq + 2 * Hk) * d
+    qkv = torch.randn(B, steps, W, device="cuda").bfloat16()[:, -1:]
+    cut = lambda t, a, b: t[..., a * d:b * d].unflatten(-1, (b - a, d))  # noqa: E731
+    xq, xk, xv = cut(qkv, 0, Hq), cut(qkv, Hq, Hq + Hk), cut(qkv, Hq + Hk, Hq + 2 * Hk)
+    assert xq.shape == (B, 1, Hq, d) and (B == 1 or not xq.is_contiguous())
+    gain, (freqs, mag) = 1 + 0.2 * torch.randn(d, device="cuda"), gdr2.rope_freqs(32)
+    pos = torch.randint(0, 4096, (B, 1), device="cuda").int()
+    out = gdr2.attn_prologue_fwd(xq, xk, gain, None, pos, freqs, mag=mag)
+    flat = lambda t: t.reshape(B, -1, d)  # noqa: E731
+    for n, x, g in (("q", xq, gain), ("k", xk, None)):
+        y, tol = ref.prologue(flat(x), g, pos.view(-1), freqs, mag=mag)
+        assert out[n].shape == x.shape and out[n].is_contiguous()
+        ref.check(n, flat(out[n]), y, tol)
+    dq, dk = torch.randn(B, 1, Hq, d, device="cuda").bfloat16(), torch.randn(B, 1, Hk, d, device="cuda").bfloat16()
+    want = gdr2.attn_prologue_bwd(xq, xk, gain, None, pos, freqs, dq, dk, mag=mag)
+    whole = torch.full((B, steps, W), 7.0, device="cuda").bfloat16()
+    grad = whole[:, -1:]
+    gdr2.attn_prologue_bwd(xq, xk, gain, None, pos, freqs, dq, dk, mag=mag,
+                           out={"dxq": cut(grad, 0, Hq), "dxk": cut(grad, Hq, Hq + Hk)})
+    for n, x, g, dy, at in (("dxq", xq, gain, dq, (0, Hq)), ("dxk", xk, None, dk, (Hq, Hq + Hk))):
+        dx, _, tol, _ = ref.prologue_grad(flat(x), g, flat(dy), pos.view(-1), freqs, mag=mag)
+        ref.check(n, flat(want[n]), dx, tol)
+        assert torch.equal(cut(grad, *at), want[n])
+    assert (whole[:, :-1] == 7).all() and (cut(grad, Hq + Hk, Hq + 2 * Hk) == 7).all()
+    # into a cache, a page for each sequence
+    k, v = torch.zeros(2, B, Hk, ps, d, device="cuda").bfloat16()
+    table, seq, at = torch.randperm(B, device="cuda").int().view(B, 1), torch.arange(B, device="cuda").int(), pos.view(-1) % ps
+    q = gdr2.attn_prologue_cache(xq, xk, xv, gain, None, seq, at, freqs, k, v, table, mag=mag)
+    near = gdr2.attn_prologue_fwd(xq, xk, gain, None, at, freqs, mag=mag)
+    page = table[:, 0].long()
+    assert q.shape == xq.shape and torch.equal(q, near["q"])
+    assert torch.equal(k[page, :, at.long()], flat(near["k"])) and torch.equal(v[page, :, at.long()], flat(xv))
+    assert int((k != 0).any(-1).sum()) == B * Hk and int((v != 0).any(-1).sum()) == B * Hk
