@@ -541,15 +541,25 @@ Blocks blocks(const KvPagesArgs &a) {
     return Blocks{(uint8_t *)a.k_pages, (uint8_t *)a.v_pages, a.Hk, a.page_size, a.d * (a.dtype == 1 ? 2 : 4)};
 }
 
-// Up to so many bytes of pages (the most that a call can move) the cluster copies them itself: eight SMs move them in
-// the time that another launch takes. 32 forks of up to 1 MB: 17.7 us a call with the copies inside and 19.8 with a
-// kernel for them (host-bound; 16.5 and 14.5 us on the device alone); a compaction of 512 pages (1.8 MB): 15.2 and
-// 17.6 (14.5 and 10.5); 256 forks of up to 33 MB: 26.6 and 19.7. (Calls with their
-// arguments one by one; by the record the 32 forks take 17.0 us and the compaction 14.7 with the copies inside.)
+// Whether the cluster copies the pages itself, which saves the host the second launch, 2.3 us a call, but has eight SMs
+// to copy with. By the bytes really moved, us of a call from Python and of the device alone, inside / by a kernel of
+// their own:
+//                           0.25 MB              1 MB                 2 MB                 4 MB
+//   fork, call              15.8 / 18.1          15.8 / 18.1          17.3 / 18.3          21.5 / 18.1
+//   fork, device            11.5 / 10.6          12.7 / 11.0          16.9 / 12.1          21.2 / 11.1
+//   compaction, call        13.6 / 15.8          13.7 / 15.8          13.8 / 16.1          16.1 / 15.8
+//   compaction, device       6.2 / 5.1            8.0 / 5.9           10.9 / 5.7           15.8 / 5.5
+// (32, 32, 256 and 32 forks; 64, 512, 512 and 64 pages.) So a call that the host makes copies inside up to 2 MB. The
+// border is on what a call can move at most, and that is about twice what it moves: a partly filled page is half full,
+// and of num_pages / 2 pages a compaction moves live (1 - live / num_pages), at most half of them, where the live ones
+// are spread evenly. A captured call, whose launches cost the host nothing, always leaves the copies to the other kernel.
 constexpr long long kOwnCopy = 4 << 20;
-bool own_copy(const Blocks &bl, long long most) {
+bool own_copy(const Blocks &bl, long long most, cudaStream_t st) {
     const long long page = 2LL * bl.Hk * bl.page_size * bl.row_bytes;  // below 2^43: copies_fit
-    return most <= kOwnCopy / page;
+    if (most > kOwnCopy / page) return false;
+    cudaStreamCaptureStatus s = cudaStreamCaptureStatusNone;
+    if (cudaStreamIsCapturing(st, &s) != cudaSuccess) (void)cudaGetLastError();  // the launch will say
+    return s == cudaStreamCaptureStatusNone;
 }
 
 // CTAs of a copy over the whole GPU: a warp for each 4 KB that may move, eight CTAs an SM at most.
@@ -579,7 +589,7 @@ cudaError_t launch_kv_reserve(const KvPagesArgs &a, cudaStream_t st) {
 cudaError_t launch_kv_fork(const KvPagesArgs &a, cudaStream_t st) {
     const Lists w = lists(a.workspace, a.R, a.P, a.num_pages);
     const Blocks bl = blocks(a);
-    const bool own = own_copy(bl, a.R);
+    const bool own = own_copy(bl, a.R, st);
     const int c = cluster_size(a, own);
     cudaError_t e;
     GDR2_LAUNCH("kv_fork", st, e = launch(kv_fork_kernel, dim3(c), dim3(kThreads), 0, c, st, a, w, bl, (int)own));
@@ -594,7 +604,7 @@ cudaError_t launch_kv_compact(const KvPagesArgs &a, cudaStream_t st) {
     const Lists w = lists(a.workspace, a.R, a.P, a.num_pages);
     const Blocks bl = blocks(a);
     const long long most = a.num_pages / 2;  // a live page above for each free one below
-    const bool own = own_copy(bl, most);
+    const bool own = own_copy(bl, most, st);
     const int c = cluster_size(a, own);
     cudaError_t e;
     GDR2_LAUNCH("kv_compact", st, e = launch(kv_compact_kernel, dim3(c), dim3(kThreads), 0, c, st, a, w, bl, (int)own));

@@ -196,3 +196,31 @@ def test_prologue_of_a_batched_decode_step(B, steps):
     assert q.shape == xq.shape and torch.equal(q, near["q"])
     assert torch.equal(k[page, :, at.long()], flat(near["k"])) and torch.equal(v[page, :, at.long()], flat(xv))
     assert int((k != 0).any(-1).sum()) == B * Hk and int((v != 0).any(-1).sum()) == B * Hk
+
+
+@pytest.mark.parametrize("Hk,ps", [(1, 8), (8, 64)])  # copies inside the cluster's kernel, and by one of their own
+def test_fork_and_compaction_captured_and_not(Hk, ps):
+    """A captured call copies its pages by another kernel than a small call that the host makes: the same bits."""
+    R, P, d, num = 12, 4, 64, 80
+    torch.manual_seed(8)
+    pools = torch.randn(2, num, Hk, ps, d, device="cuda").bfloat16()
+    table = torch.randperm(num, device="cuda")[:R * P].int().view(R, P)
+    refs = torch.zeros(num, dtype=torch.int32, device="cuda")
+    refs[table.flatten().long()] = 1
+    lens, parent = torch.randint(0, P * ps, (R,), device="cuda").int(), torch.randint(-1, R, (R,), device="cuda").int()
+
+    def both(k, v):
+        t, n, r, m = gdr2.kv_fork(table, lens, refs, parent, k, v)
+        return [t, n, r, m, *gdr2.kv_compact(t, r, k, v), k, v]
+
+    want = both(*pools.clone())
+    k, v = pools.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = both(k, v)
+    for _ in range(2):
+        k.copy_(pools[0]), v.copy_(pools[1])
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want, strict=True))
+    assert not torch.equal(k, pools[0])
