@@ -375,8 +375,14 @@ GDR2_API int gdr2_decode_step(const void *q, const void *k, const void *v, const
  * cache's bookkeeping. The conventions at the top of this file hold, except that arrays of ints, the gains gq
  * and gk, dgq, dgk and lse need the alignment of their own type only.
  *
- * Sizes: d in {64, 128}; any Hq, Hk >= 1 (attention: Hq a multiple of Hk, at most 1,024 times as
- * many; query head j reads KV head j / (Hq / Hk)); any page_size >= 1 with P * page_size below 2^31 - 65536.
+ * Sizes: d in {64, 128}; Hq, Hk from 1 to 65,535 (attention: Hq a multiple of Hk, at most 1,024 times as many; query
+ * head j reads KV head j / (Hq / Hk)); any page_size >= 1. Counted in 32 bits, and GDR2_ERR_UNSUPPORTED beyond:
+ *   P page_size (a sequence's tokens), R P (a table's entries), num_pages    at most 2^31 - 65,536 each
+ *   attention      N Hq and Hk page_size below 2^31, Hk page_size num_pages (token rows of a pool) below 2^32
+ *   kv_fork, kv_compact   with c = 2 Hk ceil(page_size d sizeof(dtype) / 4096), the pieces that a page is copied in:
+ *                  c below 2^31, c num_pages below 2^32 - 65,536
+ * Norms are formed in fp32: the sum of a row's squares has to stay below 2^128 (the row becomes 0 beyond) and, with
+ * eps = 0, above 2^-126.
  */
 
 /*
