@@ -11,14 +11,16 @@
 // instead, whose sixteen rows hold the query heads of a KV head; at 6.2 TB/s they are busy a fifth of the time. Up to 8
 // heads leave half the rows free: there the eight upper rows carry the low halves of p (p = hi + lo in bf16), so that
 // rounding p costs 2^-17 and no further instruction. 9 to 16 heads take a second product for lo.
-// fp32 caches run the same schedule on fp32 multiply-adds (tf32 products would lose 13 bits).
+// fp32 caches run the same schedule on fp32 multiply-adds (single tf32 products would lose 13 bits).
 //
 // Work split: the tiles (64 tokens; 32 for fp32 heads of 128) of all (sequence, KV head) rows lie on one line, and each
 // CTA takes an equal run of it, whatever the lengths: one long sequence spreads over the whole GPU, a ragged batch
 // leaves no CTA idle, and a row that lies in one CTA is finished there. More query heads of a KV head than one CTA holds
-// go to neighbouring CTAs with the same run, which find each other's tiles in L2. Rows cut by a border leave (m, l, o) in
-// the workspace, and a second kernel joins them in the order of the line: no atomics, the same bits every call. The
-// split depends on the lengths alone, which only the GPU reads (a captured graph stays valid as sequences grow).
+// go to neighbouring CTAs with the same run, which find each other's tiles in L2 (each block costs its own way of the
+// tiles into the SM: 400 MB take 70 us with 16 bf16 heads of 128 on a KV head and 98 with 32). Rows cut by a border
+// leave (m, l, o) in the workspace, and a second kernel joins them in the order of the line: no atomics, the same bits
+// every call. The split depends on the lengths alone, which only the GPU reads (a captured graph stays valid as
+// sequences grow).
 //
 // Inside a CTA each of 4 warps takes a quarter of every tile through its own ring of cp.async stages (16 KB) with its
 // own (m, l, o), so the main loop has no barrier; the warps' results meet at the end of a row. Two CTAs to an SM for
@@ -27,9 +29,9 @@
 // with its rows whole and 8.4 us cut and joined, but the second launch costs the host 3 us.
 //
 // Measured on one B200, back to back: 256 sequences of 100 to 4,096 tokens in a window of 2,048 (16 / 4 heads of 128,
-// bf16, pages of 16) in 133 us (829 MB, 6.2 TB/s, 95% of the measured copy); 3 sequences of 50,001 to 65,536 tokens (16 /
-// 2 heads) in 37 us (183 MB, 75%: about 7 us of it are the start, the end and the join); 33 ragged fp32 sequences of up
-// to 2,000 tokens (12 / 6 heads of 64) in 26 us (107 MB, 63%).
+// bf16, pages of 16) in 133 us (829 MB, 6.2 TB/s, 95% of the measured copy; 135 from call to call); 3 sequences of
+// 50,001 to 65,536 tokens (16 / 2 heads) in 37 us (183 MB, 75%: about 7 us of it are the start, the end and the join);
+// 33 ragged fp32 sequences of up to 2,000 tokens (12 / 6 heads of 64) in 26 us (107 MB, 63%).
 #include <math.h>
 
 #include "attn.h"
@@ -912,7 +914,8 @@ template <int D, typename F> auto dispatch(const AttnDecodeArgs &a, F f) {
     if (G == 1) return f.template operator()<D, F32Math<D, 1>>();
     if (G == 2) return f.template operator()<D, F32Math<D, 2>>();
     if (G <= 4) return f.template operator()<D, F32Math<D, 4>>();
-    return f.template operator()<D, F32Math<D, 8>>();  // 16 heads of 64 / 128, 400 MB: 140 / 143 us in blocks of 8, 133 / 158 at once
+    // 16 heads of 64 / 128, 400 MB: 141 / 142 us in blocks of 8, 133 / 158 at once: one form for both, at 6% for 64
+    return f.template operator()<D, F32Math<D, 8>>();  // more in blocks of 8
 }
 
 struct Run {

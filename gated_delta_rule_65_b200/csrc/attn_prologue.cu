@@ -22,9 +22,10 @@
 // itself: cp.async into shared memory that only it reads, several rows deep and running on into the next token, so that
 // nothing but a warp's own exchange of angles ever waits.
 //
-// Measured on one B200, back to back: that batch forward in 89 us (537 MB, 6.0 TB/s, 92% of the measured copy) and
-// backward in 138 us (805 MB, 5.8 TB/s, 89%); 17,820 new tokens of 16 packed prompts (16 + 4 + 4 heads) into the pages in
-// 42 us (219 MB, 5.2 TB/s, 80%: 7.5 tokens for a warp, so the last round is half empty).
+// Measured on one B200, back to back: 32,768 tokens of 16 + 16 bf16 heads of 128 channels forward in 89 us (537 MB,
+// 6.0 TB/s, 92% of the measured copy) and backward in 138 us (805 MB, 5.8 TB/s, 89%); 17,820 new tokens of 16 packed
+// prompts (16 + 4 + 4 heads) into the pages in 42 us (219 MB, 5.2 TB/s, 80%: 7.5 tokens for a warp, so the last round is
+// half empty). 150 MB of fp32 rows (16 + 16 heads of 128) take 53 and 77 us (86% and 90%).
 #include "attn.h"
 #include "attn_vec.cuh"
 #include "common.cuh"
