@@ -558,7 +558,10 @@ bool own_copy(const Blocks &bl, long long most, cudaStream_t st) {
     const long long page = 2LL * bl.Hk * bl.page_size * bl.row_bytes;  // below 2^43: copies_fit
     if (most > kOwnCopy / page) return false;
     cudaStreamCaptureStatus s = cudaStreamCaptureStatusNone;
-    if (cudaStreamIsCapturing(st, &s) != cudaSuccess) (void)cudaGetLastError();  // the launch will say
+    if (cudaStreamIsCapturing(st, &s) != cudaSuccess) {  // s is not set then; the launch will say what is wrong
+        (void)cudaGetLastError();
+        return true;
+    }
     return s == cudaStreamCaptureStatusNone;
 }
 
