@@ -161,3 +161,44 @@ def test_results_outlive_their_use_on_the_callers_stream():
     torch.cuda.synchronize()
     for x, y in zip(copies, want, strict=True):
         assert torch.equal(x, y)
+
+
+def test_the_threads_default_stream_by_handle():
+    """2 is the runtime's handle of the calling thread's default stream."""
+    call, _ = attention_calls()["decode"]
+    want = results(call(None))
+    torch.cuda.synchronize()
+    for _ in range(2):
+        got = call(2)
+        torch.cuda.synchronize()
+        for x, y in zip(results(got), want, strict=True):
+            assert torch.equal(x, y)
+        del got
+
+
+@pytest.mark.parametrize("name", ["bwd", "decode", "fork", "chunk_bwd"])
+def test_explicit_stream_inside_a_capture(name):
+    """A capture that forks to another stream, makes the call there and joins: fresh outputs and workspaces are the
+    graph's."""
+    call, changed = {**attention_calls(), **mixer_calls()}[name]
+    before = [t.clone() for t in changed]
+    want = [t.clone() for t in results(call(None))]
+    side = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        side.wait_stream(torch.cuda.current_stream())
+        got = results(call(side))
+        torch.cuda.current_stream().wait_stream(side)
+        twice = [t.clone() for t in got]
+    for _ in range(2):
+        for t, b in zip(changed, before):
+            t.copy_(b)
+        for t in got:
+            t.zero_()
+        trash = [torch.full((1 << n,), 0xff, dtype=torch.uint8, device="cuda") for n in range(2, 24) for _ in range(4)]
+        graph.replay()
+        torch.cuda.synchronize()
+        for x, y, z in zip(got, twice, want, strict=True):
+            assert torch.equal(x, z) and torch.equal(y, z)
+        assert all((t == 0xff).all() for t in trash)
