@@ -3,6 +3,10 @@
 Argument marshalling only: every computation happens in the library's CUDA kernels. PyTorch is used
 to hold device memory and to name the current CUDA stream. If the library cannot be loaded the
 calls raise; there is no fallback of any kind.
+
+Calls go to the current stream, or to the one given as ``stream`` (a torch stream or a cudaStream_t as an
+int). Outputs and workspaces that are not given are allocated as that stream's; inputs made on another
+stream have to be ready for it, and outputs are waited for, as with any work on two streams.
 """
 from __future__ import annotations
 
